@@ -22,7 +22,9 @@ import re
 from typing import Optional
 
 __all__ = ["fwd", "fwd_noalloc", "NOALLOC_MAX_BYTES", "bwd", "bwd_workspace_bytes", "layer_prologue", "layer_prologue_step", "layer_epilogue", "fwd_intra", "fwd_inter", "decode", "decode_kda", "fwd_kda", "fwd_kda_chunked", "kda_chunked_workspace_bytes", "chunk_wy", "workspace_bytes", "strerror", "DeltaError", "lib_path",
-           "load_library", "F32", "BF16"]
+           "load_library", "F32", "BF16", "fwd_glr", "bwd_glr", "decode_glr", "glr_workspace_bytes", "bwd_glr_workspace_bytes",
+           "layer_rmsnorm", "layer_rmsnorm_quant", "layer_rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "grad_norm",
+           "clip_grads"]
 
 F32, BF16 = 0, 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -499,3 +501,17 @@ def decode_kda(q, k, v, beta, a_log, S, *, scale: float = 1.0, O=None, stream=No
                               _dev(S, "S", torch.float32), _dev(O, "O", q.dtype), _stream(stream))
     _check(rc, "delta_decode_kda")
     return O
+
+
+_BLOCK = ("fwd_glr", "bwd_glr", "decode_glr", "glr_workspace_bytes", "bwd_glr_workspace_bytes", "layer_rmsnorm",
+          "layer_rmsnorm_quant", "layer_rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "grad_norm", "clip_grads")
+
+
+def __getattr__(name):
+    """The operators of include/delta_block.h (block.py), imported at their first use: this module
+    itself does not import torch."""
+    if name in _BLOCK:
+        from . import block
+        globals().update({n: getattr(block, n) for n in _BLOCK})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,337 @@
+"""Binding of include/delta_block.h: the gated linear recurrence, the RMS norm of the residual
+stream and gradient clipping.
+
+As the rest of the package it only marshals arguments, and it checks every tensor's shape, type
+and device before the library sees a pointer.  Work goes to the device the tensors are on,
+whichever is current: to that device's current stream, or to `stream`.  Outputs and workspaces
+that the caller does not pass are allocated on the stream that the work runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import BF16, F32, _check, load_library, make_shape
+
+GLR_CHUNK = 64  # include/delta_block.h: DELTA_GLR_CHUNK
+INPUT_GATES = {"none": 0, "complement": 1, "norm": 2}
+
+_f32 = torch.float32
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_lib = None
+
+
+def _load():
+    """libdelta.so with the argument types of delta_block.h declared."""
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        P, S, I, F, Z = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        R = ctypes.c_int64
+        for name, args in {
+            "delta_fwd_glr_workspace_bytes": [S, P], "delta_fwd_glr": [S, I] + [P] * 7 + [Z, P],
+            "delta_bwd_glr_workspace_bytes": [S, P], "delta_bwd_glr": [S, I] + [P] * 9 + [Z, P],
+            "delta_decode_glr": [S, I] + [P] * 5,
+            "delta_layer_rmsnorm": [R, I, I, F] + [P] * 6,
+            "delta_layer_rmsnorm_quant": [R, I, I, F, I] + [P] * 7,
+            "delta_layer_rmsnorm_bwd_workspace_bytes": [R, I, I, P],
+            "delta_layer_rmsnorm_bwd": [R, I, I, F] + [P] * 7 + [Z, P],
+            "delta_grad_norm_workspace_bytes": [I, P, P],
+            "delta_grad_norm": [I] + [P] * 5 + [Z, P],
+            "delta_clip_grads": [I] + [P] * 3 + [F, F] + [P] * 3 + [Z, P],
+        }.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def _on(device, stream):
+    """Context in which `device` is current and `stream` (None, a torch stream or a raw handle) its
+    current stream."""
+    if stream is None:
+        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
+def _raw(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _code(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return code
+
+
+def _arg(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of this shape, type and device (None: NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError("%s must be a GPU tensor on %s" % (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _workspace(given, need, device):
+    """(pointer, bytes, tensor to keep alive) of a workspace of at least `need` bytes."""
+    if given is None:
+        if need == 0:
+            return None, 0, None
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not isinstance(given, torch.Tensor) or given.device != device or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor on %s" % device)
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _gate(name):
+    try:
+        return INPUT_GATES[name]
+    except (KeyError, TypeError):
+        raise ValueError("input_gate must be one of %s, got %r" % (", ".join(INPUT_GATES), name)) from None
+
+
+def _glr_shape(x):
+    code = _code(x, "x")
+    if x.dim() != 4:
+        raise ValueError("x must be [B, L, H, dv]")
+    B, L, H, dv = x.shape
+    return B, L, H, dv, make_shape(B, L, H, 16, dv, 1, 64, code)
+
+
+def _bytes(fn, *args):
+    n = ctypes.c_size_t(0)
+    _check(getattr(_load(), fn)(*args, ctypes.byref(n)), fn)
+    return n.value
+
+
+def glr_workspace_bytes(B, L, H, dv, dtype=BF16) -> int:
+    """Workspace of fwd_glr for this shape."""
+    return _bytes("delta_fwd_glr_workspace_bytes", ctypes.byref(make_shape(B, L, H, 16, dv, 1, 64, dtype)))
+
+
+def bwd_glr_workspace_bytes(B, L, H, dv, dtype=BF16) -> int:
+    """Workspace of bwd_glr for this shape."""
+    return _bytes("delta_bwd_glr_workspace_bytes", ctypes.byref(make_shape(B, L, H, 16, dv, 1, 64, dtype)))
+
+
+def fwd_glr(x, g_log, h0=None, *, input_gate: str = "none", O=None, h_final=None, states=None,
+            want_state: bool = True, want_states: bool = False, workspace=None, stream=None):
+    """Gated linear recurrence over a sequence (delta_fwd_glr): h_t = a_t h_{t-1} + w_t x_t per
+    channel, a = exp(g_log), w = 1 ("none"), 1 - a ("complement") or sqrt(1 - a^2) ("norm").
+    x [B,L,H,dv] (bf16 or fp32), g_log [B,L,H,dv] fp32 (-inf: hard reset), h0 [B,H,dv] fp32 or None.
+    Returns (O, h_final, states); h_final is None if want_state is False and no buffer is given,
+    states (the states before tokens 0, 64, ..., [B,ceil(L/64),H,dv] fp32, what bwd_glr takes) None
+    unless want_states or a buffer is given.  Pass h_final=h0 to update the state in place."""
+    B, L, H, dv, sh = _glr_shape(x)
+    gate, dev = _gate(input_gate), x.device
+    with _on(dev, stream):
+        if O is None:
+            O = torch.empty_like(x)
+        if h_final is None and want_state:
+            h_final = torch.empty((B, H, dv), dtype=_f32, device=dev)
+        nc = -(-L // GLR_CHUNK)
+        if states is None and want_states:
+            states = torch.empty((B, nc, H, dv), dtype=_f32, device=dev)
+        ref = ctypes.byref(sh)
+        ws, nws, keep = _workspace(workspace, _bytes("delta_fwd_glr_workspace_bytes", ref), dev)
+        rc = _load().delta_fwd_glr(ref, gate, _arg(x, "x", x.shape, x.dtype, dev), _arg(g_log, "g_log", x.shape, _f32, dev),
+                                   _arg(h0, "h0", (B, H, dv), _f32, dev), _arg(O, "O", x.shape, x.dtype, dev),
+                                   _arg(h_final, "h_final", (B, H, dv), _f32, dev),
+                                   _arg(states, "states", (B, nc, H, dv), _f32, dev), ws, nws, _raw(dev))
+    _check(rc, "delta_fwd_glr")
+    return O, h_final, states
+
+
+def bwd_glr(x, g_log, states, dO, dh_final=None, *, input_gate: str = "none", want_dh0: bool = True, grads=None,
+            workspace=None, stream=None):
+    """Backward pass of fwd_glr (delta_bwd_glr) from the same x and g_log and the states it wrote;
+    dO has x's shape and type, dh_final [B,H,dv] fp32 may be None for zero.  Returns a dict of
+    float32 gradients dx, dg_log and dh0 (None unless want_dh0); `grads` may hold preallocated
+    outputs under the same names."""
+    B, L, H, dv, sh = _glr_shape(x)
+    gate, dev = _gate(input_gate), x.device
+    g = {"dx": None, "dg_log": None, "dh0": None}
+    g.update(grads or {})
+    with _on(dev, stream):
+        for name in ("dx", "dg_log"):
+            if g[name] is None:
+                g[name] = torch.empty(x.shape, dtype=_f32, device=dev)
+        if g["dh0"] is None and want_dh0:
+            g["dh0"] = torch.empty((B, H, dv), dtype=_f32, device=dev)
+        ref = ctypes.byref(sh)
+        ws, nws, keep = _workspace(workspace, _bytes("delta_bwd_glr_workspace_bytes", ref), dev)
+        rc = _load().delta_bwd_glr(ref, gate, _arg(x, "x", x.shape, x.dtype, dev), _arg(g_log, "g_log", x.shape, _f32, dev),
+                                   _arg(states, "states", (B, -(-L // GLR_CHUNK), H, dv), _f32, dev),
+                                   _arg(dO, "dO", x.shape, x.dtype, dev), _arg(dh_final, "dh_final", (B, H, dv), _f32, dev),
+                                   _arg(g["dx"], "dx", x.shape, _f32, dev), _arg(g["dg_log"], "dg_log", x.shape, _f32, dev),
+                                   _arg(g["dh0"], "dh0", (B, H, dv), _f32, dev), ws, nws, _raw(dev))
+    _check(rc, "delta_bwd_glr")
+    return g
+
+
+def decode_glr(x, g_log, h, *, input_gate: str = "none", O=None, stream=None):
+    """One token of the gated linear recurrence (delta_decode_glr): x [B,1,H,dv], g_log [B,1,H,dv]
+    fp32, h [B,H,dv] fp32 updated in place.  Returns O [B,1,H,dv]."""
+    B, L, H, dv, sh = _glr_shape(x)
+    if L != 1:
+        raise ValueError("decode_glr takes one token: x must be [B, 1, H, dv]")
+    gate, dev = _gate(input_gate), x.device
+    with _on(dev, stream):
+        if O is None:
+            O = torch.empty_like(x)
+        rc = _load().delta_decode_glr(ctypes.byref(sh), gate, _arg(x, "x", x.shape, x.dtype, dev),
+                                      _arg(g_log, "g_log", x.shape, _f32, dev), _arg(h, "h", (B, H, dv), _f32, dev),
+                                      _arg(O, "O", x.shape, x.dtype, dev), _raw(dev))
+    _check(rc, "delta_decode_glr")
+    return O
+
+
+def _rows(x, name):
+    code = _code(x, name)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("%s must be [..., width]" % name)
+    width = x.shape[-1]
+    return x.numel() // width, width, code
+
+
+def layer_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, sum=None, y=None, stream=None):
+    """s = x + residual (rounded to x's type) and y = s / sqrt(mean(s^2) + eps) * weight over the last
+    dimension (delta_layer_rmsnorm); weight [width] fp32.  Returns (s, y); without a residual s is x
+    itself.  Pass sum=residual to update the residual stream in place."""
+    rows, width, code = _rows(x, "x")
+    dev, shp = x.device, x.shape
+    with _on(dev, stream):
+        if residual is not None and sum is None:
+            sum = torch.empty_like(x)
+        if y is None:
+            y = torch.empty_like(x)
+        rc = _load().delta_layer_rmsnorm(rows, width, code, eps, _arg(x, "x", shp, x.dtype, dev),
+                                         _arg(residual, "residual", shp, x.dtype, dev),
+                                         _arg(weight, "weight", (width,), _f32, dev), _arg(sum, "sum", shp, x.dtype, dev),
+                                         _arg(y, "y", shp, x.dtype, dev), _raw(dev))
+    _check(rc, "delta_layer_rmsnorm")
+    return (x if residual is None else sum), y
+
+
+def layer_rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, group: int = 128, sum=None, y8=None, scale=None,
+                        stream=None):
+    """layer_rmsnorm with its output in 8 bits (delta_layer_rmsnorm_quant): y ~ y8 * scale, y8 in
+    torch.float8_e4m3fn, scale [..., ceil(width/group)] fp32 per `group` channels (128, or 0 for one
+    per row: [..., 1]).  Returns (s, y8, scale)."""
+    rows, width, code = _rows(x, "x")
+    dev, shp = x.device, x.shape
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (one scale per row) or 128, got %r" % (group,))
+    sshp = shp[:-1] + (-(-width // group) if group else 1,)
+    with _on(dev, stream):
+        if residual is not None and sum is None:
+            sum = torch.empty_like(x)
+        if y8 is None:
+            y8 = torch.empty(shp, dtype=torch.float8_e4m3fn, device=dev)
+        if scale is None:
+            scale = torch.empty(sshp, dtype=_f32, device=dev)
+        rc = _load().delta_layer_rmsnorm_quant(
+            rows, width, code, eps, group, _arg(x, "x", shp, x.dtype, dev), _arg(residual, "residual", shp, x.dtype, dev),
+            _arg(weight, "weight", (width,), _f32, dev), _arg(sum, "sum", shp, x.dtype, dev),
+            _arg(y8, "y8", shp, torch.float8_e4m3fn, dev), _arg(scale, "scale", sshp, _f32, dev), _raw(dev))
+    _check(rc, "delta_layer_rmsnorm_quant")
+    return (x if residual is None else sum), y8, scale
+
+
+def rmsnorm_bwd_workspace_bytes(rows, width, dtype=BF16) -> int:
+    """Workspace of layer_rmsnorm_bwd for this shape."""
+    return _bytes("delta_layer_rmsnorm_bwd_workspace_bytes", rows, width, dtype)
+
+
+def layer_rmsnorm_bwd(dy, s, weight, dsum=None, *, eps: float = 1e-6, want_dweight: bool = True, dx=None, dweight=None,
+                      workspace=None, stream=None):
+    """Backward pass of layer_rmsnorm (delta_layer_rmsnorm_bwd) from its s; dsum is the gradient that
+    reaches s past the norm (None for zero).  Returns (dx, dweight): dx, in s's type, is the gradient
+    of x and of residual alike; dweight [width] fp32 is None unless want_dweight."""
+    rows, width, code = _rows(s, "s")
+    dev, shp = s.device, s.shape
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty_like(s)
+        if dweight is None and want_dweight:
+            dweight = torch.empty(width, dtype=_f32, device=dev)
+        ws, nws, keep = _workspace(workspace, _bytes("delta_layer_rmsnorm_bwd_workspace_bytes", rows, width, code), dev)
+        rc = _load().delta_layer_rmsnorm_bwd(
+            rows, width, code, eps, _arg(dy, "dy", shp, s.dtype, dev), _arg(s, "s", shp, s.dtype, dev),
+            _arg(weight, "weight", (width,), _f32, dev), _arg(dsum, "dsum", shp, s.dtype, dev),
+            _arg(dx, "dx", shp, s.dtype, dev), _arg(dweight, "dweight", (width,), _f32, dev), ws, nws, _raw(dev))
+    _check(rc, "delta_layer_rmsnorm_bwd")
+    return dx, dweight
+
+
+def _tensors(grads, what="gradient"):
+    """The tensors of a sequence or dict, Nones left out."""
+    return [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
+
+
+def _grad_table(ts, device):
+    n = len(ts)
+    ptrs, sizes, dtypes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    for i, t in enumerate(ts):
+        dtypes[i] = _code(t, "gradient %d" % i)
+        if t.device != device or not t.is_contiguous():
+            raise ValueError("gradient %d must be a contiguous tensor on %s" % (i, device))
+        ptrs[i], sizes[i] = t.data_ptr(), t.numel()
+    return ptrs, sizes, dtypes
+
+
+def _norm_or_clip(grads, clip, max_norm, eps, out, norm, workspace, stream):
+    ts = _tensors(grads)
+    if not ts:
+        raise ValueError("no gradients given")
+    _code(ts[0], "gradient 0")
+    dev = ts[0].device
+    ptrs, sizes, dtypes = _grad_table(ts, dev)
+    outs = None
+    if out is not None:
+        os_ = _tensors(out)
+        if len(os_) != len(ts) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(os_, ts)):
+            raise ValueError("out must match the gradients one by one in shape and type")
+        outs = _grad_table(os_, dev)[0]
+    lib, n = _load(), len(ts)
+    with _on(dev, stream):
+        if norm is None:
+            norm = torch.empty((), dtype=_f32, device=dev)
+        pn = _arg(norm, "norm", torch.Size(()), _f32, dev)
+        ws, nws, keep = _workspace(workspace, _bytes("delta_grad_norm_workspace_bytes", n, sizes), dev)
+        if clip:
+            rc = lib.delta_clip_grads(n, ptrs, sizes, dtypes, max_norm, eps, outs, pn, ws, nws, _raw(dev))
+        else:
+            rc = lib.delta_grad_norm(n, ptrs, sizes, dtypes, pn, ws, nws, _raw(dev))
+    _check(rc, "delta_clip_grads" if clip else "delta_grad_norm")
+    return norm
+
+
+def grad_norm(grads, *, norm=None, workspace=None, stream=None):
+    """Global 2-norm of a sequence or dict of gradients (bf16 or fp32, Nones left out), as a float32
+    scalar on the device (delta_grad_norm)."""
+    return _norm_or_clip(grads, False, 0.0, 0.0, None, norm, workspace, stream)
+
+
+def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm=None, workspace=None, stream=None):
+    """Scales gradients by min(1, max_norm / (norm + eps)), norm their global 2-norm
+    (delta_clip_grads): in place, or into `out` (tensors like the gradients).  Returns the norm before
+    clipping, a float32 scalar on the device."""
+    return _norm_or_clip(grads, True, float(max_norm), float(eps), out, norm, workspace, stream)

@@ -3,12 +3,12 @@
 // never allocates device memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include <vector>
 
 #include "../../include/delta.h"
+#include "abi_common.h"
 #include "kernels.h"
 
 using delta::BwdParams;
@@ -18,35 +18,7 @@ using delta::LayerParams;
 
 namespace {
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned(const void* p, unsigned a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool aligned16(const void* p) { return aligned(p, 16); }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-size_t esize(int dtype) { return dtype == DELTA_BF16 ? 2 : 4; }
-
-// Shape checks common to all entry points.
-int check_shape(const delta_shape* s) {
-  if (!s) return DELTA_ERR_NULL_ARG;
-  if (s->B < 0 || s->L < 0 || s->H < 0 || s->n_h < 1) return DELTA_ERR_BAD_SHAPE;
-  if (s->dtype != DELTA_F32 && s->dtype != DELTA_BF16) return DELTA_ERR_UNSUPPORTED_DIM;
-  if (s->dk != 16 && s->dk != 32 && s->dk != 64 && s->dk != 128) return DELTA_ERR_UNSUPPORTED_DIM;
-  if (s->dv < 16 || s->dv > 256 || s->dv % 16 != 0) return DELTA_ERR_UNSUPPORTED_DIM;
-  // grid sizes and 64-bit element counts stay well inside what the kernels index
-  const long long Lx = (long long)s->L * s->n_h;
-  if (Lx > (1LL << 31) || (long long)s->B * s->H > (1LL << 24)) return DELTA_ERR_BAD_SHAPE;
-  return DELTA_OK;
-}
+using namespace delta::abi;
 
 int check_chunk(const delta_shape* s) {
   if (s->chunk != 16 && s->chunk != 32 && s->chunk != 48 && s->chunk != 64) return DELTA_ERR_UNSUPPORTED_DIM;
@@ -88,21 +60,6 @@ size_t gc_bytes(const FwdParams& p) { return (size_t)p.B * p.H * p.NT * p.C * 4;
 // segment summaries and start states (only with a sequence split)
 size_t sm_bytes(const FwdParams& p) { return p.P > 1 ? (size_t)p.B * p.H * p.P * p.DK * (p.DV + p.DK) * 4 : 0; }
 size_t sst_bytes(const FwdParams& p) { return p.P > 1 ? (size_t)p.B * p.H * p.P * p.DK * p.DV * 4 : 0; }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? DELTA_OK : DELTA_ERR_HIP; }
-
-// Opt-in switches, read from the environment at every call:
-//   DELTA_VALIDATE=1    check beta and the log gates before enqueuing work (validate.hip); a
-//                       value outside the contract returns DELTA_ERR_BAD_VALUE with nothing
-//                       written.  The check waits for the stream, so the call is synchronous.
-//   DELTA_FAULT=launch  every entry point that has work to enqueue fails as if its first launch
-//                       had failed: DELTA_ERR_HIP, nothing enqueued (for testing error paths).
-bool env_is(const char* name, const char* value) {
-  const char* e = getenv(name);
-  return e && strcmp(e, value) == 0;
-}
-bool validate_on() { return env_is("DELTA_VALIDATE", "1"); }
-int launch_guard() { return env_is("DELTA_FAULT", "launch") ? DELTA_ERR_HIP : DELTA_OK; }
 
 // The validation pass on the device: the flag words go to `flags` (VALIDATE_BLOCKS words of the
 // caller's workspace, overwritten afterwards by the pass itself), then are read back.
@@ -801,7 +758,7 @@ const char* delta_strerror(int code) {
       return "unsupported dimension (dk in {16,32,64,128}, dv a multiple of 16 in [16,256], chunk in "
              "{16,32,48,64}, dtype f32 or bf16)";
     case DELTA_ERR_MISALIGNED: return "a tensor pointer is misaligned (16 bytes; 4 for beta and g_log)";
-    case DELTA_ERR_WORKSPACE: return "workspace missing or smaller than delta_fwd_workspace_bytes";
+    case DELTA_ERR_WORKSPACE: return "workspace missing or smaller than the entry point's workspace size";
     case DELTA_ERR_ALIAS: return "an output overlaps an input or another output";
     case DELTA_ERR_HIP: return "HIP launch or runtime error";
     case DELTA_ERR_NOALLOC_TOO_LARGE:

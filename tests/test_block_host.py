@@ -1,0 +1,221 @@
+"""Host-side checks of include/delta_block.h and its binding (no GPU needed): exports, refusals with
+their documented codes before any launch, workspace sizes, the environment switches."""
+import ctypes
+import os
+
+import pytest
+
+import chunkwise_delta_rule_chunked_amd as D
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "delta_block.h")
+A = 1 << 24   # fake, never-dereferenced device addresses, this far apart
+EPS = ctypes.c_float(1e-6)
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(D.lib_path()):
+        pytest.fail("libdelta.so is not built (run `python -m chunkwise_delta_rule_chunked_amd.build`)")
+    from chunkwise_delta_rule_chunked_amd import block
+    return block._load()
+
+
+@pytest.fixture
+def no_gpu():
+    # a guard against a validation slip that reaches a launch with a fake address
+    if torch.cuda.is_available():
+        pytest.skip("fake-pointer argument checks run on hosts without a GPU")
+
+
+def fake(i, off=0):
+    return ctypes.c_void_p(A * (i + 1) + off)
+
+
+def shape(**kw):
+    base = dict(B=2, L=100, H=3, dk=64, dv=32, n_h=1, chunk=64, dtype=D.BF16, scale=1.0)
+    base.update(kw)
+    return D.make_shape(**base)
+
+
+def size(fn, *args):
+    n = ctypes.c_size_t(12345)
+    rc = getattr(D.load_library(), fn)(*args, ctypes.byref(n))
+    return rc, n.value
+
+
+def test_exports_every_header_function(lib):
+    names = D.header_functions(HEADER)
+    assert set(names) == {"delta_fwd_glr_workspace_bytes", "delta_fwd_glr", "delta_bwd_glr_workspace_bytes",
+                          "delta_bwd_glr", "delta_decode_glr", "delta_layer_rmsnorm", "delta_layer_rmsnorm_quant",
+                          "delta_layer_rmsnorm_bwd_workspace_bytes", "delta_layer_rmsnorm_bwd",
+                          "delta_grad_norm_workspace_bytes", "delta_grad_norm", "delta_clip_grads"}
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def test_every_public_name_resolves():
+    for n in D.__all__:
+        assert getattr(D, n) is not None
+    with pytest.raises(AttributeError):
+        D.no_such_name
+
+
+def call_fwd(sh, gate=0, **kw):
+    names = ["x", "g", "h0", "O", "hf", "st", "w"]
+    defaults = {"x": 0, "g": 1, "O": 2, "w": 3}
+    args = [kw[n] if n in kw else (fake(defaults[n]) if n in defaults else None) for n in names]
+    return D.load_library().delta_fwd_glr(ctypes.byref(sh), gate, *args, kw.get("wbytes", 1 << 20), None)
+
+
+def call_bwd(sh, gate=0, **kw):
+    names = ["x", "g", "st", "dO", "dhf", "dx", "dg", "dh0", "w"]
+    defaults = {"x": 0, "g": 1, "st": 2, "dO": 3, "dx": 4, "dg": 5, "w": 6}
+    args = [kw[n] if n in kw else (fake(defaults[n]) if n in defaults else None) for n in names]
+    return D.load_library().delta_bwd_glr(ctypes.byref(sh), gate, *args, kw.get("wbytes", 1 << 20), None)
+
+
+def test_glr_fwd_refusals(lib, no_gpu):
+    sh = shape()
+    assert call_fwd(sh, x=None) == -1 and call_fwd(sh, g=None) == -1 and call_fwd(sh, O=None) == -1
+    assert call_fwd(sh, gate=3) == -3 and call_fwd(sh, gate=-1) == -3
+    assert call_fwd(shape(n_h=2)) == -2 and call_fwd(shape(L=-1)) == -2 and call_fwd(shape(dv=40)) == -3
+    assert call_fwd(shape(dtype=5)) == -3 and call_fwd(shape(B=1, H=1 << 20)) == -2      # 2^25 channels
+    assert call_fwd(sh, x=fake(0, 8)) == -4 and call_fwd(sh, hf=fake(8, 4)) == -4 and call_fwd(sh, w=fake(3, 4)) == -4
+    assert call_fwd(sh, O=fake(0)) == -6                                          # O over x
+    assert call_fwd(sh, h0=fake(9), hf=fake(9, 256)) == -6                        # partial overlap with h0
+    assert call_fwd(sh, h0=fake(9), hf=fake(9), O=fake(1)) == -6                  # in place is let through to the next check
+    assert call_fwd(sh, st=fake(2)) == -6                                         # states over O
+    assert D.load_library().delta_fwd_glr(None, 0, *[None] * 7, 0, None) == -1
+
+
+def test_glr_ignores_dk_and_chunk(lib):
+    for kw in (dict(dk=7), dict(chunk=5), dict(scale=9.0)):
+        assert size("delta_fwd_glr_workspace_bytes", ctypes.byref(shape(**kw))) == size(
+            "delta_fwd_glr_workspace_bytes", ctypes.byref(shape()))
+
+
+def test_glr_workspace(lib, no_gpu):
+    for f, call in (("delta_fwd_glr_workspace_bytes", call_fwd), ("delta_bwd_glr_workspace_bytes", call_bwd)):
+        assert size(f, ctypes.byref(shape(L=0))) == (0, 0)
+        assert size(f, ctypes.byref(shape(dv=8)))[0] == -3
+        assert getattr(lib, f)(ctypes.byref(shape()), None) == -1
+        sh = shape(B=1, L=70000, H=2, dv=128)
+        rc, need = size(f, ctypes.byref(sh))
+        assert rc == 0
+        if need:
+            assert call(sh, w=None) == -5 and call(sh, wbytes=need - 1) == -5 and call(sh, w=fake(0)) == -6
+
+
+def test_glr_bwd_refusals(lib, no_gpu):
+    sh = shape()
+    for n in ("x", "g", "st", "dO", "dx", "dg"):
+        assert call_bwd(sh, **{n: None}) == -1, n
+    assert call_bwd(sh, gate=7) == -3 and call_bwd(shape(n_h=4)) == -2
+    assert call_bwd(sh, dx=fake(4, 8)) == -4 and call_bwd(sh, dhf=fake(8, 2)) == -4
+    assert call_bwd(sh, dx=fake(0)) == -6 and call_bwd(sh, dg=fake(4)) == -6
+    assert call_bwd(sh, dhf=fake(8), dh0=fake(8)) == -6
+
+
+def test_glr_decode_refusals(lib, no_gpu):
+    f = [fake(i) for i in range(4)]
+    L, sh = D.load_library(), shape(L=1)
+    assert L.delta_decode_glr(ctypes.byref(shape(L=2)), 0, *f, None) == -2
+    assert L.delta_decode_glr(ctypes.byref(sh), 4, *f, None) == -3
+    for i in range(4):
+        assert L.delta_decode_glr(ctypes.byref(sh), 0, *[None if j == i else p for j, p in enumerate(f)], None) == -1
+    assert L.delta_decode_glr(ctypes.byref(sh), 0, f[0], f[1], f[1], f[3], None) == -6
+    assert L.delta_decode_glr(ctypes.byref(sh), 0, f[0], f[1], fake(2, 4), f[3], None) == -4
+    assert L.delta_decode_glr(ctypes.byref(shape(B=0, L=1)), 0, *[None] * 4, None) == 0
+
+
+def test_rmsnorm_refusals(lib, no_gpu):
+    L, f = D.load_library(), [fake(i) for i in range(6)]
+    ok = dict(rows=4, width=100, dtype=D.BF16, eps=EPS, x=f[0], r=f[1], w=f[2], s=f[3], y=f[4])
+    call = lambda **kw: L.delta_layer_rmsnorm(*[{**ok, **kw}[k] for k in ok], None)
+    assert call(rows=-1) == -2 and call(width=0) == -2 and call(width=(1 << 20) + 1) == -2 and call(rows=1 << 31) == -2
+    assert call(dtype=2) == -3 and call(eps=ctypes.c_float(-1)) == -2 and call(eps=ctypes.c_float(float("nan"))) == -2
+    assert call(x=None) == -1 and call(w=None) == -1 and call(s=None) == -1 and call(y=None) == -1
+    assert call(x=fake(0, 2)) == -4
+    assert call(y=f[0]) == -6 and call(y=f[3]) == -6 and call(s=fake(0, 16)) == -6 and call(s=f[2]) == -6
+    assert call(rows=0, x=None, w=None, s=None, y=None) == 0
+    okq = dict(rows=4, width=100, dtype=D.BF16, eps=EPS, group=128, x=f[0], r=f[1], w=f[2], s=f[3], y8=f[4], sc=f[5])
+    callq = lambda **kw: L.delta_layer_rmsnorm_quant(*[{**okq, **kw}[k] for k in okq], None)
+    assert callq(group=64) == -3 and callq(y8=None) == -1 and callq(sc=None) == -1
+    assert callq(sc=fake(5, 2)) == -4 and callq(sc=f[4]) == -6 and callq(y8=f[0]) == -6
+
+
+def test_rmsnorm_bwd_refusals(lib, no_gpu):
+    L, f = D.load_library(), [fake(i) for i in range(7)]
+    rc, need = size("delta_layer_rmsnorm_bwd_workspace_bytes", 4, 100, D.BF16)
+    assert rc == 0 and need >= 4 * 100 * 4
+    ok = dict(rows=4, width=100, dtype=D.BF16, eps=EPS, dy=f[0], s=f[1], w=f[2], ds=f[3], dx=f[4], dw=f[5], ws=f[6],
+              n=ctypes.c_size_t(need))
+    call = lambda **kw: L.delta_layer_rmsnorm_bwd(*[{**ok, **kw}[k] for k in ok], None)
+    for n in ("dy", "s", "w", "dx"):
+        assert call(**{n: None}) == -1, n
+    assert call(ws=None) == -5 and call(n=ctypes.c_size_t(need - 1)) == -5
+    assert call(dx=f[0]) == -6 and call(dx=f[3]) == -6 and call(dw=f[2]) == -6 and call(ws=f[5]) == -6
+    assert call(dy=fake(0, 4)) == -4
+    assert size("delta_layer_rmsnorm_bwd_workspace_bytes", 0, 100, D.BF16) == (0, 0)
+    assert size("delta_layer_rmsnorm_bwd_workspace_bytes", 4, 100, 9)[0] == -3
+
+
+def table(sizes, dtypes=None, at=None):
+    n = len(sizes)
+    ptrs = (ctypes.c_void_p * n)(*[(A * (i + 1) if at is None else at[i]) for i in range(n)])
+    return n, ptrs, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*(dtypes or [D.F32] * n))
+
+
+def call_clip(sizes, dtypes=None, at=None, out=None, max_norm=1.0, eps=1e-6, norm=fake(100), ws=fake(101), nws=1 << 20):
+    n, p, s, d = table(sizes, dtypes, at)
+    o = None if out is None else (ctypes.c_void_p * n)(*out)
+    return D.load_library().delta_clip_grads(n, p, s, d, max_norm, eps, o, norm, ws, nws, None)
+
+
+def test_clip_refusals(lib, no_gpu):
+    assert call_clip([10, -1]) == -2 and call_clip([10], [7]) == -3
+    assert call_clip([10], max_norm=-1.0) == -2 and call_clip([10], eps=float("nan")) == -2
+    assert call_clip([10], at=[None]) == -1 and call_clip([10], norm=None) == -1
+    assert call_clip([10], at=[A + 2]) == -4 and call_clip([10], [D.BF16], at=[A + 1]) == -4
+    assert call_clip([10], ws=None) == -5 and call_clip([10], nws=7) == -5 and call_clip([10], ws=fake(101, 8)) == -4
+    assert call_clip([10, 10], at=[A, A]) == -6                    # the same tensor twice
+    assert call_clip([10, 10], at=[A, A + 36]) == -6               # overlapping by one element
+    assert call_clip([10, 10], out=[3 * A, 3 * A + 4]) == -6       # outputs overlap
+    assert call_clip([10, 10], out=[2 * A, 3 * A]) == -6           # an output over another tensor's gradient
+    assert call_clip([10], out=[A + 4]) == -6                      # an output over part of its own gradient
+    assert call_clip([10], at=[100 * A + A]) == -6                 # norm over a gradient
+    assert call_clip([1000], at=[102 * A - 400]) == -6             # a gradient reaching into the workspace
+    n, p, s, d = table([10, 10], at=[A, A])
+    assert D.load_library().delta_grad_norm(n, p, s, d, None, fake(101), 1 << 20, None) == -1
+    rc, need = size("delta_grad_norm_workspace_bytes", n, s)
+    assert rc == 0 and need >= 2 * 8
+
+
+def test_fault_injection(lib, no_gpu, monkeypatch):
+    """Every call here passes all checks, so with the switch on it ends with DELTA_ERR_HIP."""
+    monkeypatch.setenv("DELTA_FAULT", "launch")
+    L, f = D.load_library(), [fake(i) for i in range(8)]
+    assert call_fwd(shape()) == -7 and call_bwd(shape()) == -7
+    assert call_fwd(shape(dk=7, chunk=5)) == -7                                       # not looked at
+    assert call_fwd(shape(), h0=fake(9), hf=fake(9), st=fake(10)) == -7               # in place
+    assert call_fwd(shape(L=0), x=None, g=None, O=None, hf=fake(9)) == -7             # h_final = 0
+    assert call_fwd(shape(L=0), x=None, g=None, O=None) == 0 and call_fwd(shape(H=0)) == 0
+    assert L.delta_decode_glr(ctypes.byref(shape(L=1)), 2, *f[:4], None) == -7
+    assert L.delta_layer_rmsnorm(4, 100, D.F32, EPS, f[0], f[1], f[2], f[1], f[4], None) == -7   # sum over residual
+    assert L.delta_layer_rmsnorm(4, 100, D.F32, EPS, f[0], None, f[2], f[0], f[4], None) == -7   # sum not used
+    assert L.delta_layer_rmsnorm_quant(4, 100, D.F32, EPS, 0, f[0], None, f[2], None, f[4], f[5], None) == -7
+    assert L.delta_layer_rmsnorm_bwd(4, 100, D.F32, EPS, f[0], f[1], f[2], None, f[4], f[5], f[6],
+                                     ctypes.c_size_t(1 << 20), None) == -7
+    assert call_clip([10, 0, 33]) == -7 and call_clip([10, 33], out=[A, 50 * A]) == -7
+
+
+def test_binding_refuses_before_the_library(lib):
+    x, g, h = torch.zeros(1, 4, 1, 16), torch.zeros(1, 4, 1, 16), torch.zeros(1, 1, 16)
+    for f in (lambda: D.fwd_glr(x, g), lambda: D.bwd_glr(x, g, h, x), lambda: D.decode_glr(x[:, :1], g[:, :1], h),
+              lambda: D.layer_rmsnorm(x, torch.ones(16)), lambda: D.layer_rmsnorm_quant(x, torch.ones(16)),
+              lambda: D.layer_rmsnorm_bwd(x, x, torch.ones(16)), lambda: D.clip_grads([x], 1.0),
+              lambda: D.grad_norm({"dx": x}), lambda: D.grad_norm([]), lambda: D.grad_norm([None])):
+        with pytest.raises(ValueError):
+            f()
