@@ -63,7 +63,7 @@ int glr_shape(const delta_shape* s, int32_t gate, GlrParams& p, GlrSizes& z) {
   if (s->n_h != 1) return DELTA_ERR_BAD_SHAPE;
   if (gate != DELTA_GLR_NONE && gate != DELTA_GLR_COMPLEMENT && gate != DELTA_GLR_NORM) return DELTA_ERR_UNSUPPORTED_DIM;
   const long long D = (long long)s->H * s->dv;
-  if (D > (1LL << 24) || (double)s->B * s->L * D > 0x1p60) return DELTA_ERR_BAD_SHAPE;
+  if (D > (1LL << 24) || !delta::glr_grid_fits(s->B, s->L, (int)D)) return DELTA_ERR_BAD_SHAPE;
   memset(&p, 0, sizeof(p));
   p.B = s->B, p.L = s->L, p.D = (int)D, p.gate = gate;
   const size_t n = (size_t)s->B * s->L * D;
@@ -194,7 +194,7 @@ int delta_fwd_glr_workspace_bytes(const delta_shape* s, size_t* bytes) {
   const int rc = glr_shape(s, DELTA_GLR_NONE, p, z);
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
-  *bytes = 0;
+  *bytes = delta::glr_workspace(p.B, p.L, p.D, false);
   return DELTA_OK;
 }
 
@@ -221,6 +221,7 @@ int delta_fwd_glr(const delta_shape* s, int32_t input_gate, const void* x, const
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (validate_on() && (rc = validate_gates(g_log, z.g / 4, st))) return rc;
   p.x = x, p.g = g_log, p.h0 = h0, p.O = O, p.h_final = h_final, p.states = states;
+  p.ws = workspace;
   return hip_status(delta::launch_glr_fwd(p, s->dtype == DELTA_BF16, st));
 }
 
@@ -230,7 +231,7 @@ int delta_bwd_glr_workspace_bytes(const delta_shape* s, size_t* bytes) {
   const int rc = glr_shape(s, DELTA_GLR_NONE, p, z);
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
-  *bytes = 0;
+  *bytes = delta::glr_workspace(p.B, p.L, p.D, true);
   return DELTA_OK;
 }
 
@@ -258,7 +259,7 @@ int delta_bwd_glr(const delta_shape* s, int32_t input_gate, const void* x, const
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (validate_on() && (rc = validate_gates(g_log, z.g / 4, st))) return rc;
   p.x = x, p.g = g_log, p.states = const_cast<float*>(states), p.dO = dO, p.dh_final = dh_final;
-  p.dx = dx, p.dg = dg_log, p.dh0 = dh0;
+  p.dx = dx, p.dg = dg_log, p.dh0 = dh0, p.ws = workspace;
   return hip_status(delta::launch_glr_bwd(p, s->dtype == DELTA_BF16, st));
 }
 

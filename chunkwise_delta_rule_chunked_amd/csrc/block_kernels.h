@@ -20,7 +20,10 @@ struct GlrParams {
   const float* dh_final;  // [B, D] or nullptr
   float *dx, *dg;         // [B, L, D]
   float* dh0;             // [B, D] or nullptr
+  void* ws;               // glr_workspace bytes
 };
+size_t glr_workspace(int B, int L, int D, bool backward);
+bool glr_grid_fits(int B, int L, int D);  // whether the number of tiles is one a launch takes
 hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t st);
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t st);
 hipError_t launch_glr_decode(const GlrParams& p, bool bf16, hipStream_t st);

@@ -126,7 +126,11 @@ def test_glr_defaults_and_optional_outputs(gate):
     O, h, st = D.fwd_glr(xd, gd, input_gate=gate, want_state=False)
     assert h is None and st is None
     O2, h2, st2 = D.fwd_glr(xd, gd, to_dev(np.zeros((B, H, d)), "f32"), input_gate=gate, want_states=True)
-    assert torch.equal(O, O2) and torch.equal(h2, O2[:, -1]) and torch.equal(st2[:, 1:], O2[:, 63:L - 1:64])
+    assert torch.equal(O, O2)
+    # the states and the outputs at the same tokens are two evaluations of one value, each within E of it
+    E, _ = fwd_bounds(x, g, None, gate)
+    check("h_final", h2, host(O2[:, -1]), 2 * E[:, -1] + 1e-38)
+    check("states", st2[:, 1:], host(O2[:, 63:L - 1:64]), 2 * E[:, 64:L:64] + 1e-38)
     dO = to_dev(draw(13, (B, L, H, d)), "f32")
     g1 = D.bwd_glr(xd, gd, st2, dO, input_gate=gate, want_dh0=False)
     g2 = D.bwd_glr(xd, gd, st2, dO, to_dev(np.zeros((B, H, d)), "f32"), input_gate=gate)

@@ -105,7 +105,7 @@ def test_glr_workspace(lib, no_gpu):
         rc, need = size(f, ctypes.byref(sh))
         assert rc == 0
         if need:
-            assert call(sh, w=None) == -5 and call(sh, wbytes=need - 1) == -5 and call(sh, w=fake(0)) == -6
+            assert call(sh, w=None) == -5 and call(sh, wbytes=need - 1) == -5 and call(sh, w=fake(0), wbytes=need) == -6
 
 
 def test_glr_bwd_refusals(lib, no_gpu):
