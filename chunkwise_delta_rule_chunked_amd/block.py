@@ -281,45 +281,41 @@ def layer_rmsnorm_bwd(dy, s, weight, dsum=None, *, eps: float = 1e-6, want_dweig
     return dx, dweight
 
 
-def _tensors(grads, what="gradient"):
-    """The tensors of a sequence or dict, Nones left out."""
-    return [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
-
-
-def _grad_table(ts, device):
-    n = len(ts)
-    ptrs, sizes, dtypes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    for i, t in enumerate(ts):
-        dtypes[i] = _code(t, "gradient %d" % i)
-        if t.device != device or not t.is_contiguous():
-            raise ValueError("gradient %d must be a contiguous tensor on %s" % (i, device))
-        ptrs[i], sizes[i] = t.data_ptr(), t.numel()
-    return ptrs, sizes, dtypes
+def _grad_table(grads, dev, what):
+    """Host arrays describing the tensors of a sequence or dict (Nones left out), all on device `dev` or,
+    where that is None, on the first one's."""
+    ts = [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
+    if not ts:
+        raise ValueError("no %ss given" % what)
+    if dev is None:
+        _code(ts[0], "%s 0" % what)
+        dev = ts[0].device
+    codes = [_DTYPES.get(t.dtype) for t in ts]
+    if not all([t.is_cuda and t.get_device() == dev.index and t.is_contiguous() for t in ts]):
+        raise ValueError("every %s must be a contiguous GPU tensor on %s" % (what, dev))
+    if None in codes:
+        raise TypeError("every %s must be bfloat16 or float32" % what)
+    n, sizes = len(ts), [t.numel() for t in ts]
+    return dev, n, sizes, codes, (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
 
 
 def _norm_or_clip(grads, clip, max_norm, eps, out, norm, workspace, stream):
-    ts = _tensors(grads)
-    if not ts:
-        raise ValueError("no gradients given")
-    _code(ts[0], "gradient 0")
-    dev = ts[0].device
-    ptrs, sizes, dtypes = _grad_table(ts, dev)
+    dev, n, sizes, codes, ptrs = _grad_table(grads, None, "gradient")
     outs = None
     if out is not None:
-        os_ = _tensors(out)
-        if len(os_) != len(ts) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(os_, ts)):
-            raise ValueError("out must match the gradients one by one in shape and type")
-        outs = _grad_table(os_, dev)[0]
-    lib, n = _load(), len(ts)
+        _, _, osizes, ocodes, outs = _grad_table(out, dev, "output")
+        if osizes != sizes or ocodes != codes:
+            raise ValueError("out must match the gradients one by one in size and type")
+    lib, csizes, ccodes = _load(), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*codes)
     with _on(dev, stream):
         if norm is None:
             norm = torch.empty((), dtype=_f32, device=dev)
         pn = _arg(norm, "norm", torch.Size(()), _f32, dev)
-        ws, nws, keep = _workspace(workspace, _bytes("delta_grad_norm_workspace_bytes", n, sizes), dev)
+        ws, nws, keep = _workspace(workspace, _bytes("delta_grad_norm_workspace_bytes", n, csizes), dev)
         if clip:
-            rc = lib.delta_clip_grads(n, ptrs, sizes, dtypes, max_norm, eps, outs, pn, ws, nws, _raw(dev))
+            rc = lib.delta_clip_grads(n, ptrs, csizes, ccodes, max_norm, eps, outs, pn, ws, nws, _raw(dev))
         else:
-            rc = lib.delta_grad_norm(n, ptrs, sizes, dtypes, pn, ws, nws, _raw(dev))
+            rc = lib.delta_grad_norm(n, ptrs, csizes, ccodes, pn, ws, nws, _raw(dev))
     _check(rc, "delta_clip_grads" if clip else "delta_grad_norm")
     return norm
 

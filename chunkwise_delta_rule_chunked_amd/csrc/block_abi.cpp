@@ -76,7 +76,7 @@ int glr_shape(const delta_shape* s, int32_t gate, GlrParams& p, GlrSizes& z) {
 
 struct Clip {
   int64_t pieces;
-  int parts;
+  int64_t parts;  // at most: every launch but the last takes CLIP_TENSORS tensors
 };
 
 int clip_sizes(int32_t n, const int64_t* sizes, Clip& c) {
@@ -88,7 +88,9 @@ int clip_sizes(int32_t n, const int64_t* sizes, Clip& c) {
     c.pieces += (sizes[i] + delta::CLIP_PIECE - 1) / delta::CLIP_PIECE;
     if (c.pieces > 0x7fffffff) return DELTA_ERR_BAD_SHAPE;
   }
-  c.parts = (int)std::min<int64_t>(c.pieces, delta::CLIP_PARTS);
+  int64_t m = 0;
+  for (int i = 0; i < n; ++i) m += sizes[i] > 0;
+  c.parts = std::min<int64_t>(c.pieces, (m + delta::CLIP_TENSORS - 1) / delta::CLIP_TENSORS * delta::CLIP_PARTS);
   return DELTA_OK;
 }
 
@@ -111,13 +113,6 @@ int fill_table(ClipTable& t, int i, int n, const void* const* grads, void* const
   t.first[m] = pieces;
   t.count = m;
   return i;
-}
-
-// Launches of a set of n tensors: each takes up to CLIP_TENSORS non-empty ones.
-int clip_launches(int n, const int64_t* sizes) {
-  int64_t m = 0;
-  for (int i = 0; i < n; ++i) m += sizes[i] > 0;
-  return (int)((m + delta::CLIP_TENSORS - 1) / delta::CLIP_TENSORS);
 }
 
 int run_clip(int32_t n, const void* const* grads, const int64_t* sizes, const int32_t* dtypes, bool scale,
@@ -172,15 +167,17 @@ int run_clip(int32_t n, const void* const* grads, const int64_t* sizes, const in
   for (int i = 0; i < n;) {
     i = fill_table(t, i, n, grads, out, sizes, dtypes);
     if (t.count == 0) break;
-    const int np = std::min(t.first[t.count], delta::CLIP_PARTS);
+    const int np = delta::clip_parts(t.first[t.count]);
     if ((rc = hip_status(delta::launch_grad_sums(t, sums + parts, np, st)))) return rc;
     parts += np;
   }
-  if ((rc = hip_status(delta::launch_grad_finish(sums, parts, norm, st)))) return rc;
-  for (int i = 0; scale && i < n;) {
+  if (!scale) return hip_status(delta::launch_grad_finish(sums, parts, norm, st));
+  int i = 0;
+  do {  // the first launch writes the norm, also where there is no element
     i = fill_table(t, i, n, grads, out, sizes, dtypes);
-    if ((rc = hip_status(delta::launch_grad_scale(t, norm, max_norm, eps, st)))) return rc;
-  }
+    if ((rc = hip_status(delta::launch_grad_scale(t, sums, parts, max_norm, eps, norm, st)))) return rc;
+    norm = nullptr;
+  } while (i < n);
   return DELTA_OK;
 }
 
@@ -380,7 +377,7 @@ int delta_grad_norm_workspace_bytes(int32_t n, const int64_t* sizes, size_t* byt
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
   // one float64 per workgroup of every launch over the tensors
-  *bytes = align_up((size_t)std::min<int64_t>(c.pieces, (int64_t)clip_launches(n, sizes) * delta::CLIP_PARTS) * 8);
+  *bytes = align_up((size_t)c.parts * 8);
   return DELTA_OK;
 }
 

@@ -57,10 +57,17 @@ struct ClipTable {
   int32_t count;
 };
 constexpr long CLIP_PIECE = 16384;  // elements of one piece
-constexpr int CLIP_PARTS = 1024;    // partial sums at most
-// Adds nothing to what `sums` held: writes sums[part0 .. part0 + parts)
+constexpr int CLIP_PARTS = 2048;    // workgroups of the sums at most
+// Workgroups for so many pieces: the fewest that take no more rounds over them than CLIP_PARTS would.
+inline int clip_parts(int64_t pieces) {
+  const int64_t rounds = (pieces + CLIP_PARTS - 1) / CLIP_PARTS;
+  return pieces ? (int)((pieces + rounds - 1) / rounds) : 0;
+}
+// The sums of one table's squares, sums[0 .. parts); then the norm of `parts` sums in all, alone or
+// with the scaling of one table (norm may be nullptr there)
 hipError_t launch_grad_sums(const ClipTable& t, double* sums, int parts, hipStream_t st);
 hipError_t launch_grad_finish(const double* sums, int parts, float* norm, hipStream_t st);
-hipError_t launch_grad_scale(const ClipTable& t, const float* norm, float max_norm, float eps, hipStream_t st);
+hipError_t launch_grad_scale(const ClipTable& t, const double* sums, int parts, float max_norm, float eps, float* norm,
+                             hipStream_t st);
 
 }  // namespace delta

@@ -1,8 +1,13 @@
 // Global norm of a set of gradients and their clipping by it (include/delta_block.h).
 //
-// The tensors of a launch come by value in its arguments.  Each is cut into pieces of CLIP_PIECE
-// elements; workgroup j sums the squares of pieces j, j + parts, ... in float64 and stores one
-// partial sum, so the result does not depend on the order in which workgroups run.
+// The tensors of a launch come by value in its arguments, so nothing is copied to the device first.
+// Each is cut into pieces of CLIP_PIECE elements; workgroup j sums the squares of pieces j, j + parts,
+// ... in float64 and stores one partial sum, so the result does not depend on the order in which
+// workgroups run.  Every workgroup of the scaling launch then adds up the partial sums itself (in one
+// fixed order, so all get the same norm), which saves a launch between the two.
+//
+// Bound by bytes: one read for the norm, one read and one write for the scaling.  Tensors start at any
+// element: 16-byte accesses at element alignment, as gfx950 allows.
 #include <hip/hip_runtime.h>
 
 #include "block_kernels.h"
@@ -12,6 +17,7 @@ namespace delta {
 namespace {
 
 constexpr int T = 256;
+constexpr int U = 4;  // vectors of a lane in flight
 
 __device__ inline double block_sum(double x, double* lds) {
 #pragma unroll
@@ -20,6 +26,7 @@ __device__ inline double block_sum(double x, double* lds) {
   if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = x;
   __syncthreads();
   double s = 0.;
+#pragma unroll
   for (int i = 0; i < T / WAVE; ++i) s += lds[i];
   return s;
 }
@@ -36,8 +43,51 @@ __device__ inline int tensor_of(const ClipTable& t, int piece) {
 }
 __device__ inline bool is_bf16(const ClipTable& t, int i) { return t.bf16[i / 32] >> (i % 32) & 1; }
 
-__device__ inline float load(const void* p, long i, bool b) {
-  return b ? to_float(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // at any element
+
+template <typename E>
+struct Vec {
+  static constexpr int N = 16 / sizeof(E);
+  __device__ static inline void unpack(u32x4 r, float* v) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if constexpr (sizeof(E) == 4) v[e] = __builtin_bit_cast(float, (uint32_t)r[e]);
+      else v[e] = __builtin_bit_cast(float, e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
+    }
+  }
+  __device__ static inline u32x4 pack(const float* v) {
+    E x[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = to_elem<E>(v[e]);
+    u32x4 r;
+    __builtin_memcpy(&r, x, 16);
+    return r;
+  }
+};
+
+template <typename E>
+__device__ inline double piece_sum(const E* g, long n) {
+  constexpr int N = Vec<E>::N;
+  double s[4] = {};
+  long k = (long)threadIdx.x * N;
+  for (; k + (U - 1) * T * N + N <= n; k += (long)U * T * N) {
+    u32x4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = *reinterpret_cast<const u32x4_any*>(g + k + u * T * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[N];
+      Vec<E>::unpack(r[u], v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[e % 4] = __builtin_fma((double)v[e], (double)v[e], s[e % 4]);
+    }
+  }
+  for (; k < n; k += T * N)
+    for (int e = 0; e < N && k + e < n; ++e) {
+      const double v = to_float(g[k + e]);
+      s[0] += v * v;
+    }
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 __global__ __launch_bounds__(T) void grad_sums_kernel(ClipTable t, double* sums, int parts) {
@@ -45,37 +95,63 @@ __global__ __launch_bounds__(T) void grad_sums_kernel(ClipTable t, double* sums,
   double s = 0.;
   for (int piece = blockIdx.x; piece < t.first[t.count]; piece += parts) {
     const int i = tensor_of(t, piece);
-    const long lo = (piece - t.first[i]) * CLIP_PIECE, hi = min(lo + CLIP_PIECE, (long)t.n[i]);
-    const bool b = is_bf16(t, i);
-    for (long k = lo + threadIdx.x; k < hi; k += T) {
-      const double v = load(t.g[i], k, b);
-      s += v * v;
-    }
+    const long lo = (piece - t.first[i]) * CLIP_PIECE, n = min(CLIP_PIECE, (long)t.n[i] - lo);
+    s += is_bf16(t, i) ? piece_sum(static_cast<const bf16*>(t.g[i]) + lo, n)
+                       : piece_sum(static_cast<const float*>(t.g[i]) + lo, n);
   }
   s = block_sum(s, lds);
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(T) void grad_finish_kernel(const double* sums, int parts, float* norm) {
-  __shared__ double lds[T / WAVE];
+__device__ inline float norm_of(const double* sums, int parts, double* lds) {
   double s = 0.;
   for (int i = threadIdx.x; i < parts; i += T) s += sums[i];
-  s = block_sum(s, lds);
-  if (threadIdx.x == 0) *norm = (float)sqrt(s);
+  return (float)sqrt(block_sum(s, lds));
 }
 
-__global__ __launch_bounds__(T) void grad_scale_kernel(ClipTable t, const float* norm, float max_norm, float eps) {
-  const float d = *norm + eps, r = max_norm / d;
-  const float c = r >= 1.f || d == 0.f ? 1.f : r;  // NaN stays NaN
-  const int piece = blockIdx.x, i = tensor_of(t, piece);
-  const long lo = (piece - t.first[i]) * CLIP_PIECE, hi = min(lo + CLIP_PIECE, (long)t.n[i]);
-  const bool b = is_bf16(t, i);
-  if (c == 1.f && t.g[i] == t.out[i]) return;
-  for (long k = lo + threadIdx.x; k < hi; k += T) {
-    const float v = c * load(t.g[i], k, b);
-    if (b) static_cast<bf16*>(t.out[i])[k] = to_elem<bf16>(v);
-    else static_cast<float*>(t.out[i])[k] = v;
+__global__ __launch_bounds__(T) void grad_finish_kernel(const double* sums, int parts, float* norm) {
+  __shared__ double lds[T / WAVE];
+  const float n = norm_of(sums, parts, lds);
+  if (threadIdx.x == 0) *norm = n;
+}
+
+template <typename E>
+__device__ inline void piece_scale(const E* g, E* out, long n, float c) {
+  constexpr int N = Vec<E>::N;
+  long k = (long)threadIdx.x * N;
+  for (; k + (U - 1) * T * N + N <= n; k += (long)U * T * N) {
+    u32x4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(g + k + u * T * N));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[N];
+      Vec<E>::unpack(r[u], v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] *= c;
+      __builtin_nontemporal_store(Vec<E>::pack(v), reinterpret_cast<u32x4_any*>(out + k + u * T * N));
+    }
   }
+  for (; k < n; k += T * N)
+    for (int e = 0; e < N && k + e < n; ++e) out[k + e] = to_elem<E>(c * to_float(g[k + e]));
+}
+
+__global__ __launch_bounds__(T) void grad_scale_kernel(ClipTable t, const double* sums, int parts, float max_norm,
+                                                      float eps, float* norm) {
+  __shared__ double lds[T / WAVE];
+  const float total = norm_of(sums, parts, lds);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  const float d = total + eps, r = max_norm / d;
+  const float c = r >= 1.f || d == 0.f ? 1.f : r;  // NaN stays NaN
+  // from the last piece to the first: the sums read the last ones most recently, and what of them
+  // the 256 MB cache holds need not come from memory again
+  const int piece = t.first[t.count] - 1 - (int)blockIdx.x;
+  if (piece < 0) return;
+  const int i = tensor_of(t, piece);
+  const long lo = (piece - t.first[i]) * CLIP_PIECE, n = min(CLIP_PIECE, (long)t.n[i] - lo);
+  if (c == 1.f && t.g[i] == t.out[i]) return;
+  if (is_bf16(t, i)) piece_scale(static_cast<const bf16*>(t.g[i]) + lo, static_cast<bf16*>(t.out[i]) + lo, n, c);
+  else piece_scale(static_cast<const float*>(t.g[i]) + lo, static_cast<float*>(t.out[i]) + lo, n, c);
 }
 
 }  // namespace
@@ -88,9 +164,10 @@ hipError_t launch_grad_finish(const double* sums, int parts, float* norm, hipStr
   hipLaunchKernelGGL(grad_finish_kernel, dim3(1), dim3(T), 0, st, sums, parts, norm);
   return hipGetLastError();
 }
-hipError_t launch_grad_scale(const ClipTable& t, const float* norm, float max_norm, float eps, hipStream_t st) {
-  if (t.first[t.count] == 0) return hipSuccess;
-  hipLaunchKernelGGL(grad_scale_kernel, dim3(t.first[t.count]), dim3(T), 0, st, t, norm, max_norm, eps);
+hipError_t launch_grad_scale(const ClipTable& t, const double* sums, int parts, float max_norm, float eps, float* norm,
+                             hipStream_t st) {
+  const int wgs = t.first[t.count];
+  hipLaunchKernelGGL(grad_scale_kernel, dim3(wgs > 0 ? wgs : 1), dim3(T), 0, st, t, sums, parts, max_norm, eps, norm);
   return hipGetLastError();
 }
 

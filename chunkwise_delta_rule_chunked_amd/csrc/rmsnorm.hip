@@ -1,5 +1,14 @@
 // RMS norm of the residual stream with the residual's addition, its 8-bit form and its backward
-// pass (include/delta_block.h).  One workgroup per row; sums in float32.
+// pass (include/delta_block.h).  Sums in float32.
+//
+// Bound by bytes: each input is read once and each output written once, a row staying in registers
+// between its sum and its use.  LANES lanes hold a row, J vectors of 8 channels each (lane l the
+// vectors l, l + LANES, ...): the fewest lanes that hold it with few registers, so that a wavefront
+// has whole rows to itself up to 2048 channels and no barrier stands between load and store; wider
+// rows take a workgroup.  Workgroups walk over rows, keeping the weight (and, backward, their part of
+// its gradient) in registers.  Rows that are not a multiple of 8 channels start at any element: the
+// same wide accesses at element alignment, which gfx950 allows, with the row's last vector element by
+// element.  Rows past 32768 channels (backward 16384) take a kernel that reads them twice.
 #include <hip/hip_runtime.h>
 
 #include "block_kernels.h"
@@ -8,133 +17,491 @@
 namespace delta {
 namespace {
 
-constexpr int T = 256;
+constexpr int V = 8;  // channels of a vector
 constexpr float E4M3_MAX = 448.f;
 constexpr float AMAX_MIN = 0x1p-100f;  // below it a group counts as zeros: 448 / max stays finite
 
-__device__ inline float block_sum(float x, float* lds) {
-  x = wave_sum(x);
-  __syncthreads();
-  if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = x;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < T / WAVE; ++i) s += lds[i];
-  return s;
-}
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // at any element
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-// max |v| as the bits of a non-negative float, whose order as integers puts infinity above every
-// number and NaN above infinity
-__device__ inline unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
-__device__ inline unsigned block_max(unsigned x, unsigned* lds) {
+// n of 8 channels (the rest 0); n = 8 except in a row's last vector
+template <bool NT>
+__device__ inline void load8(const bf16* p, int n, float* v) {
+  if (n >= V) {
+    const auto* q = reinterpret_cast<const u32x4_any*>(p);
+    const u32x4 r = NT ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = max(x, (unsigned)__shfl_xor((int)x, o, WAVE));
-  __syncthreads();
-  if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = x;
-  __syncthreads();
-  unsigned s = 0;
-  for (int i = 0; i < T / WAVE; ++i) s = max(s, lds[i]);
-  return s;
+    for (int e = 0; e < V; ++e) v[e] = __builtin_bit_cast(float, e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = e < n ? to_float(p[e]) : 0.f;
+  }
+}
+template <bool NT>
+__device__ inline void load8(const float* p, int n, float* v) {
+  if (n >= V) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto* q = reinterpret_cast<const floatx4_any*>(p + 4 * h);
+      const floatx4 r = NT ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * h + e] = r[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = e < n ? p[e] : 0.f;
+  }
+}
+__device__ inline void store8(bf16* p, int n, const float* v) {
+  if (n >= V) {
+    bf16 r[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) r[e] = to_elem<bf16>(v[e]);
+    u32x4 q;
+    __builtin_memcpy(&q, r, 16);
+    *reinterpret_cast<u32x4_any*>(p) = q;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < n) p[e] = to_elem<bf16>(v[e]);
+  }
+}
+__device__ inline void store8(float* p, int n, const float* v) {
+  if (n >= V) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<floatx4_any*>(p + 4 * h) = floatx4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+__device__ inline void store8_e4m3(uint8_t* p, int n, const float* v) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  if (n >= V) {
+    *reinterpret_cast<u32x2_any*>(p) = u32x2{(uint32_t)lo, (uint32_t)hi};
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < n) p[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e % 4)));
+  }
 }
 
-__device__ inline uint8_t to_e4m3(float v) {
-  return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+// |v| as the bits of a non-negative float, whose order as integers puts infinity above every number
+// and NaN above infinity
+__device__ inline unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
+
+// Reductions over the LANES lanes of a row (a power of two; past a wavefront, over the workgroup,
+// through `lds`, one slot per wavefront).  Every lane gets the same value.
+template <int LANES>
+__device__ inline float row_sum(float x, float* lds) {
+#pragma unroll
+  for (int o = (LANES < WAVE ? LANES : WAVE) / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, WAVE);
+  if constexpr (LANES > WAVE) {
+    __syncthreads();
+    if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < LANES / WAVE; ++i) x += lds[i];
+  }
+  return x;
+}
+template <int LANES>
+__device__ inline unsigned row_max(unsigned x, unsigned* lds) {
+#pragma unroll
+  for (int o = (LANES < WAVE ? LANES : WAVE) / 2; o > 0; o >>= 1) x = max(x, (unsigned)__shfl_xor((int)x, o, WAVE));
+  if constexpr (LANES > WAVE) {
+    __syncthreads();
+    if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int i = 0; i < LANES / WAVE; ++i) x = max(x, lds[i]);
+  }
+  return x;
 }
 
-template <typename E>
-__global__ __launch_bounds__(T) void rmsnorm_kernel(RmsnormParams p) {
+constexpr int threads(int lanes) { return lanes > 256 ? lanes : 256; }
+
+// QUANT: 0 y, 1 y8 with a scale per row, 2 y8 with a scale per 128 channels (16 lanes).
+template <typename E, int LANES, int J, int QUANT>
+__global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p) {
+  constexpr int T = threads(LANES), RPW = T / LANES;
+  __shared__ float lds[T / WAVE];
+  __shared__ unsigned ldu[T / WAVE];
+  const int lane = threadIdx.x % LANES;
+  float w[J][V];
+#pragma unroll
+  for (int j = 0; j < J; ++j) load8<false>(p.weight + (lane + j * LANES) * V, p.width - (lane + j * LANES) * V, w[j]);
+  // every lane of a workgroup takes the same number of steps (barriers inside)
+  for (long row0 = (long)blockIdx.x * RPW; row0 < p.rows; row0 += (long)gridDim.x * RPW) {
+    const long row = row0 + threadIdx.x / LANES;
+    const bool ok = row < p.rows;
+    const long base = row * p.width;
+    float s[J][V], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+      load8<true>(static_cast<const E*>(p.x) + base + i, n, s[j]);
+      if (p.res) {
+        float r[V];
+        load8<true>(static_cast<const E*>(p.res) + base + i, n, r);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[j][e] = to_float(to_elem<E>(s[j][e] + r[e]));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+      if (p.res) store8(static_cast<E*>(p.sum) + base + i, n, s[j]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss += s[j][e] * s[j][e];
+    }
+    const float rstd = 1.f / sqrtf(row_sum<LANES>(ss, lds) / p.width + p.eps);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[j][e] = s[j][e] * rstd * w[j][e];
+    if constexpr (QUANT == 0) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int i = (lane + j * LANES) * V;
+        store8(static_cast<E*>(p.y) + base + i, ok ? p.width - i : 0, s[j]);
+      }
+    } else {
+      unsigned m[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int n = p.width - (lane + j * LANES) * V;  // what is past the row counts for nothing
+        m[j] = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) m[j] = max(m[j], e < n ? abs_bits(s[j][e]) : 0u);
+      }
+      if constexpr (QUANT == 1) {
+#pragma unroll
+        for (int j = 1; j < J; ++j) m[0] = max(m[0], m[j]);
+        m[0] = row_max<LANES>(m[0], ldu);
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int o = (LANES < 16 ? LANES : 16) / 2; o > 0; o >>= 1) m[j] = max(m[j], (unsigned)__shfl_xor((int)m[j], o, WAVE));
+      }
+      const int groups = (p.width + p.group - 1) / p.group;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+        const float amax = __builtin_bit_cast(float, m[QUANT == 1 ? 0 : j]);
+        const bool zero = amax < AMAX_MIN;
+        const float inv = zero ? 0.f : E4M3_MAX / amax;
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[j][e] *= inv;
+        store8_e4m3(p.y8 + base + i, n, s[j]);
+        if (n > 0 && i % p.group == 0) p.scale[row * groups + i / p.group] = zero ? 0.f : amax / E4M3_MAX;
+      }
+    }
+  }
+}
+
+// Rows of any width, read again for each use.
+template <typename E, int QUANT>
+__global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
+  constexpr int T = 1024;
   __shared__ float lds[T / WAVE];
   __shared__ unsigned ldu[T / WAVE];
   const long row = blockIdx.x, base = row * p.width;
   const E* x = static_cast<const E*>(p.x) + base;
-  const E* r = p.res ? static_cast<const E*>(p.res) + base : nullptr;
-  E* sum = p.res ? static_cast<E*>(p.sum) + base : nullptr;
+  E* sum = static_cast<E*>(p.sum) + base;
   float ss = 0.f;
-  for (int i = threadIdx.x; i < p.width; i += T) {
-    float s = to_float(x[i]);
-    if (r) {
-      const E e = to_elem<E>(s + to_float(r[i]));
-      sum[i] = e;
-      s = to_float(e);
+  for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+    float s[V];
+    load8<false>(x + i, p.width - i, s);
+    if (p.res) {
+      float r[V];
+      load8<false>(static_cast<const E*>(p.res) + base + i, p.width - i, r);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] = to_float(to_elem<E>(s[e] + r[e]));
+      store8(sum + i, p.width - i, s);
     }
-    ss += s * s;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ss += s[e] * s[e];
   }
-  const float rstd = 1.f / sqrtf(block_sum(ss, lds) / p.width + p.eps);
-  const E* s = sum ? sum : x;  // what this thread itself wrote
-  if (!p.y8) {
-    E* y = static_cast<E*>(p.y) + base;
-    for (int i = threadIdx.x; i < p.width; i += T) y[i] = to_elem<E>(to_float(s[i]) * rstd * p.weight[i]);
-    return;
+  const float rstd = 1.f / sqrtf(row_sum<T>(ss, lds) / p.width + p.eps);
+  const E* s0 = p.res ? sum : x;  // what this thread itself wrote
+  auto normed = [&](int i, float* y) {
+    float w[V];
+    load8<false>(s0 + i, p.width - i, y);
+    load8<false>(p.weight + i, p.width - i, w);
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * w[e];
+  };
+  const int groups = (p.width + p.group - 1) / p.group;
+  unsigned all = 0;
+  if constexpr (QUANT == 1) {
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float y[V];
+      normed(i, y);
+#pragma unroll
+      for (int e = 0; e < V; ++e) all = max(all, i + e < p.width ? abs_bits(y[e]) : 0u);
+    }
+    all = row_max<T>(all, ldu);
   }
-  const int ng = (p.width + p.group - 1) / p.group;
-  for (int n = 0; n < ng; ++n) {
-    const int lo = n * p.group, hi = min(lo + p.group, p.width);
-    unsigned m = 0;
-    for (int i = threadIdx.x; i < p.width; i += T)
-      if (i >= lo && i < hi) m = max(m, abs_bits(to_float(s[i]) * rstd * p.weight[i]));
-    const float amax = __builtin_bit_cast(float, block_max(m, ldu));
-    const bool zero = amax < AMAX_MIN;
-    const float scale = zero ? 0.f : amax / E4M3_MAX, inv = zero ? 0.f : E4M3_MAX / amax;
-    for (int i = threadIdx.x; i < p.width; i += T)
-      if (i >= lo && i < hi) p.y8[base + i] = to_e4m3(to_float(s[i]) * rstd * p.weight[i] * inv);
-    if (threadIdx.x == 0) p.scale[row * ng + n] = scale;
+  // whole groups of 16 lanes take a step together
+  for (int i = threadIdx.x * V; i - threadIdx.x % 16 * V < p.width; i += T * V) {
+    const int n = p.width - i;
+    float y[V] = {};
+    if (n > 0) normed(i, y);
+    if constexpr (QUANT == 0) {
+      if (n > 0) store8(static_cast<E*>(p.y) + base + i, n, y);
+    } else {
+      unsigned m = all;
+      if constexpr (QUANT == 2) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = max(m, e < n ? abs_bits(y[e]) : 0u);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o, WAVE));
+      }
+      const float amax = __builtin_bit_cast(float, m);
+      const bool zero = amax < AMAX_MIN;
+      const float inv = zero ? 0.f : E4M3_MAX / amax;
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] *= inv;
+      if (n > 0) {
+        store8_e4m3(p.y8 + base + i, n, y);
+        if (i % p.group == 0) p.scale[row * groups + i / p.group] = zero ? 0.f : amax / E4M3_MAX;
+      }
+    }
   }
 }
 
-// Workgroup j takes rows j, j + parts, ...; dweight's partial sums over its rows go to part[j].
-template <typename E>
-__global__ __launch_bounds__(T) void rmsnorm_bwd_kernel(RmsnormParams p, int parts) {
+// Workgroup k takes rows k RPW .., then gridDim.x * RPW further on, and stores its part of dweight in
+// part[k].  Every part is the sum over a fixed set of rows in a fixed order.
+template <typename E, int LANES, int J>
+__global__ __launch_bounds__(threads(LANES)) void rmsnorm_bwd_kernel(RmsnormParams p) {
+  constexpr int T = threads(LANES), RPW = T / LANES, COLS = LANES * J * V;
   __shared__ float lds[T / WAVE];
-  if (p.dweight)
-    for (int i = threadIdx.x; i < p.width; i += T) p.part[(long)blockIdx.x * p.width + i] = 0.f;
-  for (long row = blockIdx.x; row < p.rows; row += parts) {
+  const int lane = threadIdx.x % LANES;
+  float w[J][V], acc[J][V];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    load8<false>(p.weight + (lane + j * LANES) * V, p.width - (lane + j * LANES) * V, w[j]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
+  }
+  for (long row0 = (long)blockIdx.x * RPW; row0 < p.rows; row0 += (long)gridDim.x * RPW) {
+    const long row = row0 + threadIdx.x / LANES;
+    const bool ok = row < p.rows;
     const long base = row * p.width;
-    const E* s = static_cast<const E*>(p.x) + base;
-    const E* dy = static_cast<const E*>(p.dy) + base;
-    const E* ds = p.dsum ? static_cast<const E*>(p.dsum) + base : nullptr;
-    float ss = 0.f, dot = 0.f;
-    for (int i = threadIdx.x; i < p.width; i += T) {
-      const float v = to_float(s[i]);
-      ss += v * v;
-      dot += p.weight[i] * to_float(dy[i]) * v;
+    float s[J][V], d[J][V], o[J][V], ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+      load8<true>(static_cast<const E*>(p.x) + base + i, n, s[j]);
+      load8<true>(static_cast<const E*>(p.dy) + base + i, n, d[j]);
+      if (p.dsum) load8<true>(static_cast<const E*>(p.dsum) + base + i, n, o[j]);
+      else
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[j][e] = 0.f;
     }
-    const float rstd = 1.f / sqrtf(block_sum(ss, lds) / p.width + p.eps);
-    const float c = rstd * rstd * rstd * (block_sum(dot, lds) / p.width);
-    for (int i = threadIdx.x; i < p.width; i += T) {
-      const float v = to_float(s[i]), d = to_float(dy[i]);
-      static_cast<E*>(p.dx)[base + i] = to_elem<E>((ds ? to_float(ds[i]) : 0.f) + rstd * (p.weight[i] * d) - v * c);
-      if (p.dweight) p.part[(long)blockIdx.x * p.width + i] += d * v * rstd;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        ss += s[j][e] * s[j][e];
+        dot += w[j][e] * d[j][e] * s[j][e];
+      }
+    const float rstd = 1.f / sqrtf(row_sum<LANES>(ss, lds) / p.width + p.eps);
+    const float c = rstd * rstd * rstd * (row_sum<LANES>(dot, lds) / p.width);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        o[j][e] = o[j][e] + rstd * (w[j][e] * d[j][e]) - s[j][e] * c;
+        if (ok) acc[j][e] += d[j][e] * s[j][e] * rstd;  // a missing row's rstd is infinite for eps = 0
+      }
+      store8(static_cast<E*>(p.dx) + base + i, n, o[j]);
+    }
+  }
+  if (!p.dweight) return;
+  float* part = p.part + (long)blockIdx.x * p.width;
+  if constexpr (RPW == 1) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = (lane + j * LANES) * V;
+      store8(part + i, p.width - i, acc[j]);
+    }
+  } else {
+    // the RPW row slots add up in turn
+    __shared__ float sums[COLS];
+    for (int k = 0; k < RPW; ++k) {
+      __syncthreads();
+      if ((int)threadIdx.x / LANES == k) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            float* q = sums + (lane + j * LANES) * V + e;
+            *q = k ? *q + acc[j][e] : acc[j][e];
+          }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.width; i += T) part[i] = sums[i];
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_wide_kernel(RmsnormParams p) {
+  constexpr int T = 1024;
+  __shared__ float lds[T / WAVE];
+  float* part = p.part + (long)blockIdx.x * p.width;
+  bool first = true;
+  for (long row = blockIdx.x; row < p.rows; row += gridDim.x, first = false) {
+    const long base = row * p.width;
+    float ss = 0.f, dot = 0.f;
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float s[V], d[V], w[V];
+      load8<false>(static_cast<const E*>(p.x) + base + i, p.width - i, s);
+      load8<false>(static_cast<const E*>(p.dy) + base + i, p.width - i, d);
+      load8<false>(p.weight + i, p.width - i, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        ss += s[e] * s[e];
+        dot += w[e] * d[e] * s[e];
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<T>(ss, lds) / p.width + p.eps);
+    const float c = rstd * rstd * rstd * (row_sum<T>(dot, lds) / p.width);
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float s[V], d[V], w[V], o[V] = {}, a[V] = {};
+      load8<false>(static_cast<const E*>(p.x) + base + i, p.width - i, s);
+      load8<false>(static_cast<const E*>(p.dy) + base + i, p.width - i, d);
+      load8<false>(p.weight + i, p.width - i, w);
+      if (p.dsum) load8<false>(static_cast<const E*>(p.dsum) + base + i, p.width - i, o);
+      if (!first && p.dweight) load8<false>(part + i, p.width - i, a);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        o[e] = o[e] + rstd * (w[e] * d[e]) - s[e] * c;
+        a[e] += d[e] * s[e] * rstd;
+      }
+      store8(static_cast<E*>(p.dx) + base + i, p.width - i, o);
+      if (p.dweight) store8(part + i, p.width - i, a);
     }
   }
 }
 
-__global__ __launch_bounds__(T) void rmsnorm_dweight_kernel(const float* part, int parts, int width, float* dweight) {
-  const int i = blockIdx.x * T + threadIdx.x;
-  if (i >= width) return;
+// dweight = the sum of the parts: 16 columns and 16 lanes over the parts per workgroup.
+__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* part, int parts, int width, float* dweight) {
+  __shared__ float sums[16][17];
+  const int col = threadIdx.x % 16, k0 = threadIdx.x / 16, i = blockIdx.x * 16 + col;
   float s = 0.f;
-  for (int j = 0; j < parts; ++j) s += part[(long)j * width + i];
-  dweight[i] = s;
+  if (i < width)
+#pragma unroll 8
+    for (int k = k0; k < parts; k += 16) s += part[(long)k * width + i];
+  sums[k0][col] = s;
+  __syncthreads();
+  if (k0 == 0 && i < width) {
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += sums[k][col];
+    dweight[i] = s;
+  }
+}
+
+// Lanes and vectors per lane of a row (0: the kernels for any width).  A lane's registers hold 3 (back
+// 5) floats per channel; 1024 lanes leave 128 registers each.
+struct Split {
+  int lanes, j;
+};
+Split split(int width, bool backward) {
+  if (width <= 64) return {8, 1};
+  if (width <= 128) return {16, 1};
+  if (width <= 256) return {32, 1};
+  if (width <= 512) return {64, 1};
+  if (width <= 1024) return {64, 2};
+  if (width <= 2048) return {64, 4};
+  if (width <= 4096) return {256, 2};
+  if (width <= 8192) return {256, 4};
+  if (width <= 16384) return {1024, 2};
+  if (width <= 32768 && !backward) return {1024, 4};
+  return {0, 0};
+}
+
+// Workgroups: one step over the rows where that is no more than `most`, else `most` that walk.
+long workgroups(long rows, Split s, long most) {
+  const long per = s.lanes == 0 || s.lanes > 256 ? 1 : 256 / s.lanes;
+  const long n = (rows + per - 1) / per;
+  return n < most ? n : most;
+}
+
+template <typename E, int QUANT>
+hipError_t launch_rows(const RmsnormParams& p, hipStream_t st) {
+  const Split s = split(p.width, false);
+  if (s.lanes == 0) {
+    hipLaunchKernelGGL((rmsnorm_wide_kernel<E, QUANT>), dim3((unsigned)p.rows), dim3(1024), 0, st, p);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)workgroups(p.rows, s, s.lanes > 256 ? 512 : 2048));
+  switch (s.lanes * 16 + s.j) {
+#define DELTA_ROWS_CASE(L, J)                                                                               \
+  case L * 16 + J:                                                                                          \
+    hipLaunchKernelGGL((rmsnorm_kernel<E, L, J, QUANT>), grid, dim3(threads(L)), 0, st, p);                 \
+    break;
+#define DELTA_ROWS_CASES(M) \
+  M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(64, 2) M(64, 4) M(256, 2) M(256, 4) M(1024, 2)
+    DELTA_ROWS_CASES(DELTA_ROWS_CASE)
+    DELTA_ROWS_CASE(1024, 4)
+#undef DELTA_ROWS_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_rows_bwd(const RmsnormParams& p, hipStream_t st) {
+  const Split s = split(p.width, true);
+  const dim3 grid((unsigned)rmsnorm_bwd_parts(p.rows, p.width));
+  switch (s.lanes * 16 + s.j) {
+#define DELTA_ROWS_CASE(L, J)                                                                        \
+  case L * 16 + J:                                                                                   \
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<E, L, J>), grid, dim3(threads(L)), 0, st, p);             \
+    break;
+    DELTA_ROWS_CASES(DELTA_ROWS_CASE)
+#undef DELTA_ROWS_CASE
+#undef DELTA_ROWS_CASES
+    case 0: hipLaunchKernelGGL((rmsnorm_bwd_wide_kernel<E>), grid, dim3(1024), 0, st, p); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_quant(const RmsnormParams& p, hipStream_t st) {
+  if (!p.y8) return launch_rows<E, 0>(p, st);
+  return p.group == 128 ? launch_rows<E, 2>(p, st) : launch_rows<E, 1>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const RmsnormParams& p, bool bf16_in, hipStream_t st) {
-  const dim3 grid((unsigned)p.rows), block(T);
-  if (bf16_in) hipLaunchKernelGGL((rmsnorm_kernel<bf16>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((rmsnorm_kernel<float>), grid, block, 0, st, p);
-  return hipGetLastError();
+  return bf16_in ? launch_quant<bf16>(p, st) : launch_quant<float>(p, st);
 }
 
-int rmsnorm_bwd_parts(long rows, int) { return (int)(rows < 512 ? rows : 512); }
+int rmsnorm_bwd_parts(long rows, int width) { return (int)workgroups(rows, split(width, true), 512); }
 
 hipError_t launch_rmsnorm_bwd(const RmsnormParams& p, bool bf16_in, hipStream_t st) {
   const int parts = rmsnorm_bwd_parts(p.rows, p.width);
-  if (parts > 0) {
-    if (bf16_in) hipLaunchKernelGGL((rmsnorm_bwd_kernel<bf16>), dim3(parts), dim3(T), 0, st, p, parts);
-    else hipLaunchKernelGGL((rmsnorm_bwd_kernel<float>), dim3(parts), dim3(T), 0, st, p, parts);
-    if (const hipError_t e = hipGetLastError()) return e;
-  }
+  if (parts > 0)
+    if (const hipError_t e = bf16_in ? launch_rows_bwd<bf16>(p, st) : launch_rows_bwd<float>(p, st)) return e;
   if (!p.dweight) return hipSuccess;
-  hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((p.width + T - 1) / T), dim3(T), 0, st, p.part, parts, p.width,
+  hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((p.width + 15) / 16), dim3(256), 0, st, p.part, parts, p.width,
                      p.dweight);
   return hipGetLastError();
 }

@@ -149,7 +149,7 @@ def test_rmsnorm_refusals(lib, no_gpu):
 def test_rmsnorm_bwd_refusals(lib, no_gpu):
     L, f = D.load_library(), [fake(i) for i in range(7)]
     rc, need = size("delta_layer_rmsnorm_bwd_workspace_bytes", 4, 100, D.BF16)
-    assert rc == 0 and need >= 4 * 100 * 4
+    assert rc == 0 and need >= 100 * 4
     ok = dict(rows=4, width=100, dtype=D.BF16, eps=EPS, dy=f[0], s=f[1], w=f[2], ds=f[3], dx=f[4], dw=f[5], ws=f[6],
               n=ctypes.c_size_t(need))
     call = lambda **kw: L.delta_layer_rmsnorm_bwd(*[{**ok, **kw}[k] for k in ok], None)
