@@ -62,7 +62,8 @@ def _on(device, stream):
 
 
 def _raw(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle of torch.cuda.current_stream(device) without building the stream object (2 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _code(t, name):
@@ -78,9 +79,9 @@ def _arg(t, name, shape, dtype, device):
     """Pointer of a contiguous tensor of this shape, type and device (None: NULL)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
         raise ValueError("%s must be a GPU tensor on %s" % (name, device))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
@@ -145,10 +146,10 @@ def fwd_glr(x, g_log, h0=None, *, input_gate: str = "none", O=None, h_final=None
         if O is None:
             O = torch.empty_like(x)
         if h_final is None and want_state:
-            h_final = torch.empty((B, H, dv), dtype=_f32, device=dev)
+            h_final = x.new_empty((B, H, dv), dtype=_f32)
         nc = -(-L // GLR_CHUNK)
         if states is None and want_states:
-            states = torch.empty((B, nc, H, dv), dtype=_f32, device=dev)
+            states = x.new_empty((B, nc, H, dv), dtype=_f32)
         ref = ctypes.byref(sh)
         ws, nws, keep = _workspace(workspace, _bytes("delta_fwd_glr_workspace_bytes", ref), dev)
         rc = _load().delta_fwd_glr(ref, gate, _arg(x, "x", x.shape, x.dtype, dev), _arg(g_log, "g_log", x.shape, _f32, dev),
@@ -172,9 +173,9 @@ def bwd_glr(x, g_log, states, dO, dh_final=None, *, input_gate: str = "none", wa
     with _on(dev, stream):
         for name in ("dx", "dg_log"):
             if g[name] is None:
-                g[name] = torch.empty(x.shape, dtype=_f32, device=dev)
+                g[name] = x.new_empty(x.shape, dtype=_f32)
         if g["dh0"] is None and want_dh0:
-            g["dh0"] = torch.empty((B, H, dv), dtype=_f32, device=dev)
+            g["dh0"] = x.new_empty((B, H, dv), dtype=_f32)
         ref = ctypes.byref(sh)
         ws, nws, keep = _workspace(workspace, _bytes("delta_bwd_glr_workspace_bytes", ref), dev)
         rc = _load().delta_bwd_glr(ref, gate, _arg(x, "x", x.shape, x.dtype, dev), _arg(g_log, "g_log", x.shape, _f32, dev),
@@ -244,9 +245,9 @@ def layer_rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, group: i
         if residual is not None and sum is None:
             sum = torch.empty_like(x)
         if y8 is None:
-            y8 = torch.empty(shp, dtype=torch.float8_e4m3fn, device=dev)
+            y8 = x.new_empty(shp, dtype=torch.float8_e4m3fn)
         if scale is None:
-            scale = torch.empty(sshp, dtype=_f32, device=dev)
+            scale = x.new_empty(sshp, dtype=_f32)
         rc = _load().delta_layer_rmsnorm_quant(
             rows, width, code, eps, group, _arg(x, "x", shp, x.dtype, dev), _arg(residual, "residual", shp, x.dtype, dev),
             _arg(weight, "weight", (width,), _f32, dev), _arg(sum, "sum", shp, x.dtype, dev),
@@ -271,7 +272,7 @@ def layer_rmsnorm_bwd(dy, s, weight, dsum=None, *, eps: float = 1e-6, want_dweig
         if dx is None:
             dx = torch.empty_like(s)
         if dweight is None and want_dweight:
-            dweight = torch.empty(width, dtype=_f32, device=dev)
+            dweight = s.new_empty(width, dtype=_f32)
         ws, nws, keep = _workspace(workspace, _bytes("delta_layer_rmsnorm_bwd_workspace_bytes", rows, width, code), dev)
         rc = _load().delta_layer_rmsnorm_bwd(
             rows, width, code, eps, _arg(dy, "dy", shp, s.dtype, dev), _arg(s, "s", shp, s.dtype, dev),

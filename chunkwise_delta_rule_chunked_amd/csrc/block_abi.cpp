@@ -63,7 +63,7 @@ int glr_shape(const delta_shape* s, int32_t gate, GlrParams& p, GlrSizes& z) {
   if (s->n_h != 1) return DELTA_ERR_BAD_SHAPE;
   if (gate != DELTA_GLR_NONE && gate != DELTA_GLR_COMPLEMENT && gate != DELTA_GLR_NORM) return DELTA_ERR_UNSUPPORTED_DIM;
   const long long D = (long long)s->H * s->dv;
-  if (D > (1LL << 24) || !delta::glr_grid_fits(s->B, s->L, (int)D)) return DELTA_ERR_BAD_SHAPE;
+  if (D > (1LL << 20) || !delta::glr_grid_fits(s->B, s->L, (int)D)) return DELTA_ERR_BAD_SHAPE;
   memset(&p, 0, sizeof(p));
   p.B = s->B, p.L = s->L, p.D = (int)D, p.gate = gate;
   const size_t n = (size_t)s->B * s->L * D;

@@ -1,7 +1,7 @@
 // Gated linear recurrence: per channel h_t = a_t h_{t-1} + w_t x_t with a = exp(g), its gradients
 // and its one-token step (include/delta_block.h).
 //
-// A hard reset (g = -inf, a = 0) drops the previous state by selection rather than by
+// A hard reset (a = 0) drops the previous state by selection rather than by
 // multiplication, so that nothing of it, NaN and infinities included, is seen after it; the same
 // holds for the gradient that flows back.  State, gates and sums are float32.
 //
@@ -16,9 +16,10 @@
 //   3. each group runs its tokens again from its start state, writing outputs.
 // Tiles of one channel block and sequence form a chain.  A tile's predecessors publish their map as
 // soon as they have read their tokens and the state behind them as soon as they know it; a tile
-// starts from the nearest state it finds among its WINDOW predecessors and folds in the maps between.
+// starts from the nearest state it finds among its 64 predecessors and folds in the maps between.
 // The fold is the same left fold whichever state it starts from, so the result does not depend on
-// timing.  A published word carries its own readiness: the workspace starts as all ones, a NaN that
+// timing.  Waiting reads one flag per predecessor (a lane each, a cache line in all).  A flag is only a
+// hint: a published word carries its own readiness, since the workspace starts as all ones, a NaN that
 // no published value has, so no fence orders data and flag.  Tiles are handed out in chain order by a
 // counter: whoever a tile waits for has started before it and waits for nobody behind it, so every
 // wait ends (and is bounded besides: past POLLS polls, as can only happen if two calls share a
@@ -34,21 +35,49 @@ namespace {
 
 enum { NONE = 0, COMPLEMENT = 1, NORM = 2 };
 
-// 1 - exp(z) for z <= 0 to a few units in the last place: the difference cancels near 0, where the
-// series -z (1 + z/2 (1 + z/3 (...))) is used (|z| < 0.35: the first dropped term is below
-// 0.35^8 / 9! = 6e-10 of the result).
-__device__ inline float one_minus_exp(float z) {
-  const float series =
-      -z * (1.f + z * (1.f / 2) * (1.f + z * (1.f / 3) * (1.f + z * (1.f / 4) * (1.f + z * (1.f / 5) *
-      (1.f + z * (1.f / 6) * (1.f + z * (1.f / 7) * (1.f + z * (1.f / 8))))))));
-  return fabsf(z) < 0.35f ? series : 1.f - gate_exp(z);
-}
+__device__ inline unsigned bits(float x) { return __builtin_bit_cast(unsigned, x); }
+__device__ inline float from_bits(unsigned x) { return __builtin_bit_cast(float, x); }
 
+// a = exp(g).  a = 0 (g = -inf, or an exp that underflows) is the hard reset.  Where a product of gates
+// could underflow too, the sign bit, which no exp has (a NaN loses it here), marks a reset: products
+// carry the mark along.
+__device__ inline float factor(float g) { return fabsf(gate_exp(g)); }
+__device__ inline float mark(float a) { return a == 0.f ? -0.f : a; }
+__device__ inline bool reset(float a) { return (int)bits(a) < 0; }
+__device__ inline float times(float a, float b) {
+  return from_bits((bits(a * b) & 0x7fffffffu) | ((bits(a) | bits(b)) & 0x80000000u));
+}
+__device__ inline float step(float a, float h, float u) { return reset(a) ? u : a * h + u; }
+
+// The same for the tokens a lane holds.  RESETS: whether a reset is among the wavefront's; without one
+// (nearly always) the marks cost nothing.
+template <bool RESETS>
+struct Gates {
+  __device__ static inline float marked(float a) { return RESETS ? mark(a) : a; }
+  __device__ static inline float product(float a, float b) { return RESETS ? times(a, b) : a * b; }
+  __device__ static inline float next(float a, float h, float u) { return RESETS ? step(a, h, u) : a * h + u; }
+  // what multiplies into a gradient: nothing at a reset, whatever v is
+  __device__ static inline float pass(float a, float v) { return RESETS && reset(a) ? 0.f : v; }
+};
+
+// w(g), from a = exp(g).  1 - exp(z) cancels near z = 0, where its series to z^7 takes over (|z| < 0.35:
+// the first dropped term is below 0.35^7 / 8! = 2e-8 of the result); beyond, 1 - a or 1 - a^2 is good to
+// a dozen units of 2^-24.  For the square root z = 2 g.
 template <int GATE>
-__device__ inline float weight(float g) {
+__device__ inline float weight(float g, float a) {
   if constexpr (GATE == NONE) return 1.f;
-  if constexpr (GATE == COMPLEMENT) return one_minus_exp(g);
-  return __builtin_amdgcn_sqrtf(fmaxf(one_minus_exp(2.f * g), 0.f));
+  constexpr float K = GATE == NORM ? 2.f : 1.f;
+  float s = -K * K * K * K * K * K * K / 5040;
+  s = s * g - K * K * K * K * K * K / 720;
+  s = s * g - K * K * K * K * K / 120;
+  s = s * g - K * K * K * K / 24;
+  s = s * g - K * K * K / 6;
+  s = s * g - K * K / 2;
+  s = s * g - K;
+  s *= g;
+  const float direct = GATE == NORM ? 1.f - a * a : 1.f - a;
+  const float v = fabsf(g) < 0.35f / K ? s : direct;
+  return GATE == NORM ? __builtin_amdgcn_sqrtf(fmaxf(v, 0.f)) : v;
 }
 
 // dw/dg
@@ -58,17 +87,6 @@ __device__ inline float slope(float a, float w) {
   if constexpr (GATE == COMPLEMENT) return -a;
   return w > 0.f ? -a * a * __builtin_amdgcn_rcpf(w) : 0.f;
 }
-
-// The gate's factor, with the sign bit (which exp never sets) marking a hard reset.  Products carry
-// the mark along, so that a reset is told from a product that underflows.
-__device__ inline unsigned bits(float x) { return __builtin_bit_cast(unsigned, x); }
-__device__ inline float from_bits(unsigned x) { return __builtin_bit_cast(float, x); }
-__device__ inline bool reset(float a) { return (int)bits(a) < 0; }
-__device__ inline float gate_factor(float g) { return g == -__builtin_inff() ? -0.f : gate_exp(g); }
-__device__ inline float times(float a, float b) {
-  return from_bits((bits(a * b) & 0x7fffffffu) | ((bits(a) | bits(b)) & 0x80000000u));
-}
-__device__ inline float step(float a, float h, float u) { return reset(a) ? u : a * h + u; }
 
 // Four consecutive channels.
 __device__ inline void load4(const float* p, float* v) {
@@ -83,19 +101,33 @@ __device__ inline void load4(const bf16* p, float* v) {
 }
 
 constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
-constexpr int TPL_FWD = 16, TPL_BWD = 8;                        // tokens per lane
-constexpr int WINDOW = 8, POLLS = 1 << 22;
+#ifndef GLR_TF
+#define GLR_TF 16
+#endif
+#ifndef GLR_OF
+#define GLR_OF 2
+#endif
+#ifndef GLR_OB
+#define GLR_OB 2
+#endif
+#ifndef GLR_TB
+#define GLR_TB 8
+#endif
+constexpr int TPL_FWD = GLR_TF, TPL_BWD = GLR_TB;                        // tokens per lane
+constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
 static_assert(GLR_CHUNK % TPL_FWD == 0 && GLR_CHUNK % TPL_BWD == 0, "kept states fall between groups");
 
-// What the tiles of one call publish: per tile and channel its map and the state behind it; then
-// the counter that hands out tiles.
+// What the tiles of one call publish: per tile and channel its map and the state behind it, and per
+// tile and channel block how far it is; then the counter that hands out tiles.
 struct Chain {
-  uint64_t* map;   // [B, tiles, D]: A in the low half, H in the high one
-  uint32_t* state; // [B, tiles, D]
+  uint64_t* map;    // [B, tiles, D]: A in the low half, H in the high one
+  uint32_t* state;  // [B, tiles, D]
+  uint32_t* flag;   // [B, blocks, tiles]
   uint32_t* next;
-  int tiles;       // per sequence
+  int tiles;        // per sequence
 };
+enum : uint32_t { HAS_MAP = 1, HAS_STATE = 2 };
 
 __device__ inline unsigned plain_nan(float x) { return x != x ? (bits(x) & 0x80000000u) | 0x7fc00000u : bits(x); }
 template <typename T>
@@ -104,42 +136,56 @@ template <typename T>
 __device__ inline T look(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // The state this tile starts from, for the channel of this lane (of a whole wavefront; `live`: the
-// channel exists), publishing the tile's map and the state behind it.  at: the tile's word.
-__device__ inline float chain_state(const Chain& c, long at, long stride, int tile, bool live, float A, float H,
-                                    float init) {
+// channel exists), publishing the tile's map and the state behind it.  at: the tile's word; flag: the
+// tile's flag.
+__device__ inline float chain_state(const Chain& c, long at, long stride, uint32_t* flag, int tile, bool live, float A,
+                                    float H, float init) {
   if (c.tiles == 1) return init;
+  const int lane = threadIdx.x % WAVE;
   float h = init;
   if (tile > 0) {
     if (live) publish(c.map + at, (uint64_t)plain_nan(H) << 32 | plain_nan(A));
-    int found = -1;
-    uint64_t m[WINDOW];
-    uint32_t s[WINDOW];
-    for (int poll = 0; poll < POLLS; ++poll) {
-#pragma unroll
-      for (int k = 0; k < WINDOW; ++k) {
-        m[k] = 0, s[k] = 0;
-        if (live && k < tile) {
-          s[k] = look(c.state + at - (k + 1) * stride);
-          m[k] = look(c.map + at - (k + 1) * stride);
+    if (lane == 0) publish(flag, (uint32_t)HAS_MAP);
+    int polls = 0, found = -1;
+    for (; polls < POLLS; ++polls) {
+      const uint32_t f = lane < tile ? look(flag - 1 - lane) : 0;
+      const uint64_t states = __ballot(f == HAS_STATE), maps = __ballot(f == HAS_STATE || f == HAS_MAP);
+      if (states) {
+        const int k = __builtin_ctzll(states);
+        if ((~maps & ((1ull << k) - 1)) == 0) {
+          found = k;
+          break;
         }
       }
-      bool open = true;  // every map nearer than this one is there
-#pragma unroll
-      for (int k = 0; k < WINDOW; ++k) {
-        if (open && k < tile && found < 0 && __all(s[k] != ~0u)) found = k;
-        open = open && k < tile && __all(m[k] != ~0ull);
-      }
-      if (found >= 0) break;
       __builtin_amdgcn_s_sleep(1);
     }
-    h = __builtin_nanf("");
-#pragma unroll
-    for (int k = WINDOW - 1; k >= 0; --k) {
-      if (k == found) h = from_bits(s[k]);
-      else if (k < found) h = step(from_bits((unsigned)m[k]), h, from_bits((unsigned)(m[k] >> 32)));
+    uint32_t first = ~0u;
+    while (found >= 0 && polls < POLLS) {
+      first = live ? look(c.state + at - (found + 1) * stride) : 0;
+      if (__all(first != ~0u)) break;
+      ++polls;
     }
+    h = from_bits(first);
+    for (int k0 = found - 1; k0 >= 0; k0 -= BATCH) {
+      uint64_t m[BATCH];
+      for (; polls < POLLS; ++polls) {
+        bool there = true;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) m[i] = live && i <= k0 ? look(c.map + at - (k0 - i + 1) * stride) : 0;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) there = there && m[i] != ~0ull;
+        if (__all(there)) break;
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (i <= k0) h = step(from_bits((unsigned)m[i]), h, from_bits((unsigned)(m[i] >> 32)));
+    }
+    if (polls >= POLLS) h = __builtin_nanf("");
   }
-  if (live && tile + 1 < c.tiles) publish(c.state + at, plain_nan(step(A, h, H)));
+  if (tile + 1 < c.tiles) {
+    if (live) publish(c.state + at, plain_nan(step(A, h, H)));
+    if (lane == 0) publish(flag, (uint32_t)HAS_STATE);
+  }
   return h;
 }
 
@@ -156,44 +202,131 @@ __global__ __launch_bounds__(256) void glr_clear_kernel(u32x4* p, long n) {
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) p[i] = u32x4{~0u, ~0u, ~0u, ~0u};
 }
 
-template <typename E, int GATE>
-__global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
-  constexpr int TPL = TPL_FWD, TT = NG * TPL;
-  __shared__ float sA[NG][CC], sH[NG][CC];  // the groups' maps; then sH the groups' start states
-  const unsigned job = take_tile(chain), nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
-  const int tile = job / chains, b = job % chains / nblk, c0 = (int)(job % chains % nblk) * CC;
-  const int tid = threadIdx.x, grp = tid / LPR, c = c0 + tid % LPR * 4;
-  const int t0 = tile * TT + grp * TPL;
-  const bool here = c < p.D;
-  const long base = ((long)b * p.L + t0) * p.D + c;
-  float a[TPL][4], u[TPL][4], A[4], H[4];
+// Where a lane's tokens are: `tile` (uniform) points at the tile's first token and channel of a
+// [B, L, D] tensor, the lane's token j at element off + j D from there.  With the token's part in the
+// uniform pointer the address costs a lane nothing.  Offsets stay within 32 bits: TT * D < 2^28.
+struct Where {
+  unsigned off;   // of the lane's first token (of an existing channel)
+  int first;      // that token's place in the tile
+  int left;       // tokens of the sequence from the tile's first one on; all of the tile's or fewer
+  bool inside;    // all (uniform)
+  int stride;     // D
+};
+template <typename E>
+__device__ inline E* at_byte(E* p, unsigned off) {
+  return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) + off);
+}
+// A lane's TPL tokens; past the end 0, the identity (g = 0, x = 0).
+template <int TPL, typename E>
+__device__ inline void load_tokens(const E* tile, const Where& w, float (*v)[4]) {
+  if (w.inside) {
 #pragma unroll
-  for (int j = 0; j < TPL; ++j) {
-    // tokens past the end are the identity: g = 0 (a = 1), x = 0
+    for (int j = 0; j < TPL; ++j) load4(at_byte(tile + (long)j * w.stride, w.off * (unsigned)sizeof(E)), v[j]);
+  } else if (w.left <= 0) {  // L = 0: there is no token to read
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[j][e] = u[j][e] = 0.f;
-    if (here && t0 + j < p.L) {
-      load4(p.g + base + (long)j * p.D, a[j]);
-      load4(static_cast<const E*>(p.x) + base + (long)j * p.D, u[j]);
+    for (int j = 0; j < TPL; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[j][e] = 0.f;
+  } else {
+    const unsigned lane = w.off - (unsigned)w.first * w.stride;
+#pragma unroll
+    for (int j = 0; j < TPL; ++j) {
+      const int t = w.first + j;
+      load4(at_byte(tile, (lane + (unsigned)(t < w.left ? t : w.left - 1) * w.stride) * (unsigned)sizeof(E)), v[j]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[j][e] = t < w.left ? v[j][e] : 0.f;
     }
   }
+}
+
+// Where a workgroup's tile is.
+struct Tile {
+  int b, order, c0;      // sequence, place in its chain, first channel
+  long chain;            // b * blocks + channel block
+  bool none;             // no such tile: a counter that another call moved
+  __device__ inline Tile(const GlrParams& p, const Chain& c) {
+    const unsigned job = __builtin_amdgcn_readfirstlane(take_tile(c)), nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
+    order = job / chains;
+    none = order >= c.tiles;
+    chain = job % chains;
+    b = (unsigned)chain / nblk;
+    c0 = (int)((unsigned)chain % nblk) * CC;
+  }
+};
+
+// a <- the gates' factors; whether one of the wavefront's is 0
+template <int TPL, int GATE>
+__device__ inline bool factors(float (*a)[4], float (*w)[4]) {
+  float m = 1.f;
+#pragma unroll
+  for (int j = 0; j < TPL; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float g = a[j][e];
+      a[j][e] = factor(g);
+      m = fminf(m, a[j][e]);
+      w[j][e] = weight<GATE>(g, a[j][e]);
+    }
+  return __any(m == 0.f);
+}
+
+// The group's map.
+template <int TPL, bool RESETS>
+__device__ inline void fwd_map(float (*a)[4], const float (*u)[4], float* A, float* H) {
+  typedef Gates<RESETS> G;
 #pragma unroll
   for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = 0.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      u[j][e] *= weight<GATE>(a[j][e]);
-      a[j][e] = gate_factor(a[j][e]);
-      A[e] = times(A[e], a[j][e]);
-      H[e] = step(a[j][e], H[e], u[j][e]);
+      a[j][e] = G::marked(a[j][e]);
+      A[e] = G::product(A[e], a[j][e]);
+      H[e] = G::next(a[j][e], H[e], u[j][e]);
     }
-  const int col = tid % LPR * 4;
+}
+
+template <int TPL, bool RESETS, typename E>
+__device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4 h, E* out, const Where& w, int left) {
+#pragma unroll
+  for (int j = 0; j < TPL; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = Gates<RESETS>::next(a[j][e], h[e], u[j][e]);
+    if (j < left)
+      store4<E>(at_byte(out + (long)j * w.stride, w.off * (unsigned)sizeof(E)), h[0], h[1], h[2], h[3]);
+  }
+}
+
+template <typename E, int GATE>
+__global__ __launch_bounds__(WG, GLR_OF) void glr_fwd_kernel(GlrParams p, Chain chain) {
+  constexpr int TPL = TPL_FWD, TT = NG * TPL;
+  __shared__ float sA[NG][CC], sH[NG][CC];  // the groups' maps; then sH the groups' start states
+  const Tile tile(p, chain);
+  if (tile.none) return;
+  const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
+  const int tile0 = tile.order * TT;
+  const bool here = tile.c0 + col < p.D;
+  const Where w{(unsigned)(grp * TPL * p.D + (here ? col : 0)), grp * TPL, p.L - tile0, tile0 + TT <= p.L, p.D};
+  const long base = ((long)tile.b * p.L + tile0) * p.D + tile.c0;
+  float a[TPL][4], u[TPL][4], A[4], H[4];
+  load_tokens<TPL>(p.g + base, w, a);
+  load_tokens<TPL>(static_cast<const E*>(p.x) + base, w, u);
+  bool resets;
+  {
+    float wt[TPL][4];
+    resets = factors<TPL, GATE>(a, wt);
+#pragma unroll
+    for (int j = 0; j < TPL; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[j][e] *= wt[j][e];
+  }
+  if (resets) fwd_map<TPL, true>(a, u, A, H);
+  else fwd_map<TPL, false>(a, u, A, H);
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   __syncthreads();
   if (tid < CC) {
-    const int ch = c0 + tid;
+    const int ch = tile.c0 + tid;
     const bool live = ch < p.D;
     float TA = 1.f, TH = 0.f;
 #pragma unroll
@@ -201,84 +334,115 @@ __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
       TH = step(sA[k][tid], TH, sH[k][tid]);
       TA = times(TA, sA[k][tid]);
     }
-    float h = chain_state(chain, ((long)b * chain.tiles + tile) * p.D + ch, p.D, tile, live, TA, TH,
-                          live && p.h0 ? p.h0[(long)b * p.D + ch] : 0.f);
+    float h = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
+                          chain.flag + tile.chain * chain.tiles + tile.order, tile.order, live, TA, TH,
+                          live && p.h0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       const float next = step(sA[k][tid], h, sH[k][tid]);
       sH[k][tid] = h;
       h = next;
     }
-    if (live && p.h_final && tile == chain.tiles - 1) p.h_final[(long)b * p.D + ch] = h;
+    if (live && p.h_final && tile.order == chain.tiles - 1) p.h_final[(long)tile.b * p.D + ch] = h;
   }
   __syncthreads();
-  if (!here) return;
-  floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]);
-  if (p.states && t0 % GLR_CHUNK == 0 && t0 < p.L) {
+  const int mine = w.left - w.first;  // tokens of this lane and behind
+  if (!here || mine <= 0) return;
+  const floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]);
+  if (p.states && w.first % GLR_CHUNK == 0) {
     const int nc = (p.L + GLR_CHUNK - 1) / GLR_CHUNK;
-    *reinterpret_cast<floatx4*>(p.states + ((long)b * nc + t0 / GLR_CHUNK) * p.D + c) = h;
+    float* to = p.states + ((long)tile.b * nc + (tile0 + w.first) / GLR_CHUNK) * p.D + tile.c0 + col;
+    *reinterpret_cast<floatx4*>(to) = h;
   }
-#pragma unroll
-  for (int j = 0; j < TPL; ++j) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = step(a[j][e], h[e], u[j][e]);
-    if (t0 + j < p.L) store4<E>(static_cast<E*>(p.O) + base + (long)j * p.D, h[0], h[1], h[2], h[3]);
-  }
+  E* out = static_cast<E*>(p.O) + base;
+  const int stores = w.inside ? TPL : mine;
+  if (resets) fwd_out<TPL, true>(a, u, h, out, w, stores);
+  else fwd_out<TPL, false>(a, u, h, out, w, stores);
 }
 
 // The same from the other end.  With flow_t = a_t lambda_t, the gradient that reaches the state
 // before token t, flow_t = a_t (dO_t + flow_{t+1}): an affine recurrence over the same gates, tiles
 // handed out from the last to the first.  A group's start state comes from the kept state of its
 // 64 tokens and the maps of the groups between.
-template <typename E, int GATE>
-__global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
-  constexpr int TPL = TPL_BWD, TT = NG * TPL, GPC = GLR_CHUNK / TPL;  // groups per kept state
-  __shared__ float sA[NG][CC], sH[NG][CC], sF[NG][CC];
-  const unsigned job = take_tile(chain), nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
-  const int order = job / chains, b = job % chains / nblk, c0 = (int)(job % chains % nblk) * CC;
-  const int tid = threadIdx.x, grp = tid / LPR, c = c0 + tid % LPR * 4;
-  const int tile0 = (chain.tiles - 1 - order) * TT, t0 = tile0 + grp * TPL;
-  const bool here = c < p.D;
-  const long base = ((long)b * p.L + t0) * p.D + c;
-  float a[TPL][4], w[TPL][4], x[TPL][4], d[TPL][4], A[4], H[4], F[4];
-#pragma unroll
-  for (int j = 0; j < TPL; ++j) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[j][e] = x[j][e] = d[j][e] = 0.f;
-    if (here && t0 + j < p.L) {
-      load4(p.g + base + (long)j * p.D, a[j]);
-      load4(static_cast<const E*>(p.x) + base + (long)j * p.D, x[j]);
-      load4(static_cast<const E*>(p.dO) + base + (long)j * p.D, d[j]);
-    }
-  }
+template <int TPL, bool RESETS>
+__device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const float (*x)[4], const float (*d)[4], float* A,
+                               float* H, float* F) {
+  typedef Gates<RESETS> G;
 #pragma unroll
   for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = F[e] = 0.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[j][e] = weight<GATE>(a[j][e]);
-      a[j][e] = gate_factor(a[j][e]);
-      A[e] = times(A[e], a[j][e]);
-      H[e] = step(a[j][e], H[e], w[j][e] * x[j][e]);
+      a[j][e] = G::marked(a[j][e]);
+      A[e] = G::product(A[e], a[j][e]);
+      H[e] = G::next(a[j][e], H[e], w[j][e] * x[j][e]);
     }
 #pragma unroll
   for (int j = TPL - 1; j >= 0; --j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) F[e] = step(a[j][e], d[j][e] + F[e], 0.f);
-  const int col = tid % LPR * 4;
+    for (int e = 0; e < 4; ++e) F[e] = G::pass(a[j][e], a[j][e] * (d[j][e] + F[e]));
+}
+
+template <int TPL, int GATE, bool RESETS>
+__device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], float (*x)[4], const float (*d)[4], floatx4 h,
+                               floatx4 flow, float* dx, float* dg, const Where& at, int left) {
+  typedef Gates<RESETS> G;
+#pragma unroll
+  for (int j = 0; j < TPL; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // x becomes dh_t / dg_t
+      const float u = w[j][e] * x[j][e], ah = a[j][e] * h[e];
+      x[j][e] = G::pass(a[j][e], ah + slope<GATE>(a[j][e], w[j][e]) * x[j][e]);
+      h[e] = G::pass(a[j][e], ah) + u;
+    }
+#pragma unroll
+  for (int j = TPL - 1; j >= 0; --j) {
+    floatx4 px, pg;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lam = d[j][e] + flow[e];
+      px[e] = w[j][e] * lam;
+      pg[e] = G::pass(a[j][e], lam * x[j][e]);
+      flow[e] = G::pass(a[j][e], a[j][e] * lam);
+    }
+    if (j < left) {
+      *reinterpret_cast<floatx4*>(at_byte(dx + (long)j * at.stride, at.off * 4u)) = px;
+      *reinterpret_cast<floatx4*>(at_byte(dg + (long)j * at.stride, at.off * 4u)) = pg;
+    }
+  }
+}
+
+template <typename E, int GATE>
+__global__ __launch_bounds__(WG, GLR_OB) void glr_bwd_kernel(GlrParams p, Chain chain) {
+  constexpr int TPL = TPL_BWD, TT = NG * TPL, GPC = GLR_CHUNK / TPL;  // groups per kept state
+  __shared__ float sA[NG][CC], sH[NG][CC], sF[NG][CC];
+  const Tile tile(p, chain);
+  if (tile.none) return;
+  const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
+  const int tile0 = (chain.tiles - 1 - tile.order) * TT;
+  const bool here = tile.c0 + col < p.D;
+  const Where at{(unsigned)(grp * TPL * p.D + (here ? col : 0)), grp * TPL, p.L - tile0, tile0 + TT <= p.L, p.D};
+  const long base = ((long)tile.b * p.L + tile0) * p.D + tile.c0;
+  float a[TPL][4], w[TPL][4], x[TPL][4], d[TPL][4], A[4], H[4], F[4];
+  load_tokens<TPL>(p.g + base, at, a);
+  load_tokens<TPL>(static_cast<const E*>(p.x) + base, at, x);
+  load_tokens<TPL>(static_cast<const E*>(p.dO) + base, at, d);
+  const bool resets = factors<TPL, GATE>(a, w);
+  if (resets) bwd_map<TPL, true>(a, w, x, d, A, H, F);
+  else bwd_map<TPL, false>(a, w, x, d, A, H, F);
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   *reinterpret_cast<floatx4*>(&sF[grp][col]) = floatx4{F[0], F[1], F[2], F[3]};
   __syncthreads();
   if (tid < CC) {
-    const int ch = c0 + tid, nc = (p.L + GLR_CHUNK - 1) / GLR_CHUNK;
+    const int ch = tile.c0 + tid, nc = (p.L + GLR_CHUNK - 1) / GLR_CHUNK;
     const bool live = ch < p.D;
     float start[NG / GPC];
 #pragma unroll
     for (int n = 0; n < NG / GPC; ++n) {
       const int chunk = tile0 / GLR_CHUNK + n;
-      start[n] = live && chunk < nc ? p.states[((long)b * nc + chunk) * p.D + ch] : 0.f;
+      start[n] = live && chunk < nc ? p.states[((long)tile.b * nc + chunk) * p.D + ch] : 0.f;
     }
     float TA = 1.f, TF = 0.f;
 #pragma unroll
@@ -286,15 +450,16 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
       TF = step(sA[k][tid], TF, sF[k][tid]);
       TA = times(TA, sA[k][tid]);
     }
-    float flow = chain_state(chain, ((long)b * chain.tiles + order) * p.D + ch, p.D, order, live, TA, TF,
-                             live && p.dh_final ? p.dh_final[(long)b * p.D + ch] : 0.f);
+    float flow = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
+                             chain.flag + tile.chain * chain.tiles + tile.order, tile.order, live, TA, TF,
+                             live && p.dh_final ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = NG - 1; k >= 0; --k) {
       const float next = step(sA[k][tid], flow, sF[k][tid]);
       sF[k][tid] = flow;
       flow = next;
     }
-    if (live && p.dh0 && order == chain.tiles - 1) p.dh0[(long)b * p.D + ch] = flow;
+    if (live && p.dh0 && tile.order == chain.tiles - 1) p.dh0[(long)tile.b * p.D + ch] = flow;
 #pragma unroll
     for (int n = 0; n < NG / GPC; ++n) {
       float h = start[n];
@@ -307,39 +472,20 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
     }
   }
   __syncthreads();
-  if (!here) return;
-  floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]), flow = *reinterpret_cast<const floatx4*>(&sF[grp][col]);
-#pragma unroll
-  for (int j = 0; j < TPL; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {  // x becomes dh_t / dg_t
-      const float q = reset(a[j][e]) ? 0.f : a[j][e] * h[e] + slope<GATE>(a[j][e], w[j][e]) * x[j][e];
-      h[e] = step(a[j][e], h[e], w[j][e] * x[j][e]);
-      x[j][e] = q;
-    }
-#pragma unroll
-  for (int j = TPL - 1; j >= 0; --j) {
-    if (t0 + j < p.L) {
-      floatx4 dx, dg;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float lam = d[j][e] + flow[e];
-        dx[e] = w[j][e] * lam;
-        dg[e] = reset(a[j][e]) ? 0.f : lam * x[j][e];
-        flow[e] = step(a[j][e], lam, 0.f);
-      }
-      *reinterpret_cast<floatx4*>(p.dx + base + (long)j * p.D) = dx;
-      *reinterpret_cast<floatx4*>(p.dg + base + (long)j * p.D) = dg;
-    }
-  }
+  const int mine = at.left - at.first;
+  if (!here || mine <= 0) return;
+  const floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]), flow = *reinterpret_cast<const floatx4*>(&sF[grp][col]);
+  const int stores = at.inside ? TPL : mine;
+  if (resets) bwd_out<TPL, GATE, true>(a, w, x, d, h, flow, p.dx + base, p.dg + base, at, stores);
+  else bwd_out<TPL, GATE, false>(a, w, x, d, h, flow, p.dx + base, p.dg + base, at, stores);
 }
 
 template <typename E, int GATE>
 __global__ __launch_bounds__(256) void glr_decode_kernel(GlrParams p) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long)p.B * p.D) return;
-  const float g = p.g[i];
-  const float h = step(gate_factor(g), p.h_final[i], weight<GATE>(g) * to_float(static_cast<const E*>(p.x)[i]));
+  const float g = p.g[i], a = mark(factor(g));
+  const float h = step(a, p.h_final[i], weight<GATE>(g, a) * to_float(static_cast<const E*>(p.x)[i]));
   p.h_final[i] = h;
   static_cast<E*>(p.O)[i] = to_elem<E>(h);
 }
@@ -349,6 +495,20 @@ enum Which { FWD, BWD, DECODE };
 int tile_tokens(Which which) { return NG * (which == FWD ? TPL_FWD : TPL_BWD); }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Byte offsets of the chain's arrays in the workspace.
+struct Layout {
+  size_t state, flag, next, total;
+};
+Layout layout(int B, int tiles, int D) {
+  const size_t n = (size_t)B * tiles * D, blocks = (D + CC - 1) / CC;
+  Layout l;
+  l.state = up256(n * 8);
+  l.flag = l.state + up256(n * 4);
+  l.next = l.flag + up256((size_t)B * blocks * tiles * 4);
+  l.total = l.next + 256;
+  return l;
+}
+
 template <typename E, int GATE>
 hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
   if (which == DECODE) {
@@ -357,15 +517,15 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
     return hipGetLastError();
   }
   const int TT = tile_tokens(which);
-  Chain c{nullptr, nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1};
+  Chain c{nullptr, nullptr, nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1};
   if (c.tiles > 1) {
-    const size_t n = (size_t)p.B * c.tiles * p.D, total = up256(n * 8) + up256(n * 4) + 256;
+    const Layout l = layout(p.B, c.tiles, p.D);
     char* ws = static_cast<char*>(p.ws);
     c.map = reinterpret_cast<uint64_t*>(ws);
-    c.state = reinterpret_cast<uint32_t*>(ws + up256(n * 8));
-    c.next = reinterpret_cast<uint32_t*>(ws + total - 256);
-    const long v = (long)(total / 16);
-    const long wgs = (v + 255) / 256;
+    c.state = reinterpret_cast<uint32_t*>(ws + l.state);
+    c.flag = reinterpret_cast<uint32_t*>(ws + l.flag);
+    c.next = reinterpret_cast<uint32_t*>(ws + l.next);
+    const long v = (long)(l.total / 16), wgs = (v + 255) / 256;
     hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, st,
                        reinterpret_cast<u32x4*>(ws), v);
     if (const hipError_t e = hipGetLastError()) return e;
@@ -393,9 +553,7 @@ hipError_t launch(const GlrParams& p, bool bf16_in, Which which, hipStream_t st)
 
 size_t glr_workspace(int B, int L, int D, bool backward) {
   const int TT = tile_tokens(backward ? BWD : FWD);
-  if (L <= TT) return 0;
-  const size_t n = (size_t)B * ((L + TT - 1) / TT) * D;
-  return n ? up256(n * 8) + up256(n * 4) + 256 : 0;
+  return L > TT && B > 0 && D > 0 ? layout(B, (L + TT - 1) / TT, D).total : 0;
 }
 bool glr_grid_fits(int B, int L, int D) {
   return (double)((D + CC - 1) / CC) * B * ((L + (double)NG * TPL_BWD - 1) / (NG * TPL_BWD)) < 0x1p31;

@@ -37,10 +37,12 @@ enum {
  *     a_t = exp(g_t),   h_t = a_t h_{t-1} + w_t x_t,   o_t = h_t
  *
  * the diagonal counterpart of the delta rule's matrix state, with the same layout, log gates and
- * float32 state.  g_t <= 0 is expected (a positive value is computed as given); g_t = -inf is the
- * hard reset: h_t = w_t x_t exactly, whatever h_{t-1} holds (also infinities and NaN), so packed
- * sequences do not see each other.  Other NaN and infinite inputs propagate.
- *   s->n_h must be 1; s->dk, s->chunk and s->scale are ignored; input_gate is DELTA_GLR_*.
+ * float32 state.  g_t <= 0 is expected (a positive value is computed as given); g_t = -inf, or any
+ * g_t whose exp is 0 in float32 (below about -87), is the hard reset: h_t = w_t x_t exactly, whatever
+ * h_{t-1} holds (also infinities and NaN), so packed sequences do not see each other.  Other NaN and
+ * infinite inputs propagate.
+ *   s->n_h must be 1; s->dk, s->chunk and s->scale are ignored; input_gate is DELTA_GLR_*; at most
+ *   2^20 channels.
  *   x       [B, L, H, dv]       dtype
  *   g_log   [B, L, H, dv]       float32
  *   h0      [B, H, dv]          float32   initial state, or NULL for zeros

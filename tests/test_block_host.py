@@ -81,7 +81,7 @@ def test_glr_fwd_refusals(lib, no_gpu):
     assert call_fwd(sh, x=None) == -1 and call_fwd(sh, g=None) == -1 and call_fwd(sh, O=None) == -1
     assert call_fwd(sh, gate=3) == -3 and call_fwd(sh, gate=-1) == -3
     assert call_fwd(shape(n_h=2)) == -2 and call_fwd(shape(L=-1)) == -2 and call_fwd(shape(dv=40)) == -3
-    assert call_fwd(shape(dtype=5)) == -3 and call_fwd(shape(B=1, H=1 << 20)) == -2      # 2^25 channels
+    assert call_fwd(shape(dtype=5)) == -3 and call_fwd(shape(B=1, H=1 << 16)) == -2      # 2^21 channels
     assert call_fwd(sh, x=fake(0, 8)) == -4 and call_fwd(sh, hf=fake(8, 4)) == -4 and call_fwd(sh, w=fake(3, 4)) == -4
     assert call_fwd(sh, O=fake(0)) == -6                                          # O over x
     assert call_fwd(sh, h0=fake(9), hf=fake(9, 256)) == -6                        # partial overlap with h0
