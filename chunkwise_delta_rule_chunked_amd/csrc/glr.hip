@@ -20,8 +20,8 @@
 // The fold is the same left fold whichever state it starts from, so the result does not depend on
 // timing.  Waiting reads one flag per predecessor (a lane each, a cache line in all).  A flag is only a
 // hint: a published word carries its own readiness, since the workspace starts as all ones, a NaN that
-// no published value has, so no fence orders data and flag.  Tiles are handed out in chain order by a
-// counter: whoever a tile waits for has started before it and waits for nobody behind it, so every
+// no published value has, so no fence orders data and flag.  A counter per chain hands out its tiles in
+// order: whoever a tile waits for has started before it and waits for nobody behind it, so every
 // wait ends (and is bounded besides: past POLLS polls, as can only happen if two calls share a
 // workspace, the tile goes on with NaN).
 //
@@ -100,7 +100,13 @@ __device__ inline void load4(const bf16* p, float* v) {
   for (int e = 0; e < 4; ++e) v[e] = to_float(r[e]);
 }
 
-constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
+#ifndef GLR_WG
+#define GLR_WG 256
+#endif
+#ifndef GLR_LPR
+#define GLR_LPR 16
+#endif
+constexpr int WG = GLR_WG, LPR = GLR_LPR, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
 #ifndef GLR_TF
 #define GLR_TF 16
 #endif
@@ -118,14 +124,14 @@ constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
 static_assert(GLR_CHUNK % TPL_FWD == 0 && GLR_CHUNK % TPL_BWD == 0, "kept states fall between groups");
 
-// What the tiles of one call publish: per tile and channel its map and the state behind it, and per
-// tile and channel block how far it is; then the counter that hands out tiles.
+// What the tiles of one call publish: per tile and channel its map and the state behind it; per chain a
+// row of words, its counter and how far each tile is.
 struct Chain {
   uint64_t* map;    // [B, tiles, D]: A in the low half, H in the high one
   uint32_t* state;  // [B, tiles, D]
-  uint32_t* flag;   // [B, blocks, tiles]
-  uint32_t* next;
+  uint32_t* flag;   // [B * blocks, row]: the counter, then a word per tile
   int tiles;        // per sequence
+  int row;
 };
 enum : uint32_t { HAS_MAP = 1, HAS_STATE = 2 };
 
@@ -159,26 +165,24 @@ __device__ inline float chain_state(const Chain& c, long at, long stride, uint32
       }
       __builtin_amdgcn_s_sleep(1);
     }
-    uint32_t first = ~0u;
-    while (found >= 0 && polls < POLLS) {
-      first = live ? look(c.state + at - (found + 1) * stride) : 0;
-      if (__all(first != ~0u)) break;
-      ++polls;
-    }
-    h = from_bits(first);
-    for (int k0 = found - 1; k0 >= 0; k0 -= BATCH) {
+    // the state and the maps behind it, the farthest first, BATCH at a time
+    for (int k0 = found - 1; found >= 0; k0 -= BATCH) {
       uint64_t m[BATCH];
+      uint32_t first = 0;
       for (; polls < POLLS; ++polls) {
-        bool there = true;
+        if (live && k0 == found - 1) first = look(c.state + at - (found + 1) * stride);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) m[i] = live && i <= k0 ? look(c.map + at - (k0 - i + 1) * stride) : 0;
+        bool there = first != ~0u;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) there = there && m[i] != ~0ull;
         if (__all(there)) break;
       }
+      if (k0 == found - 1) h = from_bits(first);
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
         if (i <= k0) h = step(from_bits((unsigned)m[i]), h, from_bits((unsigned)(m[i] >> 32)));
+      if (k0 < BATCH) break;
     }
     if (polls >= POLLS) h = __builtin_nanf("");
   }
@@ -187,15 +191,6 @@ __device__ inline float chain_state(const Chain& c, long at, long stride, uint32
     if (lane == 0) publish(flag, (uint32_t)HAS_STATE);
   }
   return h;
-}
-
-// This workgroup's tile of the whole call: tiles in chain order, channel blocks fastest.
-__device__ inline unsigned take_tile(const Chain& c) {
-  if (c.tiles == 1) return blockIdx.x;
-  __shared__ unsigned mine;
-  if (threadIdx.x == 0) mine = __hip_atomic_fetch_add(c.next, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
-  __syncthreads();
-  return mine;
 }
 
 __global__ __launch_bounds__(256) void glr_clear_kernel(u32x4* p, long n) {
@@ -239,18 +234,28 @@ __device__ inline void load_tokens(const E* tile, const Where& w, float (*v)[4])
   }
 }
 
-// Where a workgroup's tile is.
+// Which tile a workgroup takes: the chain by its number, so that workgroups started one after another
+// read along the rows, shifted by one from row to row, so that an XCD (every eighth workgroup) is not
+// always at the same channels; in the chain the next one.
 struct Tile {
-  int b, order, c0;      // sequence, place in its chain, first channel
-  long chain;            // b * blocks + channel block
-  bool none;             // no such tile: a counter that another call moved
+  int b, order, c0;  // sequence, place in its chain, first channel
+  uint32_t* flag;    // the tile's
+  bool none;         // no such tile: a counter that another call moved
   __device__ inline Tile(const GlrParams& p, const Chain& c) {
-    const unsigned job = __builtin_amdgcn_readfirstlane(take_tile(c)), nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
-    order = job / chains;
-    none = order >= c.tiles;
-    chain = job % chains;
-    b = (unsigned)chain / nblk;
-    c0 = (int)((unsigned)chain % nblk) * CC;
+    const unsigned nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
+    const unsigned round = blockIdx.x / chains, chain = (blockIdx.x + round) % chains;
+    order = 0;
+    uint32_t* row = c.flag + (long)chain * c.row;
+    if (c.tiles > 1) {
+      __shared__ unsigned next;
+      if (threadIdx.x == 0) next = __hip_atomic_fetch_add(row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+      __syncthreads();
+      order = __builtin_amdgcn_readfirstlane(next);
+    }
+    flag = row + 1 + order;
+    none = order < 0 || order >= c.tiles;
+    b = chain / nblk;
+    c0 = (int)(chain % nblk) * CC;
   }
 };
 
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(WG, GLR_OF) void glr_fwd_kernel(GlrParams p, Chain 
       TA = times(TA, sA[k][tid]);
     }
     float h = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                          chain.flag + tile.chain * chain.tiles + tile.order, tile.order, live, TA, TH,
+                          tile.flag, tile.order, live, TA, TH,
                           live && p.h0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
@@ -451,7 +456,7 @@ __global__ __launch_bounds__(WG, GLR_OB) void glr_bwd_kernel(GlrParams p, Chain 
       TA = times(TA, sA[k][tid]);
     }
     float flow = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                             chain.flag + tile.chain * chain.tiles + tile.order, tile.order, live, TA, TF,
+                             tile.flag, tile.order, live, TA, TF,
                              live && p.dh_final ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = NG - 1; k >= 0; --k) {
@@ -495,17 +500,18 @@ enum Which { FWD, BWD, DECODE };
 int tile_tokens(Which which) { return NG * (which == FWD ? TPL_FWD : TPL_BWD); }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+int flag_row(int tiles) { return (tiles + 1 + 31) / 32 * 32; }  // whole 128-byte lines
+
 // Byte offsets of the chain's arrays in the workspace.
 struct Layout {
-  size_t state, flag, next, total;
+  size_t state, flag, total;
 };
 Layout layout(int B, int tiles, int D) {
   const size_t n = (size_t)B * tiles * D, blocks = (D + CC - 1) / CC;
   Layout l;
   l.state = up256(n * 8);
   l.flag = l.state + up256(n * 4);
-  l.next = l.flag + up256((size_t)B * blocks * tiles * 4);
-  l.total = l.next + 256;
+  l.total = l.flag + up256((size_t)B * blocks * flag_row(tiles) * 4);
   return l;
 }
 
@@ -517,14 +523,14 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
     return hipGetLastError();
   }
   const int TT = tile_tokens(which);
-  Chain c{nullptr, nullptr, nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1};
+  Chain c{nullptr, nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1, 0};
   if (c.tiles > 1) {
     const Layout l = layout(p.B, c.tiles, p.D);
     char* ws = static_cast<char*>(p.ws);
     c.map = reinterpret_cast<uint64_t*>(ws);
     c.state = reinterpret_cast<uint32_t*>(ws + l.state);
     c.flag = reinterpret_cast<uint32_t*>(ws + l.flag);
-    c.next = reinterpret_cast<uint32_t*>(ws + l.next);
+    c.row = flag_row(c.tiles);
     const long v = (long)(l.total / 16), wgs = (v + 255) / 256;
     hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, st,
                        reinterpret_cast<u32x4*>(ws), v);
