@@ -7,8 +7,8 @@
 //
 // Nothing but bytes bounds these kernels (an exp and about 20 other instructions per element), so
 // the sequence kernels read each input once and write each output once, in one pass.  A workgroup
-// takes a tile of TT tokens x 64 channels: 16 groups of 16 lanes, a group TPL consecutive tokens, a
-// lane 4 channels.  The tile's gates and inputs stay in registers while its place in the sequence is
+// takes a tile of 128 (backward 64) tokens x 64 channels: 16 groups of 16 lanes, a group 8 (4) consecutive
+// tokens, a lane 4 channels.  The tile's gates and inputs stay in registers while its place in the sequence is
 // found:
 //   1. each lane reduces its tokens to the affine map of the state (A, H): h -> A h + H;
 //   2. one wavefront, a lane per channel, folds the 16 groups' maps into the tile's, publishes it,
@@ -88,38 +88,33 @@ __device__ inline float slope(float a, float w) {
   return w > 0.f ? -a * a * __builtin_amdgcn_rcpf(w) : 0.f;
 }
 
-// Four consecutive channels.
-__device__ inline void load4(const float* p, float* v) {
-  const floatx4 r = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(p));
+// Four consecutive channels as they are in memory.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<float> {
+  typedef floatx4 type;
+};
+template <>
+struct Raw<bf16> {
+  typedef u32x2 type;
+};
+template <typename E>
+using raw4 = typename Raw<E>::type;
+__device__ inline void unpack4(floatx4 r, float* v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = r[e];
 }
-__device__ inline void load4(const bf16* p, float* v) {
-  const bf16x4 r = __builtin_bit_cast(bf16x4, __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p)));
+__device__ inline void unpack4(u32x2 r, float* v) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = to_float(r[e]);
+  for (int e = 0; e < 4; ++e) v[e] = from_bits(e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
 }
 
-#ifndef GLR_WG
-#define GLR_WG 256
-#endif
-#ifndef GLR_LPR
-#define GLR_LPR 16
-#endif
-constexpr int WG = GLR_WG, LPR = GLR_LPR, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
-#ifndef GLR_TF
-#define GLR_TF 16
-#endif
-#ifndef GLR_OF
-#define GLR_OF 2
-#endif
-#ifndef GLR_OB
-#define GLR_OB 2
-#endif
-#ifndef GLR_TB
-#define GLR_TB 8
-#endif
-constexpr int TPL_FWD = GLR_TF, TPL_BWD = GLR_TB;                        // tokens per lane
+constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
+// Tokens of a lane.  Fewer leave registers for more wavefronts, more make fewer and shorter chains.
+// Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 421, 8: 216,
+// 16: 230; backward 4: 119, 8: 128, 16: 174.
+constexpr int TPL_FWD = 8, TPL_BWD = 4;
 constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
 static_assert(GLR_CHUNK % TPL_FWD == 0 && GLR_CHUNK % TPL_BWD == 0, "kept states fall between groups");
@@ -211,67 +206,99 @@ template <typename E>
 __device__ inline E* at_byte(E* p, unsigned off) {
   return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) + off);
 }
-// A lane's TPL tokens; past the end 0, the identity (g = 0, x = 0).
+// A lane's TPL tokens; past the end the last one there is (none at all for L = 0).
 template <int TPL, typename E>
-__device__ inline void load_tokens(const E* tile, const Where& w, float (*v)[4]) {
+__device__ inline void load_tokens(const E* tile, const Where& w, raw4<E>* v) {
   if (w.inside) {
 #pragma unroll
-    for (int j = 0; j < TPL; ++j) load4(at_byte(tile + (long)j * w.stride, w.off * (unsigned)sizeof(E)), v[j]);
-  } else if (w.left <= 0) {  // L = 0: there is no token to read
-#pragma unroll
     for (int j = 0; j < TPL; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[j][e] = 0.f;
-  } else {
+      v[j] = __builtin_nontemporal_load(
+          reinterpret_cast<const raw4<E>*>(at_byte(tile + (long)j * w.stride, w.off * (unsigned)sizeof(E))));
+  } else if (w.left > 0) {
     const unsigned lane = w.off - (unsigned)w.first * w.stride;
 #pragma unroll
     for (int j = 0; j < TPL; ++j) {
-      const int t = w.first + j;
-      load4(at_byte(tile, (lane + (unsigned)(t < w.left ? t : w.left - 1) * w.stride) * (unsigned)sizeof(E)), v[j]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[j][e] = t < w.left ? v[j][e] : 0.f;
+      const int t = w.first + j < w.left ? w.first + j : w.left - 1;
+      v[j] = *reinterpret_cast<const raw4<E>*>(at_byte(tile, (lane + (unsigned)t * w.stride) * (unsigned)sizeof(E)));
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TPL; ++j) v[j] = raw4<E>{};
   }
 }
+// Token j as floats; past the end 0, the identity (g = 0, x = 0).
+template <typename R>
+__device__ inline void token(const R* r, int j, const Where& w, float* v) {
+  unpack4(r[j], v);
+  if (!w.inside)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = w.first + j < w.left ? v[e] : 0.f;
+}
+// What follows unpacks a token again rather than holding its floats (twice the registers) until then.
+__device__ inline void again(u32x2& r) { asm volatile("" : "+v"(r)); }
+__device__ inline void again(floatx4&) {}
+// Ends a stretch of a few tokens: left to itself the compiler works on all of them at once, in more
+// registers than there are.
+__device__ inline void stretch(int j, int tokens) {
+  if (j % tokens == tokens - 1) __builtin_amdgcn_sched_barrier(0);
+}
 
-// Which tile a workgroup takes: the chain by its number, so that workgroups started one after another
-// read along the rows, shifted by one from row to row, so that an XCD (every eighth workgroup) is not
-// always at the same channels; in the chain the next one.
+// Workgroup k takes a tile of the chain that its number names, so that workgroups started one after
+// another read along the rows, shifted by one from row to row, so that an XCD (every eighth workgroup) is
+// not always at the same channels; in its chain the workgroup takes the next tile.
+struct Jobs {
+  unsigned nblk, chains;
+  __device__ inline Jobs(const GlrParams& p, const Chain& c) : nblk((p.D + CC - 1) / CC), chains(nblk * p.B) {}
+  __device__ inline unsigned chain(unsigned job) const { return (job + job / chains) % chains; }
+};
+// The next tile of a chain, for one lane.
+__device__ inline int take_tile(const Chain& c, unsigned chain) {
+  if (c.tiles == 1) return 0;
+  return (int)(__hip_atomic_fetch_add(c.flag + (long)chain * c.row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
+}
+
+// One tile as a lane sees it.
+template <int TPL>
 struct Tile {
-  int b, order, c0;  // sequence, place in its chain, first channel
-  uint32_t* flag;    // the tile's
-  bool none;         // no such tile: a counter that another call moved
-  __device__ inline Tile(const GlrParams& p, const Chain& c) {
-    const unsigned nblk = (p.D + CC - 1) / CC, chains = nblk * p.B;
-    const unsigned round = blockIdx.x / chains, chain = (blockIdx.x + round) % chains;
-    order = 0;
-    uint32_t* row = c.flag + (long)chain * c.row;
-    if (c.tiles > 1) {
-      __shared__ unsigned next;
-      if (threadIdx.x == 0) next = __hip_atomic_fetch_add(row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
-      __syncthreads();
-      order = __builtin_amdgcn_readfirstlane(next);
-    }
-    flag = row + 1 + order;
+  int b, order, c0, tile0;  // sequence, place in its chain, first channel and token
+  unsigned chain;
+  bool none;                // no such tile: the counter was moved by another call
+  Where w;
+  long base;                // of the tile's first token and channel
+  __device__ inline void set(const GlrParams& p, const Chain& c, const Jobs& jobs, unsigned job, int taken, bool backward) {
+    constexpr int TT = NG * TPL;
+    chain = jobs.chain(job);
+    order = taken;
     none = order < 0 || order >= c.tiles;
-    b = chain / nblk;
-    c0 = (int)(chain % nblk) * CC;
+    if (none) order = 0;
+    b = chain / jobs.nblk;
+    c0 = (int)(chain % jobs.nblk) * CC;
+    tile0 = (backward ? c.tiles - 1 - order : order) * TT;
+    const int grp = threadIdx.x / LPR, col = threadIdx.x % LPR * 4;
+    w = Where{(unsigned)(grp * TPL * p.D + (c0 + col < p.D ? col : 0)), grp * TPL, p.L - tile0, tile0 + TT <= p.L, p.D};
+    base = ((long)b * p.L + tile0) * p.D + c0;
   }
 };
 
-// a <- the gates' factors; whether one of the wavefront's is 0
-template <int TPL, int GATE>
-__device__ inline bool factors(float (*a)[4], float (*w)[4]) {
+// a <- the gates' factors, w <- their weights (FOLD: times the inputs); whether one of the wavefront's
+// gates is a reset.
+template <int TPL, int GATE, bool FOLD, typename R>
+__device__ inline bool weigh(const floatx4* rg, const R* rx, const Where& at, float (*a)[4], float (*w)[4]) {
   float m = 1.f;
 #pragma unroll
-  for (int j = 0; j < TPL; ++j)
+  for (int j = 0; j < TPL; ++j) {
+    float g[4], x[4];
+    token(rg, j, at, g);
+    if (FOLD) token(rx, j, at, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float g = a[j][e];
-      a[j][e] = factor(g);
+      a[j][e] = factor(g[e]);
       m = fminf(m, a[j][e]);
-      w[j][e] = weight<GATE>(g, a[j][e]);
+      w[j][e] = weight<GATE>(g[e], a[j][e]);
+      if (FOLD) w[j][e] *= x[e];
     }
+    stretch(j, 2);
+  }
   return __any(m == 0.f);
 }
 
@@ -303,33 +330,31 @@ __device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4
 }
 
 template <typename E, int GATE>
-__global__ __launch_bounds__(WG, GLR_OF) void glr_fwd_kernel(GlrParams p, Chain chain) {
-  constexpr int TPL = TPL_FWD, TT = NG * TPL;
+__global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
+  constexpr int TPL = TPL_FWD;
   __shared__ float sA[NG][CC], sH[NG][CC];  // the groups' maps; then sH the groups' start states
-  const Tile tile(p, chain);
-  if (tile.none) return;
+  __shared__ int taken;
+  const Jobs jobs(p, chain);
   const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
-  const int tile0 = tile.order * TT;
-  const bool here = tile.c0 + col < p.D;
-  const Where w{(unsigned)(grp * TPL * p.D + (here ? col : 0)), grp * TPL, p.L - tile0, tile0 + TT <= p.L, p.D};
-  const long base = ((long)tile.b * p.L + tile0) * p.D + tile.c0;
+  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x));
+  barrier_lds();
+  Tile<TPL> tile;
+  tile.set(p, chain, jobs, blockIdx.x, __builtin_amdgcn_readfirstlane(taken), false);
+  if (tile.none) return;
   float a[TPL][4], u[TPL][4], A[4], H[4];
-  load_tokens<TPL>(p.g + base, w, a);
-  load_tokens<TPL>(static_cast<const E*>(p.x) + base, w, u);
   bool resets;
   {
-    float wt[TPL][4];
-    resets = factors<TPL, GATE>(a, wt);
-#pragma unroll
-    for (int j = 0; j < TPL; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[j][e] *= wt[j][e];
+    floatx4 rg[TPL];
+    raw4<E> rx[TPL];
+    load_tokens<TPL>(p.g + tile.base, tile.w, rg);
+    load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
+    resets = weigh<TPL, GATE, true>(rg, rx, tile.w, a, u);
   }
   if (resets) fwd_map<TPL, true>(a, u, A, H);
   else fwd_map<TPL, false>(a, u, A, H);
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
-  __syncthreads();
+  barrier_lds();
   if (tid < CC) {
     const int ch = tile.c0 + tid;
     const bool live = ch < p.D;
@@ -338,115 +363,136 @@ __global__ __launch_bounds__(WG, GLR_OF) void glr_fwd_kernel(GlrParams p, Chain 
     for (int k = 0; k < NG; ++k) {
       TH = step(sA[k][tid], TH, sH[k][tid]);
       TA = times(TA, sA[k][tid]);
+      stretch(k, 4);
     }
     float h = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                          tile.flag, tile.order, live, TA, TH,
+                          chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TH,
                           live && p.h0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      const float next = step(sA[k][tid], h, sH[k][tid]);
+      const float behind = step(sA[k][tid], h, sH[k][tid]);
       sH[k][tid] = h;
-      h = next;
+      h = behind;
+      stretch(k, 4);
     }
     if (live && p.h_final && tile.order == chain.tiles - 1) p.h_final[(long)tile.b * p.D + ch] = h;
   }
-  __syncthreads();
-  const int mine = w.left - w.first;  // tokens of this lane and behind
-  if (!here || mine <= 0) return;
+  barrier_lds();
+  const int have = tile.w.left - tile.w.first;  // tokens of this lane and behind
+  if (tile.c0 + col >= p.D || have <= 0) return;
   const floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]);
-  if (p.states && w.first % GLR_CHUNK == 0) {
+  if (p.states && tile.w.first % GLR_CHUNK == 0) {
     const int nc = (p.L + GLR_CHUNK - 1) / GLR_CHUNK;
-    float* to = p.states + ((long)tile.b * nc + (tile0 + w.first) / GLR_CHUNK) * p.D + tile.c0 + col;
+    float* to = p.states + ((long)tile.b * nc + (tile.tile0 + tile.w.first) / GLR_CHUNK) * p.D + tile.c0 + col;
     *reinterpret_cast<floatx4*>(to) = h;
   }
-  E* out = static_cast<E*>(p.O) + base;
-  const int stores = w.inside ? TPL : mine;
-  if (resets) fwd_out<TPL, true>(a, u, h, out, w, stores);
-  else fwd_out<TPL, false>(a, u, h, out, w, stores);
+  E* out = static_cast<E*>(p.O) + tile.base;
+  const int stores = tile.w.inside ? TPL : have;
+  if (resets) fwd_out<TPL, true>(a, u, h, out, tile.w, stores);
+  else fwd_out<TPL, false>(a, u, h, out, tile.w, stores);
 }
 
 // The same from the other end.  With flow_t = a_t lambda_t, the gradient that reaches the state
 // before token t, flow_t = a_t (dO_t + flow_{t+1}): an affine recurrence over the same gates, tiles
 // handed out from the last to the first.  A group's start state comes from the kept state of its
 // 64 tokens and the maps of the groups between.
-template <int TPL, bool RESETS>
-__device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const float (*x)[4], const float (*d)[4], float* A,
+template <int TPL, bool RESETS, typename R>
+__device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, const R* rd, const Where& at, float* A,
                                float* H, float* F) {
   typedef Gates<RESETS> G;
 #pragma unroll
   for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = F[e] = 0.f;
 #pragma unroll
-  for (int j = 0; j < TPL; ++j)
+  for (int j = 0; j < TPL; ++j) {
+    float x[4];
+    token(rx, j, at, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = G::marked(a[j][e]);
       A[e] = G::product(A[e], a[j][e]);
-      H[e] = G::next(a[j][e], H[e], w[j][e] * x[j][e]);
+      H[e] = G::next(a[j][e], H[e], w[j][e] * x[e]);
     }
-#pragma unroll
-  for (int j = TPL - 1; j >= 0; --j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) F[e] = G::pass(a[j][e], a[j][e] * (d[j][e] + F[e]));
-}
-
-template <int TPL, int GATE, bool RESETS>
-__device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], float (*x)[4], const float (*d)[4], floatx4 h,
-                               floatx4 flow, float* dx, float* dg, const Where& at, int left) {
-  typedef Gates<RESETS> G;
-#pragma unroll
-  for (int j = 0; j < TPL; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {  // x becomes dh_t / dg_t
-      const float u = w[j][e] * x[j][e], ah = a[j][e] * h[e];
-      x[j][e] = G::pass(a[j][e], ah + slope<GATE>(a[j][e], w[j][e]) * x[j][e]);
-      h[e] = G::pass(a[j][e], ah) + u;
-    }
+    stretch(j, 4);
+  }
 #pragma unroll
   for (int j = TPL - 1; j >= 0; --j) {
+    float d[4];
+    token(rd, j, at, d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) F[e] = G::pass(a[j][e], a[j][e] * (d[e] + F[e]));
+    stretch(j, 4);
+  }
+}
+
+template <int TPL, int GATE, bool RESETS, typename R>
+__device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], const R* rx, const R* rd, const Where& at,
+                               floatx4 h, floatx4 flow, float* dx, float* dg, int left) {
+  typedef Gates<RESETS> G;
+  float q[TPL][4];  // dh_t / dg_t
+#pragma unroll
+  for (int j = 0; j < TPL; ++j) {
+    float x[4];
+    token(rx, j, at, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ah = a[j][e] * h[e];
+      q[j][e] = G::pass(a[j][e], ah + slope<GATE>(a[j][e], w[j][e]) * x[e]);
+      h[e] = G::pass(a[j][e], ah) + w[j][e] * x[e];
+    }
+    stretch(j, 2);
+  }
+#pragma unroll
+  for (int j = TPL - 1; j >= 0; --j) {
+    float d[4];
+    token(rd, j, at, d);
     floatx4 px, pg;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float lam = d[j][e] + flow[e];
+      const float lam = d[e] + flow[e];
       px[e] = w[j][e] * lam;
-      pg[e] = G::pass(a[j][e], lam * x[j][e]);
+      pg[e] = G::pass(a[j][e], lam * q[j][e]);
       flow[e] = G::pass(a[j][e], a[j][e] * lam);
     }
     if (j < left) {
       *reinterpret_cast<floatx4*>(at_byte(dx + (long)j * at.stride, at.off * 4u)) = px;
       *reinterpret_cast<floatx4*>(at_byte(dg + (long)j * at.stride, at.off * 4u)) = pg;
     }
+    stretch(j, 2);
   }
 }
 
 template <typename E, int GATE>
-__global__ __launch_bounds__(WG, GLR_OB) void glr_bwd_kernel(GlrParams p, Chain chain) {
-  constexpr int TPL = TPL_BWD, TT = NG * TPL, GPC = GLR_CHUNK / TPL;  // groups per kept state
+__global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
+  constexpr int TPL = TPL_BWD, GPC = GLR_CHUNK / TPL;  // groups per kept state
   __shared__ float sA[NG][CC], sH[NG][CC], sF[NG][CC];
-  const Tile tile(p, chain);
-  if (tile.none) return;
+  __shared__ int taken;
+  const Jobs jobs(p, chain);
   const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
-  const int tile0 = (chain.tiles - 1 - tile.order) * TT;
-  const bool here = tile.c0 + col < p.D;
-  const Where at{(unsigned)(grp * TPL * p.D + (here ? col : 0)), grp * TPL, p.L - tile0, tile0 + TT <= p.L, p.D};
-  const long base = ((long)tile.b * p.L + tile0) * p.D + tile.c0;
-  float a[TPL][4], w[TPL][4], x[TPL][4], d[TPL][4], A[4], H[4], F[4];
-  load_tokens<TPL>(p.g + base, at, a);
-  load_tokens<TPL>(static_cast<const E*>(p.x) + base, at, x);
-  load_tokens<TPL>(static_cast<const E*>(p.dO) + base, at, d);
-  const bool resets = factors<TPL, GATE>(a, w);
-  if (resets) bwd_map<TPL, true>(a, w, x, d, A, H, F);
-  else bwd_map<TPL, false>(a, w, x, d, A, H, F);
+  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x));
+  barrier_lds();
+  Tile<TPL> tile;
+  tile.set(p, chain, jobs, blockIdx.x, __builtin_amdgcn_readfirstlane(taken), true);
+  if (tile.none) return;
+  floatx4 rg[TPL];
+  raw4<E> rx[TPL], rd[TPL];
+  load_tokens<TPL>(p.g + tile.base, tile.w, rg);
+  load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
+  load_tokens<TPL>(static_cast<const E*>(p.dO) + tile.base, tile.w, rd);
+  float a[TPL][4], w[TPL][4], A[4], H[4], F[4];
+  const bool resets = weigh<TPL, GATE, false>(rg, rx, tile.w, a, w);
+  if (resets) bwd_map<TPL, true>(a, w, rx, rd, tile.w, A, H, F);
+  else bwd_map<TPL, false>(a, w, rx, rd, tile.w, A, H, F);
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   *reinterpret_cast<floatx4*>(&sF[grp][col]) = floatx4{F[0], F[1], F[2], F[3]};
-  __syncthreads();
+  barrier_lds();
   if (tid < CC) {
     const int ch = tile.c0 + tid, nc = (p.L + GLR_CHUNK - 1) / GLR_CHUNK;
     const bool live = ch < p.D;
     float start[NG / GPC];
 #pragma unroll
     for (int n = 0; n < NG / GPC; ++n) {
-      const int chunk = tile0 / GLR_CHUNK + n;
+      const int chunk = tile.tile0 / GLR_CHUNK + n;
       start[n] = live && chunk < nc ? p.states[((long)tile.b * nc + chunk) * p.D + ch] : 0.f;
     }
     float TA = 1.f, TF = 0.f;
@@ -454,15 +500,17 @@ __global__ __launch_bounds__(WG, GLR_OB) void glr_bwd_kernel(GlrParams p, Chain 
     for (int k = NG - 1; k >= 0; --k) {
       TF = step(sA[k][tid], TF, sF[k][tid]);
       TA = times(TA, sA[k][tid]);
+      stretch(k, 4);
     }
     float flow = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                             tile.flag, tile.order, live, TA, TF,
+                             chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TF,
                              live && p.dh_final ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = NG - 1; k >= 0; --k) {
-      const float next = step(sA[k][tid], flow, sF[k][tid]);
+      const float behind = step(sA[k][tid], flow, sF[k][tid]);
       sF[k][tid] = flow;
-      flow = next;
+      flow = behind;
+      stretch(k, 4);
     }
     if (live && p.dh0 && tile.order == chain.tiles - 1) p.dh0[(long)tile.b * p.D + ch] = flow;
 #pragma unroll
@@ -470,19 +518,24 @@ __global__ __launch_bounds__(WG, GLR_OB) void glr_bwd_kernel(GlrParams p, Chain 
       float h = start[n];
 #pragma unroll
       for (int k = n * GPC; k < (n + 1) * GPC; ++k) {
-        const float next = step(sA[k][tid], h, sH[k][tid]);
+        const float behind = step(sA[k][tid], h, sH[k][tid]);
         sH[k][tid] = h;
-        h = next;
+        h = behind;
+        stretch(k, 4);
       }
     }
   }
-  __syncthreads();
-  const int mine = at.left - at.first;
-  if (!here || mine <= 0) return;
+  barrier_lds();
+  const int have = tile.w.left - tile.w.first;
+  if (tile.c0 + col >= p.D || have <= 0) return;
   const floatx4 h = *reinterpret_cast<const floatx4*>(&sH[grp][col]), flow = *reinterpret_cast<const floatx4*>(&sF[grp][col]);
-  const int stores = at.inside ? TPL : mine;
-  if (resets) bwd_out<TPL, GATE, true>(a, w, x, d, h, flow, p.dx + base, p.dg + base, at, stores);
-  else bwd_out<TPL, GATE, false>(a, w, x, d, h, flow, p.dx + base, p.dg + base, at, stores);
+  const int stores = tile.w.inside ? TPL : have;
+#pragma unroll
+  for (int j = 0; j < TPL; ++j) again(rx[j]), again(rd[j]);
+  float* dx = p.dx + tile.base;
+  float* dg = p.dg + tile.base;
+  if (resets) bwd_out<TPL, GATE, true>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
+  else bwd_out<TPL, GATE, false>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
 }
 
 template <typename E, int GATE>
@@ -536,7 +589,8 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
                        reinterpret_cast<u32x4*>(ws), v);
     if (const hipError_t e = hipGetLastError()) return e;
   }
-  const dim3 grid((unsigned)((p.D + CC - 1) / CC) * p.B * c.tiles);
+  const unsigned jobs = (unsigned)((p.D + CC - 1) / CC) * p.B * c.tiles;
+  const dim3 grid(jobs);
   if (which == FWD) hipLaunchKernelGGL((glr_fwd_kernel<E, GATE>), grid, dim3(WG), 0, st, p, c);
   else hipLaunchKernelGGL((glr_bwd_kernel<E, GATE>), grid, dim3(WG), 0, st, p, c);
   return hipGetLastError();

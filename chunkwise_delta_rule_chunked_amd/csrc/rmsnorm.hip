@@ -25,57 +25,102 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // 
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-// n of 8 channels (the rest 0); n = 8 except in a row's last vector
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
+
+// The first n < 8 elements at p in pieces of 4, 2 and 1: accesses that do not wait for each other, as a
+// row's last vector holds up its whole wavefront.  Elements of 2 bytes, the rest 0:
+__device__ inline u32x4 load_part(const bf16* p, int n) {
+  u32x2 four = {};
+  uint32_t two = 0, one = 0;
+  if (n & 4) four = *reinterpret_cast<const u32x2_any*>(p);
+  if (n & 2) two = *reinterpret_cast<const u32_any*>(p + (n & 4));
+  if (n & 1) one = *reinterpret_cast<const u16_any*>(p + (n & 6));
+  const uint32_t lo = n & 2 ? two : one, hi = n & 2 ? one : 0;
+  return u32x4{n & 4 ? four[0] : lo, n & 4 ? four[1] : hi, n & 4 ? lo : 0, n & 4 ? hi : 0};
+}
+__device__ inline void store_part(bf16* p, int n, u32x4 v) {
+  if (n & 4) *reinterpret_cast<u32x2_any*>(p) = u32x2{v[0], v[1]};
+  const uint32_t lo = n & 4 ? v[2] : v[0], hi = n & 4 ? v[3] : v[1];
+  if (n & 2) *reinterpret_cast<u32_any*>(p + (n & 4)) = lo;
+  if (n & 1) *reinterpret_cast<u16_any*>(p + (n & 6)) = (uint16_t)(n & 2 ? hi : lo);
+}
+// of 4 bytes
+struct Eight {
+  floatx4 lo, hi;
+};
+__device__ inline Eight load_part(const float* p, int n) {
+  floatx4 four = {};
+  u32x2 two = {};
+  float one = 0.f;
+  if (n & 4) four = *reinterpret_cast<const floatx4_any*>(p);
+  if (n & 2) two = *reinterpret_cast<const u32x2_any*>(p + (n & 4));
+  if (n & 1) one = p[n & 6];
+  const float r0 = n & 2 ? __builtin_bit_cast(float, (uint32_t)two[0]) : one;
+  const float r1 = __builtin_bit_cast(float, (uint32_t)two[1]), r2 = n & 2 ? one : 0.f;
+  Eight v;
+  v.lo = floatx4{n & 4 ? four[0] : r0, n & 4 ? four[1] : r1, n & 4 ? four[2] : r2, n & 4 ? four[3] : 0.f};
+  v.hi = floatx4{n & 4 ? r0 : 0.f, n & 4 ? r1 : 0.f, n & 4 ? r2 : 0.f, 0.f};
+  return v;
+}
+__device__ inline void store_part(float* p, int n, Eight v) {
+  if (n & 4) *reinterpret_cast<floatx4_any*>(p) = v.lo;
+  const floatx4 r = n & 4 ? v.hi : v.lo;
+  if (n & 2)
+    *reinterpret_cast<u32x2_any*>(p + (n & 4)) = u32x2{__builtin_bit_cast(uint32_t, (float)r[0]), __builtin_bit_cast(uint32_t, (float)r[1])};
+  if (n & 1) p[n & 6] = n & 2 ? r[2] : r[0];
+}
+// of 1 byte
+__device__ inline void store_part(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+  if (n & 4) *reinterpret_cast<u32_any*>(p) = lo;
+  const uint32_t rest = n & 4 ? hi : lo;
+  if (n & 2) *reinterpret_cast<u16_any*>(p + (n & 4)) = (uint16_t)rest;
+  if (n & 1) p[n & 6] = (uint8_t)(n & 2 ? rest >> 16 : rest);
+}
+
+// n of 8 channels (the rest 0; none for n <= 0); n < 8 only in a row's last vector
 template <bool NT>
 __device__ inline void load8(const bf16* p, int n, float* v) {
+  u32x4 r = {};
   if (n >= V) {
     const auto* q = reinterpret_cast<const u32x4_any*>(p);
-    const u32x4 r = NT ? __builtin_nontemporal_load(q) : *q;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __builtin_bit_cast(float, e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = e < n ? to_float(p[e]) : 0.f;
+    r = NT ? __builtin_nontemporal_load(q) : *q;
+  } else if (n > 0) {
+    r = load_part(p, n);
   }
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = __builtin_bit_cast(float, e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
 }
 template <bool NT>
 __device__ inline void load8(const float* p, int n, float* v) {
+  Eight r = {};
   if (n >= V) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const auto* q = reinterpret_cast<const floatx4_any*>(p + 4 * h);
-      const floatx4 r = NT ? __builtin_nontemporal_load(q) : *q;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * h + e] = r[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = e < n ? p[e] : 0.f;
+    const auto* q = reinterpret_cast<const floatx4_any*>(p);
+    r.lo = NT ? __builtin_nontemporal_load(q) : *q;
+    q = reinterpret_cast<const floatx4_any*>(p + 4);
+    r.hi = NT ? __builtin_nontemporal_load(q) : *q;
+  } else if (n > 0) {
+    r = load_part(p, n);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = r.lo[e], v[4 + e] = r.hi[e];
 }
 __device__ inline void store8(bf16* p, int n, const float* v) {
-  if (n >= V) {
-    bf16 r[V];
+  bf16 r[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) r[e] = to_elem<bf16>(v[e]);
-    u32x4 q;
-    __builtin_memcpy(&q, r, 16);
-    *reinterpret_cast<u32x4_any*>(p) = q;
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < n) p[e] = to_elem<bf16>(v[e]);
-  }
+  for (int e = 0; e < V; ++e) r[e] = to_elem<bf16>(v[e]);
+  u32x4 q;
+  __builtin_memcpy(&q, r, 16);
+  if (n >= V) *reinterpret_cast<u32x4_any*>(p) = q;
+  else if (n > 0) store_part(p, n, q);
 }
 __device__ inline void store8(float* p, int n, const float* v) {
+  const Eight r{floatx4{v[0], v[1], v[2], v[3]}, floatx4{v[4], v[5], v[6], v[7]}};
   if (n >= V) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<floatx4_any*>(p + 4 * h) = floatx4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < n) p[e] = v[e];
+    *reinterpret_cast<floatx4_any*>(p) = r.lo;
+    *reinterpret_cast<floatx4_any*>(p + 4) = r.hi;
+  } else if (n > 0) {
+    store_part(p, n, r);
   }
 }
 __device__ inline void store8_e4m3(uint8_t* p, int n, const float* v) {
@@ -85,10 +130,8 @@ __device__ inline void store8_e4m3(uint8_t* p, int n, const float* v) {
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
   if (n >= V) {
     *reinterpret_cast<u32x2_any*>(p) = u32x2{(uint32_t)lo, (uint32_t)hi};
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < n) p[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e % 4)));
+  } else if (n > 0) {
+    store_part(p, n, (uint32_t)lo, (uint32_t)hi);
   }
 }
 
@@ -125,6 +168,28 @@ __device__ inline unsigned row_max(unsigned x, unsigned* lds) {
     for (int i = 0; i < LANES / WAVE; ++i) x = max(x, lds[i]);
   }
   return x;
+}
+
+// Two sums at once; `slot`: which row of the workgroup's (all slots of a workgroup take every step
+// together).
+template <int LANES, int W>
+__device__ inline void row_sums(float& x, float& y, int slot, float (*lds)[W]) {
+#pragma unroll
+  for (int o = (LANES < WAVE ? LANES : WAVE) / 2; o > 0; o >>= 1) {
+    x += __shfl_xor(x, o, WAVE);
+    y += __shfl_xor(y, o, WAVE);
+  }
+  if constexpr (LANES > WAVE) {
+    __syncthreads();
+    if (threadIdx.x % WAVE == 0) lds[0][threadIdx.x / WAVE] = x, lds[1][threadIdx.x / WAVE] = y;
+    __syncthreads();
+    x = y = 0.f;
+#pragma unroll
+    for (int i = 0; i < LANES / WAVE; ++i) {
+      x += lds[0][slot * (LANES / WAVE) + i];
+      y += lds[1][slot * (LANES / WAVE) + i];
+    }
+  }
 }
 
 constexpr int threads(int lanes) { return lanes > 256 ? lanes : 256; }
@@ -280,13 +345,50 @@ __global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
   }
 }
 
+// Eight channels as they are in memory: half a float's registers each for bf16.  What is used twice is
+// unpacked twice (`again` keeps the compiler from holding the floats between).
+template <typename E>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  u32x4 r;
+  __device__ inline void load(const bf16* p, int n) {
+    r = u32x4{};
+    if (n >= V) {
+      r = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    } else if (n > 0) {
+      r = load_part(p, n);
+    }
+  }
+  __device__ inline float operator[](int e) const {
+    return __builtin_bit_cast(float, e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
+  }
+  __device__ inline void again() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x = r[i];
+      asm volatile("" : "+v"(x));
+      r[i] = x;
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float v[V];
+  __device__ inline void load(const float* p, int n) { load8<true>(p, n, v); }
+  __device__ inline float operator[](int e) const { return v[e]; }
+  __device__ inline void again() {}
+};
+
+constexpr int bwd_threads(int lanes) { return lanes > 512 ? lanes : 512; }
+
 // Workgroup k takes rows k RPW .., then gridDim.x * RPW further on, and stores its part of dweight in
 // part[k].  Every part is the sum over a fixed set of rows in a fixed order.
 template <typename E, int LANES, int J>
-__global__ __launch_bounds__(threads(LANES)) void rmsnorm_bwd_kernel(RmsnormParams p) {
-  constexpr int T = threads(LANES), RPW = T / LANES, COLS = LANES * J * V;
-  __shared__ float lds[T / WAVE];
-  const int lane = threadIdx.x % LANES;
+__global__ __launch_bounds__(bwd_threads(LANES), 4) void rmsnorm_bwd_kernel(RmsnormParams p) {
+  constexpr int T = bwd_threads(LANES), RPW = T / LANES, COLS = LANES * J * V;
+  __shared__ float lds[2][T / WAVE];
+  const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
   float w[J][V], acc[J][V];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -295,38 +397,49 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_bwd_kernel(RmsnormPara
     for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
   }
   for (long row0 = (long)blockIdx.x * RPW; row0 < p.rows; row0 += (long)gridDim.x * RPW) {
-    const long row = row0 + threadIdx.x / LANES;
+    const long row = row0 + slot;
     const bool ok = row < p.rows;
     const long base = row * p.width;
-    float s[J][V], d[J][V], o[J][V], ss = 0.f, dot = 0.f;
+    Raw8<E> s[J], d[J], o[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
-      load8<true>(static_cast<const E*>(p.x) + base + i, n, s[j]);
-      load8<true>(static_cast<const E*>(p.dy) + base + i, n, d[j]);
-      if (p.dsum) load8<true>(static_cast<const E*>(p.dsum) + base + i, n, o[j]);
-      else
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[j][e] = 0.f;
+      s[j].load(static_cast<const E*>(p.x) + base + i, n);
+      d[j].load(static_cast<const E*>(p.dy) + base + i, n);
     }
+    if (p.dsum) {
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+      for (int j = 0; j < J; ++j) {
+        const int i = (lane + j * LANES) * V;
+        o[j].load(static_cast<const E*>(p.dsum) + base + i, ok ? p.width - i : 0);
+      }
+    }
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         ss += s[j][e] * s[j][e];
         dot += w[j][e] * d[j][e] * s[j][e];
       }
-    const float rstd = 1.f / sqrtf(row_sum<LANES>(ss, lds) / p.width + p.eps);
-    const float c = rstd * rstd * rstd * (row_sum<LANES>(dot, lds) / p.width);
+      s[j].again(), d[j].again();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    row_sums<LANES>(ss, dot, slot, lds);
+    const float rstd = 1.f / sqrtf(ss / p.width + p.eps);
+    const float c = rstd * rstd * rstd * (dot / p.width);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+      float v[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        o[j][e] = o[j][e] + rstd * (w[j][e] * d[j][e]) - s[j][e] * c;
-        if (ok) acc[j][e] += d[j][e] * s[j][e] * rstd;  // a missing row's rstd is infinite for eps = 0
+        const float t = rstd * d[j][e];
+        v[e] = (p.dsum ? o[j][e] : 0.f) + w[j][e] * t - s[j][e] * c;
+        if (ok) acc[j][e] += t * s[j][e];  // a missing row's rstd is infinite for eps = 0
       }
-      store8(static_cast<E*>(p.dx) + base + i, n, o[j]);
+      store8(static_cast<E*>(p.dx) + base + i, n, v);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (!p.dweight) return;
@@ -342,7 +455,7 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_bwd_kernel(RmsnormPara
     __shared__ float sums[COLS];
     for (int k = 0; k < RPW; ++k) {
       __syncthreads();
-      if ((int)threadIdx.x / LANES == k) {
+      if (slot == k) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -426,17 +539,24 @@ Split split(int width, bool backward) {
   if (width <= 256) return {32, 1};
   if (width <= 512) return {64, 1};
   if (width <= 1024) return {64, 2};
+  if (backward) {
+    if (width <= 2048) return {128, 2};
+    if (width <= 4096) return {256, 2};
+    if (width <= 8192) return {512, 2};
+    if (width <= 16384) return {1024, 2};
+    return {0, 0};
+  }
   if (width <= 2048) return {64, 4};
   if (width <= 4096) return {256, 2};
   if (width <= 8192) return {256, 4};
   if (width <= 16384) return {1024, 2};
-  if (width <= 32768 && !backward) return {1024, 4};
+  if (width <= 32768) return {1024, 4};
   return {0, 0};
 }
 
 // Workgroups: one step over the rows where that is no more than `most`, else `most` that walk.
-long workgroups(long rows, Split s, long most) {
-  const long per = s.lanes == 0 || s.lanes > 256 ? 1 : 256 / s.lanes;
+long workgroups(long rows, Split s, int threads, long most) {
+  const long per = s.lanes == 0 || s.lanes > threads ? 1 : threads / s.lanes;
   const long n = (rows + per - 1) / per;
   return n < most ? n : most;
 }
@@ -448,16 +568,15 @@ hipError_t launch_rows(const RmsnormParams& p, hipStream_t st) {
     hipLaunchKernelGGL((rmsnorm_wide_kernel<E, QUANT>), dim3((unsigned)p.rows), dim3(1024), 0, st, p);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)workgroups(p.rows, s, s.lanes > 256 ? 512 : 2048));
+  const dim3 grid((unsigned)workgroups(p.rows, s, 256, s.lanes > 256 ? 512 : 2048));
   switch (s.lanes * 16 + s.j) {
 #define DELTA_ROWS_CASE(L, J)                                                                               \
   case L * 16 + J:                                                                                          \
     hipLaunchKernelGGL((rmsnorm_kernel<E, L, J, QUANT>), grid, dim3(threads(L)), 0, st, p);                 \
     break;
-#define DELTA_ROWS_CASES(M) \
-  M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(64, 2) M(64, 4) M(256, 2) M(256, 4) M(1024, 2)
+#define DELTA_ROWS_CASES(M) M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(64, 2) M(256, 2) M(1024, 2)
     DELTA_ROWS_CASES(DELTA_ROWS_CASE)
-    DELTA_ROWS_CASE(1024, 4)
+    DELTA_ROWS_CASE(64, 4) DELTA_ROWS_CASE(256, 4) DELTA_ROWS_CASE(1024, 4)
 #undef DELTA_ROWS_CASE
     default: return hipErrorInvalidValue;
   }
@@ -471,9 +590,10 @@ hipError_t launch_rows_bwd(const RmsnormParams& p, hipStream_t st) {
   switch (s.lanes * 16 + s.j) {
 #define DELTA_ROWS_CASE(L, J)                                                                        \
   case L * 16 + J:                                                                                   \
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<E, L, J>), grid, dim3(threads(L)), 0, st, p);             \
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<E, L, J>), grid, dim3(bwd_threads(L)), 0, st, p);             \
     break;
     DELTA_ROWS_CASES(DELTA_ROWS_CASE)
+    DELTA_ROWS_CASE(128, 2) DELTA_ROWS_CASE(512, 2)
 #undef DELTA_ROWS_CASE
 #undef DELTA_ROWS_CASES
     case 0: hipLaunchKernelGGL((rmsnorm_bwd_wide_kernel<E>), grid, dim3(1024), 0, st, p); break;
@@ -494,7 +614,7 @@ hipError_t launch_rmsnorm(const RmsnormParams& p, bool bf16_in, hipStream_t st) 
   return bf16_in ? launch_quant<bf16>(p, st) : launch_quant<float>(p, st);
 }
 
-int rmsnorm_bwd_parts(long rows, int width) { return (int)workgroups(rows, split(width, true), 512); }
+int rmsnorm_bwd_parts(long rows, int width) { return (int)workgroups(rows, split(width, true), 512, 512); }
 
 hipError_t launch_rmsnorm_bwd(const RmsnormParams& p, bool bf16_in, hipStream_t st) {
   const int parts = rmsnorm_bwd_parts(p.rows, p.width);
