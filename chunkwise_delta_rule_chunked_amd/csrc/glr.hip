@@ -206,7 +206,7 @@ template <typename E>
 __device__ inline E* at_byte(E* p, unsigned off) {
   return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) + off);
 }
-// A lane's TPL tokens; past the end the last one there is (none at all for L = 0).
+// A lane's TPL tokens; past the end the last one there is (a tile has one at least).
 template <int TPL, typename E>
 __device__ inline void load_tokens(const E* tile, const Where& w, raw4<E>* v) {
   if (w.inside) {
@@ -214,16 +214,13 @@ __device__ inline void load_tokens(const E* tile, const Where& w, raw4<E>* v) {
     for (int j = 0; j < TPL; ++j)
       v[j] = __builtin_nontemporal_load(
           reinterpret_cast<const raw4<E>*>(at_byte(tile + (long)j * w.stride, w.off * (unsigned)sizeof(E))));
-  } else if (w.left > 0) {
+  } else {
     const unsigned lane = w.off - (unsigned)w.first * w.stride;
 #pragma unroll
     for (int j = 0; j < TPL; ++j) {
       const int t = w.first + j < w.left ? w.first + j : w.left - 1;
       v[j] = *reinterpret_cast<const raw4<E>*>(at_byte(tile, (lane + (unsigned)t * w.stride) * (unsigned)sizeof(E)));
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < TPL; ++j) v[j] = raw4<E>{};
   }
 }
 // Token j as floats; past the end 0, the identity (g = 0, x = 0).
@@ -538,6 +535,114 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
   else bwd_out<TPL, GATE, false>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
 }
 
+// Sequences of up to SHORT tokens: a lane runs its 4 channels from the first token to the last, STEP at a
+// time, where a tile would leave most of its groups without tokens.  Nothing is shared between lanes.
+// Measured at 512 sequences x 2048 channels, bf16: 32 tokens here 53 us (backward 130), 33 tokens in tiles
+// 116 us (135).
+constexpr int SHORT = 32, STEP = 8;
+
+// Sequence, first channel and the lane's place in every [B, L, D] tensor; false past the last lane.
+struct Lane {
+  long first;  // element of token 0
+  long state;  // element of a [B, D] tensor
+  __device__ inline bool set(const GlrParams& p) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x, per = p.D / 4;
+    const long b = i / per;
+    state = i * 4;
+    first = b * p.L * p.D + i % per * 4;
+    return b < p.B;
+  }
+  __device__ inline Where where(const GlrParams& p, int t0) const { return Where{0, 0, p.L - t0, t0 + STEP <= p.L, p.D}; }
+};
+
+template <int TPL, typename E>
+__device__ inline void load_lane(const E* at, const Where& w, raw4<E>* v) {
+#pragma unroll
+  for (int j = 0; j < TPL; ++j) v[j] = *reinterpret_cast<const raw4<E>*>(at + (long)(j < w.left ? j : w.left - 1) * w.stride);
+}
+
+template <typename E, int GATE>
+__global__ __launch_bounds__(256) void glr_fwd_short_kernel(GlrParams p) {
+  Lane lane;
+  if (!lane.set(p)) return;
+  floatx4 h = {};
+  if (p.h0) h = *reinterpret_cast<const floatx4*>(p.h0 + lane.state);
+  if (p.states && p.L > 0) *reinterpret_cast<floatx4*>(p.states + lane.state) = h;
+  for (int t0 = 0; t0 < p.L; t0 += STEP) {
+    const Where w = lane.where(p, t0);
+    const long at = lane.first + (long)t0 * p.D;
+    floatx4 rg[STEP];
+    raw4<E> rx[STEP];
+    float a[STEP][4], u[STEP][4];
+    load_lane<STEP>(p.g + at, w, rg);
+    load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
+    weigh<STEP, GATE, true>(rg, rx, w, a, u);
+#pragma unroll
+    for (int j = 0; j < STEP; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = step(mark(a[j][e]), h[e], u[j][e]);
+      if (j < w.left) store4<E>(static_cast<E*>(p.O) + at + (long)j * p.D, h[0], h[1], h[2], h[3]);
+    }
+  }
+  if (p.h_final) *reinterpret_cast<floatx4*>(p.h_final + lane.state) = h;
+}
+
+template <typename E, int GATE>
+__global__ __launch_bounds__(256) void glr_bwd_short_kernel(GlrParams p) {
+  Lane lane;
+  if (!lane.set(p)) return;
+  floatx4 flow = {};
+  if (p.dh_final) flow = *reinterpret_cast<const floatx4*>(p.dh_final + lane.state);
+  // the states before every STEP tokens, then the steps from the last to the first (their tokens are in
+  // the caches by then)
+  floatx4 start[SHORT / STEP];
+  if (p.L > 0) start[0] = *reinterpret_cast<const floatx4*>(p.states + lane.state);
+#pragma unroll
+  for (int n = 1; n < SHORT / STEP; ++n) {
+    start[n] = start[n - 1];
+    if (n * STEP < p.L) {
+      const Where w = lane.where(p, (n - 1) * STEP);
+      const long at = lane.first + (long)(n - 1) * STEP * p.D;
+      floatx4 rg[STEP];
+      raw4<E> rx[STEP];
+      float a[STEP][4], u[STEP][4];
+      load_lane<STEP>(p.g + at, w, rg);
+      load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
+      weigh<STEP, GATE, true>(rg, rx, w, a, u);
+#pragma unroll
+      for (int j = 0; j < STEP; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) start[n][e] = step(mark(a[j][e]), start[n][e], u[j][e]);
+    }
+  }
+#pragma unroll
+  for (int n = SHORT / STEP - 1; n >= 0; --n) {
+    if (n * STEP >= p.L) continue;
+    const Where w = lane.where(p, n * STEP);
+    const long at = lane.first + (long)n * STEP * p.D;
+    floatx4 rg[STEP];
+    raw4<E> rx[STEP], rd[STEP];
+    float a[STEP][4], wt[STEP][4];
+    load_lane<STEP>(p.g + at, w, rg);
+    load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
+    load_lane<STEP>(static_cast<const E*>(p.dO) + at, w, rd);
+    weigh<STEP, GATE, false>(rg, rx, w, a, wt);
+#pragma unroll
+    for (int j = 0; j < STEP; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[j][e] = mark(a[j][e]);
+    bwd_out<STEP, GATE, true>(a, wt, rx, rd, w, start[n], flow, p.dx + at, p.dg + at, w.inside ? STEP : w.left);
+#pragma unroll
+    for (int j = STEP - 1; j >= 0; --j) {
+      float d[4];
+      token(rd, j, w, d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) flow[e] = Gates<true>::pass(a[j][e], a[j][e] * (d[e] + flow[e]));
+    }
+  }
+  if (p.dh0) *reinterpret_cast<floatx4*>(p.dh0 + lane.state) = flow;
+}
+
 template <typename E, int GATE>
 __global__ __launch_bounds__(256) void glr_decode_kernel(GlrParams p) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
@@ -573,6 +678,12 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
   if (which == DECODE) {
     const long n = (long)p.B * p.D;
     hipLaunchKernelGGL((glr_decode_kernel<E, GATE>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
+  if (p.L <= SHORT) {
+    const dim3 grid((unsigned)(((long)p.B * p.D / 4 + 255) / 256));
+    if (which == FWD) hipLaunchKernelGGL((glr_fwd_short_kernel<E, GATE>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((glr_bwd_short_kernel<E, GATE>), grid, dim3(256), 0, st, p);
     return hipGetLastError();
   }
   const int TT = tile_tokens(which);
