@@ -192,6 +192,20 @@ __device__ inline void row_sums(float& x, float& y, int slot, float (*lds)[W]) {
   }
 }
 
+// How a group's s w, the largest of which is `most` in magnitude, become 8 bits.  rstd cancels from
+// y / scale = 448 s w / max|s w|, and with it a rounding of each value; where that quotient could overflow
+// (`most` tiny, rstd large) it stays in.
+struct Quant {
+  float scale, f1, f2;  // the value is (s w) f1 f2
+  __device__ inline Quant(float most, float rstd) {
+    const float amax = most * rstd;
+    const bool zero = amax < AMAX_MIN, tiny = most < AMAX_MIN;
+    scale = zero ? 0.f : amax / E4M3_MAX;
+    f1 = tiny ? rstd : 1.f;
+    f2 = zero ? 0.f : E4M3_MAX / (tiny ? amax : most);
+  }
+};
+
 constexpr int threads(int lanes) { return lanes > 256 ? lanes : 256; }
 
 // QUANT: 0 y, 1 y8 with a scale per row, 2 y8 with a scale per 128 channels (16 lanes).
@@ -232,7 +246,7 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[j][e] = s[j][e] * rstd * w[j][e];
+      for (int e = 0; e < V; ++e) s[j][e] = (QUANT ? s[j][e] : s[j][e] * rstd) * w[j][e];
     if constexpr (QUANT == 0) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -262,13 +276,11 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
-        const float amax = __builtin_bit_cast(float, m[QUANT == 1 ? 0 : j]);
-        const bool zero = amax < AMAX_MIN;
-        const float inv = zero ? 0.f : E4M3_MAX / amax;
+        const Quant q(__builtin_bit_cast(float, m[QUANT == 1 ? 0 : j]), rstd);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[j][e] *= inv;
+        for (int e = 0; e < V; ++e) s[j][e] = s[j][e] * q.f1 * q.f2;
         store8_e4m3(p.y8 + base + i, n, s[j]);
-        if (n > 0 && i % p.group == 0) p.scale[row * groups + i / p.group] = zero ? 0.f : amax / E4M3_MAX;
+        if (n > 0 && i % p.group == 0) p.scale[row * groups + i / p.group] = q.scale;
       }
     }
   }
@@ -304,7 +316,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
     load8<false>(s0 + i, p.width - i, y);
     load8<false>(p.weight + i, p.width - i, w);
 #pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = y[e] * rstd * w[e];
+    for (int e = 0; e < V; ++e) y[e] = (QUANT ? y[e] : y[e] * rstd) * w[e];
   };
   const int groups = (p.width + p.group - 1) / p.group;
   unsigned all = 0;
@@ -332,14 +344,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o, WAVE));
       }
-      const float amax = __builtin_bit_cast(float, m);
-      const bool zero = amax < AMAX_MIN;
-      const float inv = zero ? 0.f : E4M3_MAX / amax;
+      const Quant q(__builtin_bit_cast(float, m), rstd);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] *= inv;
+      for (int e = 0; e < V; ++e) y[e] = y[e] * q.f1 * q.f2;
       if (n > 0) {
         store8_e4m3(p.y8 + base + i, n, y);
-        if (i % p.group == 0) p.scale[row * groups + i / p.group] = zero ? 0.f : amax / E4M3_MAX;
+        if (i % p.group == 0) p.scale[row * groups + i / p.group] = q.scale;
       }
     }
   }

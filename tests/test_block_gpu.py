@@ -664,3 +664,15 @@ def test_a_serving_step_of_a_block():
     E, _ = fwd_bounds(host(u), host(g), None, "complement")
     check("h", h, hr, E[:, -1] + 1e-38)
     check("o", o[:, 0], hr, E[:, -1] + HALF["bf16"] * (np.abs(hr) + E[:, -1]) + 1e-38)
+
+
+def test_rmsnorm_quant_small_products():
+    """s and the weight both small, rstd large: s w is near the smallest floats, y is not."""
+    W = 256
+    s = 1e-17 * draw(130, (3, W))
+    w = (1e-21 * (1 + 0.2 * draw(131, (W,)))).astype(np.float32)
+    _, y8, sc = D.layer_rmsnorm_quant(to_dev(s, "f32"), to_dev(w, "f32"), eps=0.0, group=128)
+    y = Bk.rmsnorm(s, w, 0.0)
+    full = np.repeat(host(sc), 128, axis=1)
+    # the products keep 2^-149 / 1e-38 of their value or better: 2^-23 or so; the rest as above
+    check("y8 * scale", host(y8) * full, y, np.abs(y) * (2.0 ** -4 + 1e-4) + full * 2.0 ** -9)
