@@ -49,11 +49,14 @@ def _load():
     return _lib
 
 
+_here = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Context in which `device` is current and `stream` (None, a torch stream or a raw handle) its
     current stream."""
     if stream is None:
-        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream))
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
@@ -77,9 +80,7 @@ def _code(t, name):
 
 
 def _arg(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor of this shape, type and device (None: NULL)."""
-    if t is None:
-        return None
+    """Pointer of a contiguous tensor of this shape, type and device."""
     if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
         raise ValueError("%s must be a GPU tensor on %s" % (name, device))
     if t.dtype is not dtype:
@@ -91,11 +92,16 @@ def _arg(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
-def _out(t, name, shape, dtype, device, like=None):
-    """(tensor, pointer) of an output: the given one, checked, or a new one (as `like`, a checked input of
-    its shape and type, where there is one: that is quicker)."""
+def _opt(t, *spec):
+    """As _arg; None: NULL."""
+    return None if t is None else _arg(t, *spec)
+
+
+def _out(t, name, shape, dtype, device, like):
+    """(tensor, pointer) of an output: the given one, checked, or a new one made from the checked input
+    `like` (quicker than from a device, and most so where the shape is the same)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
+        t = torch.empty_like(like, dtype=dtype) if like.shape == shape else like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     return t, _arg(t, name, shape, dtype, device)
 
@@ -163,12 +169,12 @@ def fwd_glr(x, g_log, h0=None, *, input_gate: str = "none", O=None, h_final=None
     gate, dev, sshp = _gate(input_gate), x.device, (B, H, dv)
     with _on(dev, stream):
         px, pg = _arg(x, "x", shp, x.dtype, dev), _arg(g_log, "g_log", shp, _f32, dev)
-        p0, ph, ps = _arg(h0, "h0", sshp, _f32, dev), None, None
+        p0, ph, ps = _opt(h0, "h0", sshp, _f32, dev), None, None
         O, po = _out(O, "O", shp, x.dtype, dev, x)
         if h_final is not None or want_state:
-            h_final, ph = _out(h_final, "h_final", sshp, _f32, dev, h0)
+            h_final, ph = _out(h_final, "h_final", sshp, _f32, dev, x)
         if states is not None or want_states:
-            states, ps = _out(states, "states", (B, -(-L // GLR_CHUNK), H, dv), _f32, dev)
+            states, ps = _out(states, "states", (B, -(-L // GLR_CHUNK), H, dv), _f32, dev, x)
         ws, nws, keep = _workspace(workspace, need, dev)
         rc = _load().delta_fwd_glr(ref, gate, px, pg, p0, po, ph, ps, ws, nws, _raw(dev))
     _check(rc, "delta_fwd_glr")
@@ -189,13 +195,11 @@ def bwd_glr(x, g_log, states, dO, dh_final=None, *, input_gate: str = "none", wa
     with _on(dev, stream):
         px, pg = _arg(x, "x", shp, x.dtype, dev), _arg(g_log, "g_log", shp, _f32, dev)
         ps = _arg(states, "states", (B, -(-L // GLR_CHUNK), H, dv), _f32, dev)
-        pd, ph, p0 = _arg(dO, "dO", shp, x.dtype, dev), _arg(dh_final, "dh_final", sshp, _f32, dev), None
-        if dO is None:
-            raise ValueError("dO is required")
+        pd, ph, p0 = _arg(dO, "dO", shp, x.dtype, dev), _opt(dh_final, "dh_final", sshp, _f32, dev), None
         g["dx"], pdx = _out(g["dx"], "dx", shp, _f32, dev, g_log)
         g["dg_log"], pdg = _out(g["dg_log"], "dg_log", shp, _f32, dev, g_log)
         if g["dh0"] is not None or want_dh0:
-            g["dh0"], p0 = _out(g["dh0"], "dh0", sshp, _f32, dev, dh_final)
+            g["dh0"], p0 = _out(g["dh0"], "dh0", sshp, _f32, dev, x)
         ws, nws, keep = _workspace(workspace, need, dev)
         rc = _load().delta_bwd_glr(ref, gate, px, pg, ps, pd, ph, pdx, pdg, p0, ws, nws, _raw(dev))
     _check(rc, "delta_bwd_glr")
@@ -234,7 +238,7 @@ def layer_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, sum=None, y=No
     rows, width, code = _rows(x, "x")
     dev, shp = x.device, x.shape
     with _on(dev, stream):
-        px, pr, pw = _arg(x, "x", shp, x.dtype, dev), _arg(residual, "residual", shp, x.dtype, dev), \
+        px, pr, pw = _arg(x, "x", shp, x.dtype, dev), _opt(residual, "residual", shp, x.dtype, dev), \
             _arg(weight, "weight", (width,), _f32, dev)
         ps = None
         if residual is not None:
@@ -256,13 +260,13 @@ def layer_rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, group: i
         raise ValueError("group must be 0 (one scale per row) or 128, got %r" % (group,))
     sshp = shp[:-1] + (-(-width // group) if group else 1,)
     with _on(dev, stream):
-        px, pr, pw = _arg(x, "x", shp, x.dtype, dev), _arg(residual, "residual", shp, x.dtype, dev), \
+        px, pr, pw = _arg(x, "x", shp, x.dtype, dev), _opt(residual, "residual", shp, x.dtype, dev), \
             _arg(weight, "weight", (width,), _f32, dev)
         ps = None
         if residual is not None:
             sum, ps = _out(sum, "sum", shp, x.dtype, dev, x)
-        y8, py = _out(y8, "y8", shp, torch.float8_e4m3fn, dev)
-        scale, pc = _out(scale, "scale", sshp, _f32, dev)
+        y8, py = _out(y8, "y8", shp, torch.float8_e4m3fn, dev, x)
+        scale, pc = _out(scale, "scale", sshp, _f32, dev, x)
         rc = _load().delta_layer_rmsnorm_quant(rows, width, code, eps, group, px, pr, pw, ps, py, pc, _raw(dev))
     _check(rc, "delta_layer_rmsnorm_quant")
     return (x if residual is None else sum), y8, scale
@@ -284,7 +288,7 @@ def layer_rmsnorm_bwd(dy, s, weight, dsum=None, *, eps: float = 1e-6, want_dweig
     with _on(dev, stream):
         pdy, ps, pw = _arg(dy, "dy", shp, s.dtype, dev), _arg(s, "s", shp, s.dtype, dev), \
             _arg(weight, "weight", (width,), _f32, dev)
-        pds, pdw = _arg(dsum, "dsum", shp, s.dtype, dev), None
+        pds, pdw = _opt(dsum, "dsum", shp, s.dtype, dev), None
         dx, pdx = _out(dx, "dx", shp, s.dtype, dev, s)
         if dweight is not None or want_dweight:
             dweight, pdw = _out(dweight, "dweight", (width,), _f32, dev, weight)

@@ -119,13 +119,13 @@ constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
 static_assert(GLR_CHUNK % TPL_FWD == 0 && GLR_CHUNK % TPL_BWD == 0, "kept states fall between groups");
 
-// What the tiles of one call publish: per tile and channel its map and the state behind it; per chain a
-// row of words, its counter and how far each tile is.
+// What the tiles of one call publish: a word per tile and channel, first its map, then the state behind
+// it, as the map that forgets what was before (a reset): a reader that expects the one and finds the other
+// folds it in all the same.  Per chain a row of words: its counter and how far each tile is.
 struct Chain {
-  uint64_t* map;    // [B, tiles, D]: A in the low half, H in the high one
-  uint32_t* state;  // [B, tiles, D]
-  uint32_t* flag;   // [B * blocks, row]: the counter, then a word per tile
-  int tiles;        // per sequence
+  uint64_t* map;   // [B, tiles, D]: A in the low half, H in the high one
+  uint32_t* flag;  // [B * blocks, row]: the counter, then a word per tile
+  int tiles;       // per sequence
   int row;
 };
 enum : uint32_t { HAS_MAP = 1, HAS_STATE = 2 };
@@ -136,6 +136,8 @@ __device__ inline void publish(T* p, T v) { __hip_atomic_store(p, v, __ATOMIC_RE
 template <typename T>
 __device__ inline T look(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
+__device__ inline uint64_t map_word(float A, float H) { return (uint64_t)plain_nan(H) << 32 | plain_nan(A); }
+
 // The state this tile starts from, for the channel of this lane (of a whole wavefront; `live`: the
 // channel exists), publishing the tile's map and the state behind it.  at: the tile's word; flag: the
 // tile's flag.
@@ -145,9 +147,9 @@ __device__ inline float chain_state(const Chain& c, long at, long stride, uint32
   const int lane = threadIdx.x % WAVE;
   float h = init;
   if (tile > 0) {
-    if (live) publish(c.map + at, (uint64_t)plain_nan(H) << 32 | plain_nan(A));
+    if (live) publish(c.map + at, map_word(A, H));
     if (lane == 0) publish(flag, (uint32_t)HAS_MAP);
-    int polls = 0, found = -1;
+    int polls = 0, found = -1;  // the nearest predecessor (0: the one before) with a state, and maps behind it
     for (; polls < POLLS; ++polls) {
       const uint32_t f = lane < tile ? look(flag - 1 - lane) : 0;
       const uint64_t states = __ballot(f == HAS_STATE), maps = __ballot(f == HAS_STATE || f == HAS_MAP);
@@ -160,29 +162,27 @@ __device__ inline float chain_state(const Chain& c, long at, long stride, uint32
       }
       __builtin_amdgcn_s_sleep(1);
     }
-    // the state and the maps behind it, the farthest first, BATCH at a time
-    for (int k0 = found - 1; found >= 0; k0 -= BATCH) {
+    // from the farthest on, BATCH at a time
+    for (int k0 = found; k0 >= 0; k0 -= BATCH) {
       uint64_t m[BATCH];
-      uint32_t first = 0;
       for (; polls < POLLS; ++polls) {
-        if (live && k0 == found - 1) first = look(c.state + at - (found + 1) * stride);
+        bool there = true;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) m[i] = live && i <= k0 ? look(c.map + at - (k0 - i + 1) * stride) : 0;
-        bool there = first != ~0u;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) there = there && m[i] != ~0ull;
+        // the flag may be seen before the state: what the fold starts from has to forget what was before
+        if (k0 == found) there = there && (!live || reset(from_bits((unsigned)m[0])));
         if (__all(there)) break;
       }
-      if (k0 == found - 1) h = from_bits(first);
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
         if (i <= k0) h = step(from_bits((unsigned)m[i]), h, from_bits((unsigned)(m[i] >> 32)));
-      if (k0 < BATCH) break;
     }
     if (polls >= POLLS) h = __builtin_nanf("");
   }
   if (tile + 1 < c.tiles) {
-    if (live) publish(c.state + at, plain_nan(step(A, h, H)));
+    if (live) publish(c.map + at, map_word(-0.f, step(A, h, H)));
     if (lane == 0) publish(flag, (uint32_t)HAS_STATE);
   }
   return h;
@@ -240,13 +240,17 @@ __device__ inline void stretch(int j, int tokens) {
   if (j % tokens == tokens - 1) __builtin_amdgcn_sched_barrier(0);
 }
 
-// Workgroup k takes a tile of the chain that its number names, so that workgroups started one after
-// another read along the rows, shifted by one from row to row, so that an XCD (every eighth workgroup) is
-// not always at the same channels; in its chain the workgroup takes the next tile.
+// Workgroup k takes a tile of the chain that its number names; in its chain it takes the next one.  One
+// sequence after the other (rows of many sequences at once would often be the same power of two apart and
+// meet in the same memory channels), along the rows of each, shifted by one block from row to row, so that
+// an XCD (every eighth workgroup) is not always at the same channels.
 struct Jobs {
-  unsigned nblk, chains;
-  __device__ inline Jobs(const GlrParams& p, const Chain& c) : nblk((p.D + CC - 1) / CC), chains(nblk * p.B) {}
-  __device__ inline unsigned chain(unsigned job) const { return (job + job / chains) % chains; }
+  unsigned nblk, per;  // channel blocks; tiles of a sequence
+  __device__ inline Jobs(const GlrParams& p, const Chain& c) : nblk((p.D + CC - 1) / CC), per(nblk * c.tiles) {}
+  __device__ inline unsigned chain(unsigned job) const {
+    const unsigned in = job % per;
+    return job / per * nblk + (in + in / nblk) % nblk;
+  }
 };
 // The next tile of a chain, for one lane.
 __device__ inline int take_tile(const Chain& c, unsigned chain) {
@@ -662,13 +666,12 @@ int flag_row(int tiles) { return (tiles + 1 + 31) / 32 * 32; }  // whole 128-byt
 
 // Byte offsets of the chain's arrays in the workspace.
 struct Layout {
-  size_t state, flag, total;
+  size_t flag, total;
 };
 Layout layout(int B, int tiles, int D) {
   const size_t n = (size_t)B * tiles * D, blocks = (D + CC - 1) / CC;
   Layout l;
-  l.state = up256(n * 8);
-  l.flag = l.state + up256(n * 4);
+  l.flag = up256(n * 8);
   l.total = l.flag + up256((size_t)B * blocks * flag_row(tiles) * 4);
   return l;
 }
@@ -687,12 +690,11 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
     return hipGetLastError();
   }
   const int TT = tile_tokens(which);
-  Chain c{nullptr, nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1, 0};
+  Chain c{nullptr, nullptr, p.L > TT ? (p.L + TT - 1) / TT : 1, 0};
   if (c.tiles > 1) {
     const Layout l = layout(p.B, c.tiles, p.D);
     char* ws = static_cast<char*>(p.ws);
     c.map = reinterpret_cast<uint64_t*>(ws);
-    c.state = reinterpret_cast<uint32_t*>(ws + l.state);
     c.flag = reinterpret_cast<uint32_t*>(ws + l.flag);
     c.row = flag_row(c.tiles);
     const long v = (long)(l.total / 16), wgs = (v + 255) / 256;

@@ -552,6 +552,8 @@ def test_binding_refusals():
         (D.DeltaError, lambda: D.layer_rmsnorm(x, w, eps=-1.0)), (D.DeltaError, lambda: D.layer_rmsnorm(x, w, y=x)),
         (ValueError, lambda: D.layer_rmsnorm_quant(x, w, group=64)), (TypeError, lambda: D.layer_rmsnorm_bwd(x, x.bfloat16(), w)),
         (ValueError, lambda: D.layer_rmsnorm_quant(x, w, scale=torch.empty(2, 8, 2, 2, device="cuda"))),
+        (ValueError, lambda: D.fwd_glr(x, None)), (ValueError, lambda: D.bwd_glr(x, g, None, x)), (ValueError, lambda: D.bwd_glr(x, None, h, x)),
+        (ValueError, lambda: D.layer_rmsnorm(x, None)), (ValueError, lambda: D.decode_glr(x[:, :1].contiguous(), g[:, :1].contiguous(), None)),
         (ValueError, lambda: D.grad_norm([x.transpose(1, 2)])), (TypeError, lambda: D.grad_norm([x.long()])),
     ]
     for i, (err, f) in enumerate(bad):
