@@ -319,6 +319,20 @@ __device__ inline void fwd_map(float (*a)[4], const float (*u)[4], float* A, flo
     }
 }
 
+// Outputs are stored non-temporally (as the inputs are loaded), so that what streams through does not push
+// out the chain's words: 512 x 128 x 2048 forward 169 us (6.4 TB/s) against 202, one 64K sequence 206
+// against 214, backward 2 x 8K 115 against 117.
+template <typename E>
+__device__ inline void store_out(E* p, floatx4 h) {
+  E v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = to_elem<E>(h[e]);
+  raw4<E> r;
+  __builtin_memcpy(&r, v, sizeof(r));
+  __builtin_nontemporal_store(r, reinterpret_cast<raw4<E>*>(p));
+}
+__device__ inline void store_grad(float* p, floatx4 v) { __builtin_nontemporal_store(v, reinterpret_cast<floatx4*>(p)); }
+
 template <int TPL, bool RESETS, typename E>
 __device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4 h, E* out, const Where& w, int left) {
 #pragma unroll
@@ -326,7 +340,7 @@ __device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = Gates<RESETS>::next(a[j][e], h[e], u[j][e]);
     if (j < left)
-      store4<E>(at_byte(out + (long)j * w.stride, w.off * (unsigned)sizeof(E)), h[0], h[1], h[2], h[3]);
+      store_out<E>(at_byte(out + (long)j * w.stride, w.off * (unsigned)sizeof(E)), h);
   }
 }
 
@@ -455,8 +469,8 @@ __device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], const R
       flow[e] = G::pass(a[j][e], a[j][e] * lam);
     }
     if (j < left) {
-      *reinterpret_cast<floatx4*>(at_byte(dx + (long)j * at.stride, at.off * 4u)) = px;
-      *reinterpret_cast<floatx4*>(at_byte(dg + (long)j * at.stride, at.off * 4u)) = pg;
+      store_grad(at_byte(dx + (long)j * at.stride, at.off * 4u), px);
+      store_grad(at_byte(dg + (long)j * at.stride, at.off * 4u), pg);
     }
     stretch(j, 2);
   }
