@@ -163,21 +163,24 @@ int run_clip(int32_t n, const void* const* grads, const int64_t* sizes, const in
   hipStream_t st = static_cast<hipStream_t>(stream);
   double* sums = static_cast<double*>(workspace);
   ClipTable t;
-  int parts = 0;
-  for (int i = 0; i < n;) {
+  int parts = 0, tables = 0;
+  for (int i = 0; i < n; ++tables) {
     i = fill_table(t, i, n, grads, out, sizes, dtypes);
     if (t.count == 0) break;
     const int np = delta::clip_parts(t.first[t.count]);
     if ((rc = hip_status(delta::launch_grad_sums(t, sums + parts, np, st)))) return rc;
     parts += np;
   }
-  if (!scale) return hip_status(delta::launch_grad_finish(sums, parts, norm, st));
-  int i = 0;
-  do {  // the first launch writes the norm, also where there is no element
+  // all tensors in one table: the scaling adds the sums up itself
+  if (scale && tables <= 1) {
+    fill_table(t, 0, n, grads, out, sizes, dtypes);
+    return hip_status(delta::launch_grad_scale(t, sums, parts, max_norm, eps, norm, st));
+  }
+  if ((rc = hip_status(delta::launch_grad_finish(sums, parts, norm, st)))) return rc;
+  for (int i = 0; scale && i < n;) {
     i = fill_table(t, i, n, grads, out, sizes, dtypes);
-    if ((rc = hip_status(delta::launch_grad_scale(t, sums, parts, max_norm, eps, norm, st)))) return rc;
-    norm = nullptr;
-  } while (i < n);
+    if (t.count && (rc = hip_status(delta::launch_grad_scale(t, sums, -1, max_norm, eps, norm, st)))) return rc;
+  }
   return DELTA_OK;
 }
 

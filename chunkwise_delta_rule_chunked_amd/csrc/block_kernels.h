@@ -63,8 +63,8 @@ inline int clip_parts(int64_t pieces) {
   const int64_t rounds = (pieces + CLIP_PARTS - 1) / CLIP_PARTS;
   return pieces ? (int)((pieces + rounds - 1) / rounds) : 0;
 }
-// The sums of one table's squares, sums[0 .. parts); then the norm of `parts` sums in all, alone or
-// with the scaling of one table (norm may be nullptr there)
+// The sums of one table's squares, sums[0 .. parts); then the norm of `parts` sums in all, alone or with
+// the scaling of one table (there parts = -1: *norm is there already)
 hipError_t launch_grad_sums(const ClipTable& t, double* sums, int parts, hipStream_t st);
 hipError_t launch_grad_finish(const double* sums, int parts, float* norm, hipStream_t st);
 hipError_t launch_grad_scale(const ClipTable& t, const double* sums, int parts, float max_norm, float eps, float* norm,

@@ -3,11 +3,14 @@
 // The tensors of a launch come by value in its arguments, so nothing is copied to the device first.
 // Each is cut into pieces of CLIP_PIECE elements; workgroup j sums the squares of pieces j, j + parts,
 // ... in float64 and stores one partial sum, so the result does not depend on the order in which
-// workgroups run.  Every workgroup of the scaling launch then adds up the partial sums itself (in one
-// fixed order, so all get the same norm), which saves a launch between the two.
+// workgroups run.  Where one launch holds all tensors, every workgroup of the scaling then adds up the
+// partial sums itself (in one fixed order, so all get the same norm), which saves a launch between the two.
 //
 // Bound by bytes: one read for the norm, one read and one write for the scaling.  Tensors start at any
-// element: 16-byte accesses at element alignment, as gfx950 allows.
+// element: 16-byte accesses at element alignment, as gfx950 allows.  The sums load ordinarily, the scaling
+// loads and stores non-temporally: what the sums leave in the 256 MB cache serves the scaling.  102M float32
+// values (1.22 GB in all) take 197 us, 6.2 TB/s, the rate of a streaming copy; 206 with non-temporal loads
+// in the sums, 209 with ordinary ones in the scaling, 202 scaling from the last piece to the first.
 #include <hip/hip_runtime.h>
 
 #include "block_kernels.h"
@@ -139,14 +142,12 @@ __device__ inline void piece_scale(const E* g, E* out, long n, float c) {
 __global__ __launch_bounds__(T) void grad_scale_kernel(ClipTable t, const double* sums, int parts, float max_norm,
                                                       float eps, float* norm) {
   __shared__ double lds[T / WAVE];
-  const float total = norm_of(sums, parts, lds);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  const float total = parts < 0 ? *norm : norm_of(sums, parts, lds);
+  if (parts >= 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const float d = total + eps, r = max_norm / d;
   const float c = r >= 1.f || d == 0.f ? 1.f : r;  // NaN stays NaN
-  // from the last piece to the first: the sums read the last ones most recently, and what of them
-  // the 256 MB cache holds need not come from memory again
-  const int piece = t.first[t.count] - 1 - (int)blockIdx.x;
-  if (piece < 0) return;
+  const int piece = blockIdx.x;
+  if (piece >= t.first[t.count]) return;  // no elements at all: the norm is all there is to write
   const int i = tensor_of(t, piece);
   const long lo = (piece - t.first[i]) * CLIP_PIECE, n = min(CLIP_PIECE, (long)t.n[i] - lo);
   if (c == 1.f && t.g[i] == t.out[i]) return;

@@ -678,3 +678,59 @@ def test_rmsnorm_quant_small_products():
     full = np.repeat(host(sc), 128, axis=1)
     # the products keep 2^-149 / 1e-38 of their value or better: 2^-23 or so; the rest as above
     check("y8 * scale", host(y8) * full, y, np.abs(y) * (2.0 ** -4 + 1e-4) + full * 2.0 ** -9)
+
+
+@pytest.mark.parametrize("n,empty", [(95, 1), (96, 0), (96, 3), (97, 0), (192, 2), (193, 0)])
+def test_clip_around_a_full_table(n, empty):
+    """A launch describes 96 tensors: sets that fill one or two exactly, with empty tensors behind them."""
+    gs = [to_dev(draw(140 + i % 5, (3 + i % 7,)), "f32") for i in range(n)] + [torch.empty(0, device="cuda")] * empty
+    ref, outs = Bk.clip([host(g) for g in gs], 1.0, 1e-6)
+    got = D.clip_grads(gs, 1.0, out=[torch.empty_like(g) for g in gs[:n]] + gs[n:])
+    assert abs(float(got) - ref) <= 2 * U * ref
+    norm = D.clip_grads(gs, 1.0)
+    assert torch.equal(norm, got)
+    for i in range(n):
+        check("out %d" % i, gs[i], outs[i], 6 * U * np.abs(outs[i]) + 1e-38) if i % 48 in (0, 47) else None
+        assert torch.allclose(gs[i].double().cpu(), torch.from_numpy(outs[i]), rtol=1e-6, atol=0)
+    assert float(D.clip_grads([torch.empty(0, device="cuda")] * 2, 1.0)) == 0.0
+
+
+def test_glr_batch_does_not_matter():
+    """A sequence's results are the same bits whatever batch it is in."""
+    for L in (7, 32, 33, 128, 129, 3000):
+        x, g = to_dev(draw(150, (5, L, 3, 32), "bf16"), "bf16"), to_dev(log_gates(151, (5, L, 3, 32)), "f32")
+        O, h, st = D.fwd_glr(x, g, input_gate="norm", want_states=True)
+        G = D.bwd_glr(x, g, st, x, h, input_gate="norm")
+        for b in (0, 4):
+            O1, h1, st1 = D.fwd_glr(x[b:b + 1], g[b:b + 1], input_gate="norm", want_states=True)
+            G1 = D.bwd_glr(x[b:b + 1], g[b:b + 1], st1, x[b:b + 1], h1, input_gate="norm")
+            assert torch.equal(O[b:b + 1], O1) and torch.equal(h[b:b + 1], h1) and torch.equal(st[b:b + 1], st1)
+            assert all(torch.equal(G[n][b:b + 1], G1[n]) for n in G)
+
+
+def test_calls_from_several_threads():
+    """Calls at once from several host threads, each on its own stream and without a given workspace."""
+    import threading
+    B, L, H, d = 2, 5000, 2, 64
+    x, g = to_dev(draw(160, (B, L, H, d), "bf16"), "bf16"), to_dev(log_gates(161, (B, L, H, d)), "f32")
+    want = D.fwd_glr(x, g, input_gate="complement", want_states=True)
+    n0 = D.grad_norm([g.clamp_min(-9.0)])
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(6):
+            r = D.fwd_glr(x, g, input_gate="complement", want_states=True, stream=s)
+            with torch.cuda.stream(s):
+                n = D.grad_norm([g.clamp_min(-9.0)])
+            s.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(r, want)) or not torch.equal(n, n0):
+                bad.append(1)
+
+    ts = [threading.Thread(target=work) for _ in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
