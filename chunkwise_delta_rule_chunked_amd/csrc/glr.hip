@@ -68,24 +68,27 @@ struct Gates {
   __device__ static inline float pass(float a, float v) { return RESETS && reset(a) ? 0.f : v; }
 };
 
-// w(g), from a = exp(g).  1 - exp(z) cancels near z = 0, where its series to z^7 takes over (|z| < 0.35:
-// the first dropped term is below 0.35^7 / 8! = 2e-8 of the result); beyond, 1 - a or 1 - a^2 is good to
-// a dozen units of 2^-24.  For the square root z = 2 g.
+// w(g), from a = exp(g).  1 - a and 1 - a^2 cancel near g = 0, where a series takes over.  For 1 - a it is
+// that of 1 - exp(g) to g^7 (|g| < 0.35: the first dropped term is below 0.35^7 / 8! = 2e-8 of the result);
+// for 1 - a^2 = -2 a sinh(g) that of sinh, two terms shorter (|g| < 0.25: 0.25^6 / 7! = 5e-8).  Beyond,
+// the difference is good to a dozen units of 2^-24.
 template <int GATE>
 __device__ inline float weight(float g, float a) {
-  if constexpr (GATE == NONE) return 1.f;
-  constexpr float K = GATE == NORM ? 2.f : 1.f;
-  float s = -K * K * K * K * K * K * K / 5040;
-  s = s * g - K * K * K * K * K * K / 720;
-  s = s * g - K * K * K * K * K / 120;
-  s = s * g - K * K * K * K / 24;
-  s = s * g - K * K * K / 6;
-  s = s * g - K * K / 2;
-  s = s * g - K;
-  s *= g;
-  const float direct = GATE == NORM ? 1.f - a * a : 1.f - a;
-  const float v = fabsf(g) < 0.35f / K ? s : direct;
-  return GATE == NORM ? __builtin_amdgcn_sqrtf(fmaxf(v, 0.f)) : v;
+  if constexpr (GATE == NONE) {
+    return 1.f;
+  } else if constexpr (GATE == COMPLEMENT) {
+    float s = -1.f / 5040;
+    s = s * g - 1.f / 720;
+    s = s * g - 1.f / 120;
+    s = s * g - 1.f / 24;
+    s = s * g - 1.f / 6;
+    s = s * g - 1.f / 2;
+    s = s * g - 1.f;
+    return fabsf(g) < 0.35f ? s * g : 1.f - a;
+  } else {
+    const float t = g * g, s = (t * (t * (-2.f / 120) - 2.f / 6) - 2.f) * (g * a);
+    return __builtin_amdgcn_sqrtf(fmaxf(fabsf(g) < 0.25f ? s : 1.f - a * a, 0.f));
+  }
 }
 
 // dw/dg
@@ -214,7 +217,7 @@ template <typename E>
 __device__ inline E* at_byte(E* p, unsigned off) {
   return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) + off);
 }
-// A lane's TPL tokens; past the end the last one there is (a tile has one at least).
+// A lane's TPL tokens; past the end 0, the identity (g = 0, x = 0).  (A tile has one token at least.)
 template <int TPL, typename E>
 __device__ inline void load_tokens(const E* tile, const Where& w, raw4<E>* v) {
   if (w.inside) {
@@ -228,16 +231,9 @@ __device__ inline void load_tokens(const E* tile, const Where& w, raw4<E>* v) {
     for (int j = 0; j < TPL; ++j) {
       const int t = w.first + j < w.left ? w.first + j : w.left - 1;
       v[j] = *reinterpret_cast<const raw4<E>*>(at_byte(tile, (lane + (unsigned)t * w.stride) * (unsigned)sizeof(E)));
+      if (w.first + j >= w.left) v[j] = raw4<E>{};
     }
   }
-}
-// Token j as floats; past the end 0, the identity (g = 0, x = 0).
-template <typename R>
-__device__ inline void token(const R* r, int j, const Where& w, float* v) {
-  unpack4(r[j], v);
-  if (!w.inside)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = w.first + j < w.left ? v[e] : 0.f;
 }
 // What follows unpacks a token again rather than holding its floats (twice the registers) until then.
 __device__ inline void again(u32x2& r) { asm volatile("" : "+v"(r)); }
@@ -292,13 +288,13 @@ struct Tile {
 // a <- the gates' factors, w <- their weights (FOLD: times the inputs); whether one of the wavefront's
 // gates is a reset.
 template <int TPL, int GATE, bool FOLD, typename R>
-__device__ inline bool weigh(const floatx4* rg, const R* rx, const Where& at, float (*a)[4], float (*w)[4]) {
+__device__ inline bool weigh(const floatx4* rg, const R* rx, float (*a)[4], float (*w)[4]) {
   float m = 1.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j) {
     float g[4], x[4];
-    token(rg, j, at, g);
-    if (FOLD) token(rx, j, at, x);
+    unpack4(rg[j], g);
+    if (FOLD) unpack4(rx[j], x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = factor(g[e]);
@@ -371,7 +367,7 @@ __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
     raw4<E> rx[TPL];
     load_tokens<TPL>(p.g + tile.base, tile.w, rg);
     load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
-    resets = weigh<TPL, GATE, true>(rg, rx, tile.w, a, u);
+    resets = weigh<TPL, GATE, true>(rg, rx, a, u);
   }
   if (resets) fwd_map<TPL, true>(a, u, A, H);
   else fwd_map<TPL, false>(a, u, A, H);
@@ -420,15 +416,15 @@ __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
 // handed out from the last to the first.  A group's start state comes from the kept state of its
 // 64 tokens and the maps of the groups between.
 template <int TPL, bool RESETS, typename R>
-__device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, const R* rd, const Where& at, float* A,
-                               float* H, float* F) {
+__device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, const R* rd, float* A, float* H,
+                               float* F) {
   typedef Gates<RESETS> G;
 #pragma unroll
   for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = F[e] = 0.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j) {
     float x[4];
-    token(rx, j, at, x);
+    unpack4(rx[j], x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = G::marked(a[j][e]);
@@ -440,7 +436,7 @@ __device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, 
 #pragma unroll
   for (int j = TPL - 1; j >= 0; --j) {
     float d[4];
-    token(rd, j, at, d);
+    unpack4(rd[j], d);
 #pragma unroll
     for (int e = 0; e < 4; ++e) F[e] = G::pass(a[j][e], a[j][e] * (d[e] + F[e]));
     stretch(j, 4);
@@ -455,7 +451,7 @@ __device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], const R
 #pragma unroll
   for (int j = 0; j < TPL; ++j) {
     float x[4];
-    token(rx, j, at, x);
+    unpack4(rx[j], x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float ah = a[j][e] * h[e];
@@ -467,7 +463,7 @@ __device__ inline void bwd_out(const float (*a)[4], const float (*w)[4], const R
 #pragma unroll
   for (int j = TPL - 1; j >= 0; --j) {
     float d[4];
-    token(rd, j, at, d);
+    unpack4(rd[j], d);
     floatx4 px, pg;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -502,9 +498,9 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
   load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
   load_tokens<TPL>(static_cast<const E*>(p.dO) + tile.base, tile.w, rd);
   float a[TPL][4], w[TPL][4], A[4], H[4], F[4];
-  const bool resets = weigh<TPL, GATE, false>(rg, rx, tile.w, a, w);
-  if (resets) bwd_map<TPL, true>(a, w, rx, rd, tile.w, A, H, F);
-  else bwd_map<TPL, false>(a, w, rx, rd, tile.w, A, H, F);
+  const bool resets = weigh<TPL, GATE, false>(rg, rx, a, w);
+  if (resets) bwd_map<TPL, true>(a, w, rx, rd, A, H, F);
+  else bwd_map<TPL, false>(a, w, rx, rd, A, H, F);
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   *reinterpret_cast<floatx4*>(&sF[grp][col]) = floatx4{F[0], F[1], F[2], F[3]};
@@ -584,7 +580,10 @@ struct Lane {
 template <int TPL, typename E>
 __device__ inline void load_lane(const E* at, const Where& w, raw4<E>* v) {
 #pragma unroll
-  for (int j = 0; j < TPL; ++j) v[j] = *reinterpret_cast<const raw4<E>*>(at + (long)(j < w.left ? j : w.left - 1) * w.stride);
+  for (int j = 0; j < TPL; ++j) {
+    v[j] = *reinterpret_cast<const raw4<E>*>(at + (long)(j < w.left ? j : w.left - 1) * w.stride);
+    if (j >= w.left) v[j] = raw4<E>{};
+  }
 }
 
 template <typename E, int GATE>
@@ -602,7 +601,7 @@ __global__ __launch_bounds__(256) void glr_fwd_short_kernel(GlrParams p) {
     float a[STEP][4], u[STEP][4];
     load_lane<STEP>(p.g + at, w, rg);
     load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
-    weigh<STEP, GATE, true>(rg, rx, w, a, u);
+    weigh<STEP, GATE, true>(rg, rx, a, u);
 #pragma unroll
     for (int j = 0; j < STEP; ++j) {
 #pragma unroll
@@ -634,7 +633,7 @@ __global__ __launch_bounds__(256) void glr_bwd_short_kernel(GlrParams p) {
       float a[STEP][4], u[STEP][4];
       load_lane<STEP>(p.g + at, w, rg);
       load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
-      weigh<STEP, GATE, true>(rg, rx, w, a, u);
+      weigh<STEP, GATE, true>(rg, rx, a, u);
 #pragma unroll
       for (int j = 0; j < STEP; ++j)
 #pragma unroll
@@ -652,7 +651,7 @@ __global__ __launch_bounds__(256) void glr_bwd_short_kernel(GlrParams p) {
     load_lane<STEP>(p.g + at, w, rg);
     load_lane<STEP>(static_cast<const E*>(p.x) + at, w, rx);
     load_lane<STEP>(static_cast<const E*>(p.dO) + at, w, rd);
-    weigh<STEP, GATE, false>(rg, rx, w, a, wt);
+    weigh<STEP, GATE, false>(rg, rx, a, wt);
 #pragma unroll
     for (int j = 0; j < STEP; ++j)
 #pragma unroll
@@ -661,7 +660,7 @@ __global__ __launch_bounds__(256) void glr_bwd_short_kernel(GlrParams p) {
 #pragma unroll
     for (int j = STEP - 1; j >= 0; --j) {
       float d[4];
-      token(rd, j, w, d);
+      unpack4(rd[j], d);
 #pragma unroll
       for (int e = 0; e < 4; ++e) flow[e] = Gates<true>::pass(a[j][e], a[j][e] * (d[e] + flow[e]));
     }
