@@ -26,8 +26,8 @@
 // workspace, the tile goes on with NaN).
 //
 // Measured, bf16, 2048 channels: 512 sequences of 128 tokens (no chain) 169 us, 6.4 TB/s; one of 64K tokens
-// 206 us, 5.2 TB/s: clearing the workspace (5 us) and waiting along the chain cost the rest; backward
-// 2 x 8K tokens 115 us, 4.7 TB/s.  HBM traffic is what the formulas need plus 7% (forward) and 6%.
+// 205 us, 5.2 TB/s: clearing the workspace (5 us) and waiting along the chain cost the rest; backward
+// 2 x 8K tokens 114 us, 4.7 TB/s.  HBM traffic is what the formulas need plus 7% (forward) and 6%.
 // Tried and slower: workgroups that stay and load their next tile while they wait (its map is published a
 // tile too late: 288 us); one counter for all chains (6 us more at the start of every call); a workgroup per
 // narrow channel block that walks the whole sequence (its scans across lanes: 23 us for 4 x 2K x 1024
@@ -123,9 +123,10 @@ __device__ inline void unpack4(u32x2 r, float* v) {
 
 constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
 // Tokens of a lane.  Fewer leave registers for more wavefronts, more make fewer and shorter chains.
-// Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 421, 8: 216,
-// 16: 230; backward 4: 119, 8: 128, 16: 174.
-constexpr int TPL_FWD = 8, TPL_BWD = 4;
+// Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 265, 8: 206,
+// 16: 235; backward 4: 115, 8: 124.  A sequence of up to 64 tokens is one tile of TPL_SHORT tokens a lane
+// with none left over (256 x 64 x 2048: 47.5 us, 64 with 8).
+constexpr int TPL_FWD = 8, TPL_BWD = 4, TPL_SHORT = 4;
 constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
 static_assert(GLR_CHUNK % TPL_FWD == 0 && GLR_CHUNK % TPL_BWD == 0, "kept states fall between groups");
@@ -348,9 +349,8 @@ __device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4
   }
 }
 
-template <typename E, int GATE>
+template <typename E, int GATE, int TPL>
 __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
-  constexpr int TPL = TPL_FWD;
   __shared__ float sA[NG][CC], sH[NG][CC];  // the groups' maps; then sH the groups' start states
   __shared__ int taken;
   const Jobs jobs(p, chain);
@@ -559,8 +559,8 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
 
 // Sequences of up to SHORT tokens: a lane runs its 4 channels from the first token to the last, STEP at a
 // time, where a tile would leave most of its groups without tokens.  Nothing is shared between lanes.
-// Measured at 512 sequences x 2048 channels, bf16: 32 tokens here 53 us (backward 130), 33 tokens in tiles
-// 116 us (135).
+// Measured at 2048 channels, bf16: 512 sequences of 32 tokens here 53 us (backward 113), of 33 tokens in
+// tiles 78 us (124); 4 of 64 tokens would take 19 us here (37), 11.5 in tiles (13).
 constexpr int SHORT = 32, STEP = 8;
 
 // Sequence, first channel and the lane's place in every [B, L, D] tensor; false past the last lane.
@@ -733,7 +733,8 @@ hipError_t launch_one(const GlrParams& p, Which which, hipStream_t st) {
   }
   const unsigned jobs = (unsigned)((p.D + CC - 1) / CC) * p.B * c.tiles;
   const dim3 grid(jobs);
-  if (which == FWD) hipLaunchKernelGGL((glr_fwd_kernel<E, GATE>), grid, dim3(WG), 0, st, p, c);
+  if (which == FWD && p.L <= NG * TPL_SHORT) hipLaunchKernelGGL((glr_fwd_kernel<E, GATE, TPL_SHORT>), grid, dim3(WG), 0, st, p, c);
+  else if (which == FWD) hipLaunchKernelGGL((glr_fwd_kernel<E, GATE, TPL_FWD>), grid, dim3(WG), 0, st, p, c);
   else hipLaunchKernelGGL((glr_bwd_kernel<E, GATE>), grid, dim3(WG), 0, st, p, c);
   return hipGetLastError();
 }

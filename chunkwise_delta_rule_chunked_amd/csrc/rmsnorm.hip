@@ -10,8 +10,8 @@
 // at any element: the same wide accesses at element alignment, which gfx950 allows, with the row's last
 // vector in three pieces.  Rows past 32768 channels (backward 16384) take a kernel that reads them twice.
 //
-// Measured, bf16: 16384 rows of 2048, forward 48 us (5.6 TB/s), with y in 8 bits 46, backward 57 us (4.8
-// TB/s, of which 5 for adding up dweight's parts); 65536 x 512 forward 43.6 us (6.2 TB/s); 32768 x 1003
+// Measured, bf16: 16384 rows of 2048, forward 48 us (5.6 TB/s), with y in 8 bits 46, backward 54 us (5.0
+// TB/s; 5 of it for adding up dweight's parts); 65536 x 512 forward 43.6 us (6.2 TB/s); 32768 x 1003
 // forward 59 us (4.5 TB/s: accesses that cross their natural alignment), x 1008 50 us; 64 x 2048 in 8 bits
 // 5.8 us, the latency of two rounds to memory and a launch.  Non-temporal stores made no difference to 3% worse.
 #include <hip/hip_runtime.h>
