@@ -317,16 +317,36 @@ def _grad_table(grads, dev, what):
     return dev, len(ts), array.array("q", map(T.numel, ts)), array.array("i", codes), array.array("Q", map(T.data_ptr, ts))
 
 
+def _outs_of(grads, out):
+    """The outputs of the gradients that are not None, in the gradients' order: a dict's by name, a
+    sequence's by place."""
+    if isinstance(grads, dict):
+        if not isinstance(out, dict) or out.keys() != grads.keys():
+            raise ValueError("out must be a dict with the gradients' names")
+        pairs = [(g, out[k]) for k, g in grads.items()]
+    else:
+        out = out if isinstance(out, dict) else list(out)
+        if isinstance(out, dict) or len(out) != len(grads):
+            raise ValueError("out must be a sequence as long as the gradients")
+        pairs = list(zip(grads, out))
+    outs = [o for g, o in pairs if g is not None]
+    if any(o is None for o in outs):
+        raise ValueError("out must have a tensor for every gradient")
+    return outs
+
+
 def _host(a):
     """Address of a host array (of its elements; the caller keeps it alive)."""
     return None if a is None else a.buffer_info()[0]
 
 
 def _norm_or_clip(grads, clip, max_norm, eps, out, norm, workspace, stream):
+    if not isinstance(grads, (dict, list, tuple)):
+        grads = list(grads)
     dev, n, sizes, codes, ptrs = _grad_table(grads, None, "gradient")
     outs = None
     if out is not None:
-        _, _, osizes, ocodes, outs = _grad_table(out, dev, "output")
+        _, _, osizes, ocodes, outs = _grad_table(_outs_of(grads, out), dev, "output")
         if osizes != sizes or ocodes != codes:
             raise ValueError("out must match the gradients one by one in size and type")
     lib, hp, hs, hc = _load(), _host(ptrs), _host(sizes), _host(codes)
@@ -351,6 +371,7 @@ def grad_norm(grads, *, norm=None, workspace=None, stream=None):
 
 def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm=None, workspace=None, stream=None):
     """Scales gradients by min(1, max_norm / (norm + eps)), norm their global 2-norm
-    (delta_clip_grads): in place, or into `out` (tensors like the gradients).  Returns the norm before
+    (delta_clip_grads): in place, or into `out` (tensors like the gradients: for a dict one with the same
+    names, for a sequence one as long, read only where there is a gradient).  Returns the norm before
     clipping, a float32 scalar on the device."""
     return _norm_or_clip(grads, True, float(max_norm), float(eps), out, norm, workspace, stream)

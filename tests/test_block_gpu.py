@@ -734,3 +734,18 @@ def test_calls_from_several_threads():
     for t in ts:
         t.join()
     assert not bad
+
+
+def test_clip_outputs_by_name():
+    """Outputs of a dict are found by name whatever its order; a gradient that is None has none."""
+    gs = {k: to_dev(draw(150 + i, (64,), "f32"), "f32") for i, k in enumerate("wvu")}
+    gs["none"] = None
+    out = {k: None if gs[k] is None else torch.zeros_like(gs[k]) for k in ("none", "u", "v", "w")}
+    ref, outs = Bk.clip([host(gs[k]) for k in "wvu"], 1.0, 1e-6)
+    n = D.clip_grads(gs, 1.0, out=out)
+    assert abs(float(n) - ref) <= 2 * U * ref
+    for k, r in zip("wvu", outs):
+        check(k, out[k], r, 6 * U * np.abs(r))
+    mine = [torch.zeros_like(g) for g in (gs["w"], gs["u"])]
+    D.clip_grads([gs["w"], None, gs["u"]], 1e9, out=[mine[0], torch.zeros(64, device="cuda"), mine[1]])
+    assert torch.equal(mine[0], gs["w"]) and torch.equal(mine[1], gs["u"])

@@ -219,3 +219,16 @@ def test_binding_refuses_before_the_library(lib):
               lambda: D.grad_norm({"dx": x}), lambda: D.grad_norm([]), lambda: D.grad_norm([None])):
         with pytest.raises(ValueError):
             f()
+
+
+def test_clip_outputs_are_paired_by_name_or_place():
+    from chunkwise_delta_rule_chunked_amd.block import _outs_of
+    a, b, c = (torch.zeros(n) for n in (1, 2, 3))
+    grads = {"w": torch.ones(1), "v": None, "u": torch.ones(1)}
+    got = _outs_of(grads, {"u": b, "v": None, "w": a})
+    assert len(got) == 2 and got[0] is a and got[1] is b
+    assert _outs_of([torch.ones(1), None], [a, c])[0] is a and len(_outs_of([None, torch.ones(1)], iter([a, c]))) == 1
+    for g, o in [(grads, [a, b]), (grads, {"w": a}), (grads, {"w": a, "v": c, "u": None}), ([a], {"w": b}), ([a], [b, c]),
+                 ([a, b], [c, None])]:
+        with pytest.raises(ValueError):
+            _outs_of(g, o)
