@@ -124,7 +124,8 @@ __device__ inline void unpack4(u32x2 r, float* v) {
 constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
 // Tokens of a lane.  Fewer leave registers for more wavefronts, more make fewer and shorter chains.
 // Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 265, 8: 206,
-// 16: 235; backward 4: 115, 8: 124.  A sequence of up to 64 tokens is one tile of TPL_SHORT tokens a lane
+// 16: 235; backward 4: 115, 8: 124.  Forward with clearing, 4 x 2K x 1024: 27, 20 and 21; 32 x 512 x 2048: 62,
+// 55 and 59; 3 x 1237 x 240 in float32: 11.4, 10.5 and 12.1.  A sequence of up to 64 tokens is one tile of TPL_SHORT tokens a lane
 // with none left over (256 x 64 x 2048: 47.5 us, 64 with 8).
 constexpr int TPL_FWD = 8, TPL_BWD = 4, TPL_SHORT = 4;
 constexpr int BATCH = 8, POLLS = 1 << 20;
