@@ -3,9 +3,8 @@
 //
 // Bound by bytes: each input is read once and each output written once, a row staying in registers
 // between its sum and its use.  LANES lanes hold a row, J vectors of 8 channels each (lane l the
-// vectors l, l + LANES, ...): the fewest lanes that hold it with few registers, so that a wavefront
-// has whole rows to itself up to 2048 channels (backward 1024) and no barrier stands between load and
-// store; wider rows take several wavefronts.  Workgroups walk over rows, keeping the weight (and,
+// vectors l, l + LANES, ...): one vector where that is possible, up to a workgroup of 512 lanes for 4096
+// channels (`split` has what else was measured).  Workgroups walk over rows, keeping the weight (and,
 // backward, their part of its gradient) in registers.  Rows that are not a multiple of 8 channels start
 // at any element: the same wide accesses at element alignment, which gfx950 allows, with the row's last
 // vector in three pieces.  Rows past 32768 channels (backward 16384) take a kernel that reads them twice.
@@ -211,12 +210,13 @@ struct Quant {
   }
 };
 
-constexpr int threads(int lanes) { return lanes > 256 ? lanes : 256; }
+constexpr int threads(int lanes) { return lanes > WAVE ? lanes : 256; }
 
 // QUANT: 0 y, 1 y8 with a scale per row, 2 y8 with a scale per 128 channels (16 lanes).
 template <typename E, int LANES, int J, int QUANT>
 __global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p) {
   constexpr int T = threads(LANES), RPW = T / LANES;
+  static_assert(LANES <= WAVE || RPW == 1, "row_sum over wavefronts takes all of the workgroup's");
   __shared__ float lds[T / WAVE];
   __shared__ unsigned ldu[T / WAVE];
   const int lane = threadIdx.x % LANES;
@@ -543,55 +543,70 @@ __global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* part,
   }
 }
 
-// Lanes and vectors per lane of a row (0: the kernels for any width).  A lane's registers hold 3 (back
-// 5) floats per channel; 1024 lanes leave 128 registers each.
+// Lanes and vectors per lane of a row (0: the kernels for any width), and the workgroups that walk over
+// the rows where those are many: as many as the card holds, 2048 lanes on each of 256 compute units.  One
+// vector per lane leaves the registers for all of them, which is worth more than rows that need no barrier;
+// measured, bf16, us, to y / to y8 per row: 16384 x 2048, 256 lanes 43.4 / 43.8, 64 lanes of 4 vectors
+// 47.2 / 45.5 (64 rows: 2.9 / 3.6, 4.3 / 5.1); 32768 x 1003, 128 lanes 51.3 / 49.6, 64 of 2 57.6 / 55.8;
+// 8192 x 4096, 512 lanes 44.1 / 44.4, 256 of 2 50.5 / 47.8.  Half or twice the workgroups: 32768 x 1003 66.7
+// and 58.3.  4096 x 8192: 512 of 2 46.0 / 50.8, 1024 lanes 43.6 / 58.4, 256 of 4 48.8 / 55.3; with half the
+// workgroups 50.2 / 46.8.
 struct Split {
-  int lanes, j;
+  int lanes, j, most;
 };
-Split split(int width, bool backward) {
-  if (width <= 64) return {8, 1};
-  if (width <= 128) return {16, 1};
-  if (width <= 256) return {32, 1};
-  if (width <= 512) return {64, 1};
-  if (width <= 1024) return {64, 2};
-  if (backward) {
-    if (width <= 2048) return {128, 2};
-    if (width <= 4096) return {256, 2};
-    if (width <= 8192) return {512, 2};
-    if (width <= 16384) return {1024, 2};
-    return {0, 0};
-  }
-  if (width <= 2048) return {64, 4};
-  if (width <= 4096) return {256, 2};
-  if (width <= 8192) return {256, 4};
-  if (width <= 16384) return {1024, 2};
-  if (width <= 32768) return {1024, 4};
-  return {0, 0};
+Split split(int width) {
+  if (width <= 64) return {8, 1, 2048};
+  if (width <= 128) return {16, 1, 2048};
+  if (width <= 256) return {32, 1, 2048};
+  if (width <= 512) return {64, 1, 2048};
+  if (width <= 1024) return {128, 1, 4096};
+  if (width <= 2048) return {256, 1, 2048};
+  if (width <= 4096) return {512, 1, 1024};
+  if (width <= 8192) return {512, 2, 2048};
+  if (width <= 16384) return {1024, 2, 512};
+  if (width <= 32768) return {1024, 4, 512};
+  return {0, 0, 0};
+}
+// Backward, with its sums for dweight in registers and a part of it per workgroup to add up, 16 wavefronts
+// on a compute unit.  With dsum and dweight, us: 16384 x 2048, 256 lanes 55.0, 128 of 2 vectors 55.7 (64
+// rows: 5.8 and 6.9); 8192 x 4096, 512 lanes 56.0, 256 of 2 59.5; but 32768 x 1003, 128 lanes 73.6, 64 of 2,
+// which need no barrier, 65.8.
+Split split_bwd(int width) {
+  if (width <= 64) return {8, 1, 512};
+  if (width <= 128) return {16, 1, 512};
+  if (width <= 256) return {32, 1, 512};
+  if (width <= 512) return {64, 1, 512};
+  if (width <= 1024) return {64, 2, 512};
+  if (width <= 2048) return {256, 1, 512};
+  if (width <= 4096) return {512, 1, 512};
+  if (width <= 8192) return {512, 2, 512};
+  if (width <= 16384) return {1024, 2, 256};
+  return {0, 0, 256};
 }
 
 // Workgroups: one step over the rows where that is no more than `most`, else `most` that walk.
-long workgroups(long rows, Split s, int threads, long most) {
-  const long per = s.lanes == 0 || s.lanes > threads ? 1 : threads / s.lanes;
+long workgroups(long rows, Split s, int threads) {
+  const long per = s.lanes == 0 ? 1 : threads / s.lanes;
   const long n = (rows + per - 1) / per;
-  return n < most ? n : most;
+  return n < s.most ? n : s.most;
 }
 
 template <typename E, int QUANT>
 hipError_t launch_rows(const RmsnormParams& p, hipStream_t st) {
-  const Split s = split(p.width, false);
+  const Split s = split(p.width);
   if (s.lanes == 0) {
     hipLaunchKernelGGL((rmsnorm_wide_kernel<E, QUANT>), dim3((unsigned)p.rows), dim3(1024), 0, st, p);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)workgroups(p.rows, s, 256, s.lanes > 256 ? 512 : 2048));
+  const dim3 grid((unsigned)workgroups(p.rows, s, threads(s.lanes)));
   switch (s.lanes * 16 + s.j) {
 #define DELTA_ROWS_CASE(L, J)                                                                               \
   case L * 16 + J:                                                                                          \
     hipLaunchKernelGGL((rmsnorm_kernel<E, L, J, QUANT>), grid, dim3(threads(L)), 0, st, p);                 \
     break;
-#define DELTA_ROWS_CASES(M) M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(64, 2) M(256, 2) M(1024, 2)
+#define DELTA_ROWS_CASES(M) M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(256, 1) M(512, 1) M(512, 2) M(1024, 2)
     DELTA_ROWS_CASES(DELTA_ROWS_CASE)
-    DELTA_ROWS_CASE(64, 4) DELTA_ROWS_CASE(256, 4) DELTA_ROWS_CASE(1024, 4)
+    DELTA_ROWS_CASE(128, 1) DELTA_ROWS_CASE(1024, 4)
 #undef DELTA_ROWS_CASE
     default: return hipErrorInvalidValue;
   }
@@ -600,7 +615,7 @@ hipError_t launch_rows(const RmsnormParams& p, hipStream_t st) {
 
 template <typename E>
 hipError_t launch_rows_bwd(const RmsnormParams& p, hipStream_t st) {
-  const Split s = split(p.width, true);
+  const Split s = split_bwd(p.width);
   const dim3 grid((unsigned)rmsnorm_bwd_parts(p.rows, p.width));
   switch (s.lanes * 16 + s.j) {
 #define DELTA_ROWS_CASE(L, J)                                                                        \
@@ -608,7 +623,7 @@ hipError_t launch_rows_bwd(const RmsnormParams& p, hipStream_t st) {
     hipLaunchKernelGGL((rmsnorm_bwd_kernel<E, L, J>), grid, dim3(bwd_threads(L)), 0, st, p);             \
     break;
     DELTA_ROWS_CASES(DELTA_ROWS_CASE)
-    DELTA_ROWS_CASE(128, 2) DELTA_ROWS_CASE(512, 2)
+    DELTA_ROWS_CASE(64, 2)
 #undef DELTA_ROWS_CASE
 #undef DELTA_ROWS_CASES
     case 0: hipLaunchKernelGGL((rmsnorm_bwd_wide_kernel<E>), grid, dim3(1024), 0, st, p); break;
@@ -632,8 +647,8 @@ hipError_t launch_rmsnorm(const RmsnormParams& p, bool bf16_in, hipStream_t st) 
 // As many as the card holds: 2 workgroups of 512 threads on each of 256 compute units, or 1 of 1024.  16K
 // rows of 2048 channels, us: 256 threads 57.5, 512 56.4, 1024 61.8; twice the workgroups 60, 64.
 int rmsnorm_bwd_parts(long rows, int width) {
-  const Split s = split(width, true);
-  return (int)workgroups(rows, s, 512, s.lanes == 1024 || s.lanes == 0 ? 256 : 512);
+  const Split s = split_bwd(width);
+  return (int)workgroups(rows, s, bwd_threads(s.lanes));
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsnormParams& p, bool bf16_in, hipStream_t st) {

@@ -749,3 +749,12 @@ def test_clip_outputs_by_name():
     mine = [torch.zeros_like(g) for g in (gs["w"], gs["u"])]
     D.clip_grads([gs["w"], None, gs["u"]], 1e9, out=[mine[0], torch.zeros(64, device="cuda"), mine[1]])
     assert torch.equal(mine[0], gs["w"]) and torch.equal(mine[1], gs["u"])
+
+
+@pytest.mark.parametrize("N,W", [(4103, 1003), (2051, 2048), (1030, 2056), (1029, 4096), (2050, 4104)])
+def test_rmsnorm_more_rows_than_workgroups(N, W):
+    """Rows of several wavefronts, more than one launch has workgroups for: these walk over them."""
+    test_rmsnorm(N, W, "bf16")
+    for group in (0, 128):
+        test_rmsnorm_quant(N, W, "bf16", group)
+    test_rmsnorm_bwd(N, W, "bf16")
