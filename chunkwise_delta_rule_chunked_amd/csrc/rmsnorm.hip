@@ -9,10 +9,10 @@
 // at any element: the same wide accesses at element alignment, which gfx950 allows, with the row's last
 // vector in three pieces.  Rows past 32768 channels (backward 16384) take a kernel that reads them twice.
 //
-// Measured, bf16: 16384 rows of 2048, forward 48 us (5.6 TB/s), with y in 8 bits 46, backward 54 us (5.0
-// TB/s; 5 of it for adding up dweight's parts); 65536 x 512 forward 43.6 us (6.2 TB/s); 32768 x 1003
-// forward 59 us (4.5 TB/s: accesses that cross their natural alignment), x 1008 50 us; 64 x 2048 in 8 bits
-// 5.8 us, the latency of two rounds to memory and a launch.  Non-temporal stores made no difference to 3% worse.
+// Measured, bf16: 16384 rows of 2048, forward 44 us (6.1 TB/s), with y in 8 bits 44, backward 51 us (5.3
+// TB/s; 5 of it for adding up dweight's parts); 65536 x 512 forward 43.4 us (6.2 TB/s); 32768 x 1003
+// forward 51 us (5.1 TB/s: accesses that cross their natural alignment), x 1008 47 us; 64 x 2048 in 8 bits
+// 3.3 us, the latency of two rounds to memory and a launch.  Non-temporal stores made no difference to 3% worse.
 #include <hip/hip_runtime.h>
 
 #include "block_kernels.h"
@@ -525,20 +525,23 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_wide_kernel(RmsnormParams p)
   }
 }
 
-// dweight = the sum of the parts: 16 columns and 16 lanes over the parts per workgroup.
-__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* part, int parts, int width, float* dweight) {
-  __shared__ float sums[16][17];
-  const int col = threadIdx.x % 16, k0 = threadIdx.x / 16, i = blockIdx.x * 16 + col;
+// dweight = the sum of the parts: 16 columns and 64 lanes over the parts per workgroup.
+constexpr int DW_THREADS = 1024;
+__global__ __launch_bounds__(DW_THREADS) void rmsnorm_dweight_kernel(const float* part, int parts, int width, float* dweight) {
+  __shared__ float sums[DW_THREADS / WAVE][17];
+  const int col = threadIdx.x % 16, i = blockIdx.x * 16 + col;
   float s = 0.f;
   if (i < width)
 #pragma unroll 8
-    for (int k = k0; k < parts; k += 16) s += part[(long)k * width + i];
-  sums[k0][col] = s;
+    for (int k = threadIdx.x / 16; k < parts; k += DW_THREADS / 16) s += part[(long)k * width + i];
+  s += __shfl_xor(s, 16, WAVE);
+  s += __shfl_xor(s, 32, WAVE);
+  if (threadIdx.x % WAVE < 16) sums[threadIdx.x / WAVE][col] = s;
   __syncthreads();
-  if (k0 == 0 && i < width) {
+  if (threadIdx.x < 16 && i < width) {
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += sums[k][col];
+    for (int k = 0; k < DW_THREADS / WAVE; ++k) s += sums[k][col];
     dweight[i] = s;
   }
 }
@@ -656,7 +659,7 @@ hipError_t launch_rmsnorm_bwd(const RmsnormParams& p, bool bf16_in, hipStream_t 
   if (parts > 0)
     if (const hipError_t e = bf16_in ? launch_rows_bwd<bf16>(p, st) : launch_rows_bwd<float>(p, st)) return e;
   if (!p.dweight) return hipSuccess;
-  hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((p.width + 15) / 16), dim3(256), 0, st, p.part, parts, p.width,
+  hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((p.width + 15) / 16), dim3(DW_THREADS), 0, st, p.part, parts, p.width,
                      p.dweight);
   return hipGetLastError();
 }
