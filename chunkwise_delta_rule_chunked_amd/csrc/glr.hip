@@ -153,7 +153,8 @@ __device__ inline uint64_t map_word(float A, float H) { return (uint64_t)plain_n
 
 // The state this tile starts from, for the channel of this lane (of a whole wavefront; `live`: the
 // channel exists), publishing the tile's map and the state behind it.  at: the tile's word; flag: the
-// tile's flag.
+// tile's flag.  init: the first tile's start state, which no other tile may read: where h_final is h0, the
+// chain's last tile writes over it.
 __device__ inline float chain_state(const Chain& c, long at, long stride, uint32_t* flag, int tile, bool live, float A,
                                     float H, float init) {
   if (c.tiles == 1) return init;
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
     }
     float h = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
                           chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TH,
-                          live && p.h0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
+                          live && p.h0 && tile.order == 0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       const float behind = step(sA[k][tid], h, sH[k][tid]);
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
     }
     float flow = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
                              chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TF,
-                             live && p.dh_final ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
+                             live && p.dh_final && tile.order == 0 ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
 #pragma unroll
     for (int k = NG - 1; k >= 0; --k) {
       const float behind = step(sA[k][tid], flow, sF[k][tid]);
