@@ -399,6 +399,8 @@ constexpr int bwd_threads(int lanes) { return lanes > 512 ? lanes : 512; }
 
 // Workgroup k takes rows k RPW .., then gridDim.x * RPW further on, and stores its part of dweight in
 // part[k].  Every part is the sum over a fixed set of rows in a fixed order.
+// With z = s rstd, dx = dsum + rstd (w dy - z mean(w dy z)), dweight = sum dy z: z is of order 1 whatever the
+// row's size, where rstd^3 leaves float32's range from rms 1e13 on (and below 1e-13 with eps = 0).
 template <typename E, int LANES, int J>
 __global__ __launch_bounds__(bwd_threads(LANES), 4) void rmsnorm_bwd_kernel(RmsnormParams p) {
   constexpr int T = bwd_threads(LANES), RPW = T / LANES, COLS = LANES * J * V;
@@ -442,16 +444,16 @@ __global__ __launch_bounds__(bwd_threads(LANES), 4) void rmsnorm_bwd_kernel(Rmsn
     }
     row_sums<LANES>(ss, dot, slot, lds);
     const float rstd = 1.f / sqrtf(ss / p.width + p.eps);
-    const float c = rstd * rstd * rstd * (dot / p.width);
+    const float c = rstd * (dot / p.width);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
       float v[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float t = rstd * d[j][e];
-        v[e] = (p.dsum ? o[j][e] : 0.f) + w[j][e] * t - s[j][e] * c;
-        if (ok) acc[j][e] += t * s[j][e];  // a missing row's rstd is infinite for eps = 0
+        const float z = s[j][e] * rstd;
+        v[e] = (p.dsum ? o[j][e] : 0.f) + rstd * (w[j][e] * d[j][e] - z * c);
+        if (ok) acc[j][e] += d[j][e] * z;  // a missing row's rstd is infinite for eps = 0
       }
       store8(static_cast<E*>(p.dx) + base + i, n, v);
       __builtin_amdgcn_sched_barrier(0);
@@ -506,7 +508,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_wide_kernel(RmsnormParams p)
       }
     }
     const float rstd = 1.f / sqrtf(row_sum<T>(ss, lds) / p.width + p.eps);
-    const float c = rstd * rstd * rstd * (row_sum<T>(dot, lds) / p.width);
+    const float c = rstd * (row_sum<T>(dot, lds) / p.width);
     for (int i = threadIdx.x * V; i < p.width; i += T * V) {
       float s[V], d[V], w[V], o[V] = {}, a[V] = {};
       load8<false>(static_cast<const E*>(p.x) + base + i, p.width - i, s);
@@ -516,8 +518,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_wide_kernel(RmsnormParams p)
       if (!first && p.dweight) load8<false>(part + i, p.width - i, a);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        o[e] = o[e] + rstd * (w[e] * d[e]) - s[e] * c;
-        a[e] += d[e] * s[e] * rstd;
+        const float z = s[e] * rstd;
+        o[e] = o[e] + rstd * (w[e] * d[e] - z * c);
+        a[e] += d[e] * z;
       }
       store8(static_cast<E*>(p.dx) + base + i, p.width - i, o);
       if (p.dweight) store8(part + i, p.width - i, a);

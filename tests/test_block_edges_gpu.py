@@ -26,3 +26,27 @@ def test_glr_in_place_equals_out_of_place(L):
         s = h0.clone()
         Oi, hi, sti = D.fwd_glr(x, g, s, input_gate="norm", h_final=s, want_states=True)
         assert hi is s and torch.equal(Oi, O) and torch.equal(s, h) and torch.equal(sti, st)
+
+
+# ---- norm backward ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [64, 1003, 2048, 16392])
+@pytest.mark.parametrize("rms,eps", [(1e14, 1e-6), (1e15, 1e-6), (1e16, 1e-6), (1e-13, 0.0), (1e-16, 0.0)])
+def test_rmsnorm_bwd_large_and_tiny_rows(rms, eps, W, dtype):
+    """rstd^3 leaves float32's range here, the gradient does not.  Half of the rows have dy along s, where the
+    two terms cancel.  Bounds as in test_rmsnorm_bwd: relative to the sum of the terms' magnitudes."""
+    N = 6
+    say("rmsnorm bwd", rms, eps, W, dtype)
+    s, dy = draw(200, (N, W), dtype), draw(201, (N, W), dtype)
+    dy[1::2] = s[1::2]
+    s = host(to_dev(s * np.float32(rms), dtype)).astype(np.float32)
+    w = (1 + 0.2 * draw(202, (W,))).astype(np.float32)
+    w[: W // 2] = 1.0
+    dx, dw = D.layer_rmsnorm_bwd(to_dev(dy, dtype), to_dev(s, dtype), to_dev(w, "f32"), eps=eps)
+    ref, rw = Bk.rmsnorm_bwd(dy, s, w, None, eps)
+    S, DY, WT = (np.abs(v.astype(np.float64)) for v in (s, dy, w))
+    r = 1 / np.sqrt(np.mean(S * S, axis=1, keepdims=True) + eps)
+    mag = r * WT * DY + S * r ** 3 * np.mean(WT * DY * S, axis=1, keepdims=True)
+    check("dx", dx, ref, (W / 64 + 24) * U * mag + half_step(ref, dtype))
+    check("dweight", dw, rw, (N + W / 64 + 24) * U * np.sum(DY * S * r, axis=0) + 1e-38)
