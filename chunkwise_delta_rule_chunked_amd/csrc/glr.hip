@@ -87,7 +87,8 @@ __device__ inline float weight(float g, float a) {
     return fabsf(g) < 0.35f ? s * g : 1.f - a;
   } else {
     const float t = g * g, s = (t * (t * (-2.f / 120) - 2.f / 6) - 2.f) * (g * a);
-    return __builtin_amdgcn_sqrtf(fmaxf(fabsf(g) < 0.25f ? s : 1.f - a * a, 0.f));
+    const float v = fabsf(g) < 0.25f ? s : 1.f - a * a;
+    return __builtin_amdgcn_sqrtf(v < 0.f ? 0.f : v);  // not fmaxf, which would hide a NaN gate
   }
 }
 
@@ -96,7 +97,7 @@ template <int GATE>
 __device__ inline float slope(float a, float w) {
   if constexpr (GATE == NONE) return 0.f;
   if constexpr (GATE == COMPLEMENT) return -a;
-  return w > 0.f ? -a * a * __builtin_amdgcn_rcpf(w) : 0.f;
+  return w == 0.f ? 0.f : -a * a * __builtin_amdgcn_rcpf(w);
 }
 
 // Four consecutive channels as they are in memory.

@@ -50,3 +50,38 @@ def test_rmsnorm_bwd_large_and_tiny_rows(rms, eps, W, dtype):
     mag = r * WT * DY + S * r ** 3 * np.mean(WT * DY * S, axis=1, keepdims=True)
     check("dx", dx, ref, (W / 64 + 24) * U * mag + half_step(ref, dtype))
     check("dweight", dw, rw, (N + W / 64 + 24) * U * np.sum(DY * S * r, axis=0) + 1e-38)
+
+
+# ---- NaN gates --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [20, 50, 300])
+@pytest.mark.parametrize("gate", GATES)
+def test_glr_nan_gate_reaches_everything_it_touches(gate, L, dtype):
+    """One log gate is NaN: outputs and gradients are NaN exactly where the formulas' are, and every other
+    channel keeps its bits.  Lane and tile routes."""
+    B, H, d, t, ch = 1, 2, 16, 13, 5
+    say("nan gate", gate, L, dtype)
+    x, g, h0, dO, dh = draw(210, (B, L, H, d), dtype), log_gates(211, (B, L, H, d)), draw(212, (B, H, d)), \
+        draw(213, (B, L, H, d), dtype), draw(214, (B, H, d))
+    bad = g.copy()
+    bad[0, t, 1, ch] = np.nan
+
+    def both(gates):
+        xd, gd = to_dev(x, dtype), to_dev(gates, "f32")
+        O, h, st = D.fwd_glr(xd, gd, to_dev(h0, "f32"), input_gate=gate, want_states=True)
+        G = D.bwd_glr(xd, gd, st, to_dev(dO, dtype), to_dev(dh, "f32"), input_gate=gate)
+        return {"O": O, "h": h, "states": st, **G}
+
+    got, want = both(bad), both(g)
+    O, h, st = Bk.glr_fwd(x, bad, h0, gate)
+    dx, dg, dh0 = Bk.glr_bwd(x, bad, h0, dO, dh, gate)
+    for n, r in {"O": O, "h": h, "states": st, "dx": dx, "dg_log": dg, "dh0": dh0}.items():
+        assert np.array_equal(np.isnan(host(got[n])), np.isnan(r)), n
+        a, b = got[n].clone(), want[n].clone()
+        a[..., 1, ch], b[..., 1, ch] = 0, 0
+        assert torch.equal(a, b), n
+    assert torch.isnan(got["dx"][0, t, 1, ch]) == (gate != "none") and torch.isnan(got["dg_log"][0, t, 1, ch])
+    s = to_dev(h0, "f32")
+    o = D.decode_glr(to_dev(x[:, t:t + 1], dtype), to_dev(bad[:, t:t + 1], "f32"), s, input_gate=gate)
+    assert torch.isnan(o).sum() == 1 and torch.isnan(s).sum() == 1 and torch.isnan(s[0, 1, ch])
