@@ -23,7 +23,7 @@ namespace {
 
 constexpr int V = 8;  // channels of a vector
 constexpr float E4M3_MAX = 448.f;
-constexpr float AMAX_MIN = 0x1p-100f;  // below it a group counts as zeros: 448 / max stays finite
+constexpr float AMAX_MIN = 0x1p-100f;  // below it a group counts as zeros: 448 / max|z w| stays finite
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // at any element
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
@@ -196,17 +196,28 @@ __device__ inline void row_sums(float& x, float& y, int slot, float (*lds)[W]) {
   }
 }
 
-// How a group's s w, the largest of which is `most` in magnitude, become 8 bits.  rstd cancels from
-// y / scale = 448 s w / max|s w|, and with it a rounding of each value; where that quotient could overflow
-// (`most` tiny, rstd large) it stays in.
+// The two parts of a row's rstd in the 8-bit form: a power of two `up`, with which s becomes z of order 1
+// (exactly), and the rest m in [1, 2).  The products z w are within a factor of 2 of y, so they leave float32's
+// range only where y does, which s w would not.  An rstd that is 0, infinite or NaN is all in m.
+struct Rstd {
+  float up, m;
+  __device__ inline explicit Rstd(float rstd) {
+    const unsigned b = __builtin_bit_cast(unsigned, rstd), e = b & 0x7f800000u;
+    const bool plain = e != 0 && e != 0x7f800000u;
+    up = plain ? __builtin_bit_cast(float, e) : 1.f;
+    m = plain ? __builtin_bit_cast(float, (b & 0x007fffffu) | 0x3f800000u) : rstd;
+  }
+};
+
+// How a group's z w, the largest of which is `most` in magnitude, become 8 bits.  m cancels from
+// y / scale = 448 z w / max|z w|.
 struct Quant {
-  float scale, f1, f2;  // the value is (s w) f1 f2
-  __device__ inline Quant(float most, float rstd) {
-    const float amax = most * rstd;
-    const bool zero = amax < AMAX_MIN, tiny = most < AMAX_MIN;
+  float scale, f;  // the value is (z w) f
+  __device__ inline Quant(float most, float m) {
+    const float amax = most * m;
+    const bool zero = amax < AMAX_MIN;
     scale = zero ? 0.f : amax / E4M3_MAX;
-    f1 = tiny ? rstd : 1.f;
-    f2 = zero ? 0.f : E4M3_MAX / (tiny ? amax : most);
+    f = zero ? 0.f : E4M3_MAX / most;
   }
 };
 
@@ -248,10 +259,11 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p
       for (int e = 0; e < V; ++e) ss += s[j][e] * s[j][e];
     }
     const float rstd = 1.f / sqrtf(row_sum<LANES>(ss, lds) / p.width + p.eps);
+    const Rstd r(rstd);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[j][e] = (QUANT ? s[j][e] : s[j][e] * rstd) * w[j][e];
+      for (int e = 0; e < V; ++e) s[j][e] = s[j][e] * (QUANT ? r.up : rstd) * w[j][e];
     if constexpr (QUANT == 0) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -281,9 +293,9 @@ __global__ __launch_bounds__(threads(LANES)) void rmsnorm_kernel(RmsnormParams p
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
-        const Quant q(__builtin_bit_cast(float, m[QUANT == 1 ? 0 : j]), rstd);
+        const Quant q(__builtin_bit_cast(float, m[QUANT == 1 ? 0 : j]), r.m);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[j][e] = s[j][e] * q.f1 * q.f2;
+        for (int e = 0; e < V; ++e) s[j][e] *= q.f;
         store8_e4m3(p.y8 + base + i, n, s[j]);
         if (n > 0 && i % p.group == 0) p.scale[row * groups + i / p.group] = q.scale;
       }
@@ -315,13 +327,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
     for (int e = 0; e < V; ++e) ss += s[e] * s[e];
   }
   const float rstd = 1.f / sqrtf(row_sum<T>(ss, lds) / p.width + p.eps);
+  const Rstd r(rstd);
   const E* s0 = p.res ? sum : x;  // what this thread itself wrote
   auto normed = [&](int i, float* y) {
     float w[V];
     load8<false>(s0 + i, p.width - i, y);
     load8<false>(p.weight + i, p.width - i, w);
 #pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = (QUANT ? y[e] : y[e] * rstd) * w[e];
+    for (int e = 0; e < V; ++e) y[e] = y[e] * (QUANT ? r.up : rstd) * w[e];
   };
   const int groups = (p.width + p.group - 1) / p.group;
   unsigned all = 0;
@@ -349,9 +362,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_wide_kernel(RmsnormParams p) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o, WAVE));
       }
-      const Quant q(__builtin_bit_cast(float, m), rstd);
+      const Quant q(__builtin_bit_cast(float, m), r.m);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = y[e] * q.f1 * q.f2;
+      for (int e = 0; e < V; ++e) y[e] *= q.f;
       if (n > 0) {
         store8_e4m3(p.y8 + base + i, n, y);
         if (i % p.group == 0) p.scale[row * groups + i / p.group] = q.scale;

@@ -85,3 +85,23 @@ def test_glr_nan_gate_reaches_everything_it_touches(gate, L, dtype):
     s = to_dev(h0, "f32")
     o = D.decode_glr(to_dev(x[:, t:t + 1], dtype), to_dev(bad[:, t:t + 1], "f32"), s, input_gate=gate)
     assert torch.isnan(o).sum() == 1 and torch.isnan(s).sum() == 1 and torch.isnan(s[0, 1, ch])
+
+
+# ---- norm to 8 bits ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("W", [60, 256, 1003, 40000])
+@pytest.mark.parametrize("rms,weight,eps", [(1e16, 1e25, 1e-6), (1e-18, 1e-22, 0.0), (1e3, 1e37, 1e-6)])
+def test_rmsnorm_quant_products_past_float32(rms, weight, eps, W, group):
+    """s times the weight leaves float32's range, y does not.  Bounds as in test_rmsnorm_quant."""
+    say("quant range", rms, weight, W, group)
+    s = rms * draw(240, (5, W)).astype(np.float64)
+    s = s.astype(np.float32)
+    w = (weight * np.exp2(draw(241, (W,)).clip(-2, 2)).astype(np.float64)).astype(np.float32)
+    _, y8, sc = D.layer_rmsnorm_quant(to_dev(s, "f32"), to_dev(w, "f32"), eps=eps, group=group)
+    y = Bk.rmsnorm(s, w, eps)
+    scale, _ = Bk.quantise(y, group)
+    rel = (W / 64 + 18) * U
+    check("scale", sc, scale, rel * scale + 1e-38)
+    full = np.repeat(host(sc), group or W, axis=1)[:, :W]
+    check("y8 * scale", host(y8) * full, y, np.abs(y) * (2.0 ** -4 + 2 * rel) + full * 2.0 ** -10 + 1e-38)
