@@ -35,6 +35,8 @@
 //
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "block_kernels.h"
 #include "common.h"
 
@@ -57,13 +59,47 @@ __device__ inline float times(float a, float b) {
 }
 __device__ inline float step(float a, float h, float u) { return reset(a) ? u : a * h + u; }
 
-// The same for the tokens a lane holds.  RESETS: whether a reset is among the wavefront's; without one
-// (nearly always) the marks cost nothing.
+// Gates above 1.  With factors up to GROWS the products of a tile's 128 stay below 2^75.  With larger ones a
+// product can leave float32's range where no state does (a small or zero state, or decay behind it).  A map's
+// factor of 2^127 or more is then held as minus its value times 2^-192; 2^319 stands for all above, where any state
+// but 0 overflows.  Products are formed in 64 bits.  Ordinary factors give the same bits either way, so it does not
+// matter to which of a chain's folds such a factor came too.  What this costs calls without such gates: up to 1.5%
+// on the shortest chains, 0.3% on 64K tokens.
+constexpr float GROWS = 1.5f;
+__device__ inline double whole(float a) { return a < 0.f ? -0x1p192 * a : a; }
+__device__ inline float factor_of(double d) {
+  if (d >= 0x1p127) return -(float)(d < 0x1p319 ? d * 0x1p-192 : 0x1p127);
+  return d != d ? __builtin_nanf("") : (float)d;
+}
+template <bool GROWN>
+struct Maps {
+  __device__ static inline float product(float a, float b) {
+    if constexpr (!GROWN) return times(a, b);
+    return (a == 0.f && reset(a)) || (b == 0.f && reset(b)) ? -0.f : factor_of(whole(a) * whole(b));
+  }
+  __device__ static inline float next(float a, float h, float u) {
+    if constexpr (!GROWN) return step(a, h, u);
+    return a < 0.f ? (float)__builtin_fma(whole(a), (double)h, (double)u) : step(a, h, u);
+  }
+};
+
+// The same for the tokens a lane holds.  RESETS: whether a reset, or a factor above GROWS, is among the
+// wavefront's; without one (nearly always) the marks cost nothing.
 template <bool RESETS>
 struct Gates {
   __device__ static inline float marked(float a) { return RESETS ? mark(a) : a; }
-  __device__ static inline float product(float a, float b) { return RESETS ? times(a, b) : a * b; }
   __device__ static inline float next(float a, float h, float u) { return RESETS ? step(a, h, u) : a * h + u; }
+  // the product of the factors
+  struct Product {
+    typename std::conditional<RESETS, double, float>::type v = 1;
+    bool forgets = false;
+    __device__ inline void by(float a) {
+      forgets = forgets || (RESETS && reset(a));
+      v *= a;
+      if (RESETS && v > 0x1p400) v = 0x1p400;
+    }
+    __device__ inline float get() const { return !RESETS ? (float)v : forgets ? -0.f : factor_of(v); }
+  };
   // what multiplies into a gradient: nothing at a reset, whatever v is
   __device__ static inline float pass(float a, float v) { return RESETS && reset(a) ? 0.f : v; }
 };
@@ -88,7 +124,7 @@ __device__ inline float weight(float g, float a) {
   } else {
     const float t = g * g, s = (t * (t * (-2.f / 120) - 2.f / 6) - 2.f) * (g * a);
     const float v = fabsf(g) < 0.25f ? s : 1.f - a * a;
-    return __builtin_amdgcn_sqrtf(v < 0.f ? 0.f : v);  // not fmaxf, which would hide a NaN gate
+    return __builtin_amdgcn_sqrtf(__builtin_elementwise_maximum(v, 0.f));  // a NaN gate's is NaN, as fmaxf's is not
   }
 }
 
@@ -142,7 +178,7 @@ struct Chain {
   int tiles;       // per sequence
   int row;
 };
-enum : uint32_t { HAS_MAP = 1, HAS_STATE = 2 };
+enum : uint32_t { HAS_MAP = 1, HAS_STATE = 2, HAS_GROWN_MAP = 3 };  // grown: with factors that Maps<true> takes
 
 __device__ inline unsigned plain_nan(float x) { return x != x ? (bits(x) & 0x80000000u) | 0x7fc00000u : bits(x); }
 template <typename T>
@@ -152,25 +188,35 @@ __device__ inline T look(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELA
 
 __device__ inline uint64_t map_word(float A, float H) { return (uint64_t)plain_nan(H) << 32 | plain_nan(A); }
 
+template <bool GROWN>
+__device__ inline float fold_words(const uint64_t* m, int last, float h) {
+#pragma unroll
+  for (int i = 0; i < BATCH; ++i)
+    if (i <= last) h = Maps<GROWN>::next(from_bits((unsigned)m[i]), h, from_bits((unsigned)(m[i] >> 32)));
+  return h;
+}
+
 // The state this tile starts from, for the channel of this lane (of a whole wavefront; `live`: the
-// channel exists), publishing the tile's map and the state behind it.  at: the tile's word; flag: the
-// tile's flag.  init: the first tile's start state, which no other tile may read: where h_final is h0, the
-// chain's last tile writes over it.
-__device__ inline float chain_state(const Chain& c, long at, long stride, uint32_t* flag, int tile, bool live, float A,
-                                    float H, float init) {
+// channel exists), publishing the tile's map and the state behind it.  grown: a factor of the tile is above
+// GROWS.  at: the tile's word; flag: the tile's flag.  init: the first tile's start state, which no other tile may
+// read: where h_final is h0, the chain's last tile writes over it.
+__device__ inline float chain_state(const Chain& c, long at, long stride, uint32_t* flag, int tile, bool live, bool grown,
+                                    float A, float H, float init) {
   if (c.tiles == 1) return init;
   const int lane = threadIdx.x % WAVE;
   float h = init;
   if (tile > 0) {
     if (live) publish(c.map + at, map_word(A, H));
-    if (lane == 0) publish(flag, (uint32_t)HAS_MAP);
+    if (lane == 0) publish(flag, (uint32_t)(grown ? HAS_GROWN_MAP : HAS_MAP));
     int polls = 0, found = -1;  // the nearest predecessor (0: the one before) with a state, and maps behind it
+    bool any_grown = false;     // among those maps
     for (; polls < POLLS; ++polls) {
       const uint32_t f = lane < tile ? look(flag - 1 - lane) : 0;
-      const uint64_t states = __ballot(f == HAS_STATE), maps = __ballot(f == HAS_STATE || f == HAS_MAP);
+      const uint64_t states = __ballot(f == HAS_STATE), words = __ballot(f - 1u < 3u);
       if (states) {
         const int k = __builtin_ctzll(states);
-        if ((~maps & ((1ull << k) - 1)) == 0) {
+        if ((~words & ((1ull << k) - 1)) == 0) {
+          any_grown = __ballot(f == HAS_GROWN_MAP) & ((1ull << k) - 1);
           found = k;
           break;
         }
@@ -187,17 +233,16 @@ __device__ inline float chain_state(const Chain& c, long at, long stride, uint32
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) there = there && m[i] != ~0ull;
         // the flag may be seen before the state: what the fold starts from has to forget what was before
-        if (k0 == found) there = there && (!live || reset(from_bits((unsigned)m[0])));
+        if (k0 == found) there = there && (!live || (unsigned)m[0] == 0x80000000u);
         if (__all(there)) break;
       }
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i)
-        if (i <= k0) h = step(from_bits((unsigned)m[i]), h, from_bits((unsigned)(m[i] >> 32)));
+      if (__builtin_expect(any_grown, 0)) h = fold_words<true>(m, k0, h);
+      else h = fold_words<false>(m, k0, h);
     }
     if (polls >= POLLS) h = __builtin_nanf("");
   }
   if (tile + 1 < c.tiles) {
-    if (live) publish(c.map + at, map_word(-0.f, step(A, h, H)));
+    if (live) publish(c.map + at, map_word(-0.f, __builtin_expect(grown, 0) ? Maps<true>::next(A, h, H) : step(A, h, H)));
     if (lane == 0) publish(flag, (uint32_t)HAS_STATE);
   }
   return h;
@@ -290,10 +335,15 @@ struct Tile {
 };
 
 // a <- the gates' factors, w <- their weights (FOLD: times the inputs); whether one of the wavefront's
-// gates is a reset.
-template <int TPL, int GATE, bool FOLD, typename R>
-__device__ inline bool weigh(const floatx4* rg, const R* rx, float (*a)[4], float (*w)[4]) {
-  float m = 1.f;
+// factors is a reset or above GROWS, and the lane's largest.  PIN: the weights are made here and now; left to itself the compiler
+// holds what their roots are made from for many tokens (172 registers for 115).
+struct Seen {
+  bool special;
+  float most;
+};
+template <int TPL, int GATE, bool FOLD, bool PIN = false, typename R>
+__device__ inline Seen weigh(const floatx4* rg, const R* rx, float (*a)[4], float (*w)[4]) {
+  float least = 1.f, most = 1.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j) {
     float g[4], x[4];
@@ -302,29 +352,63 @@ __device__ inline bool weigh(const floatx4* rg, const R* rx, float (*a)[4], floa
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = factor(g[e]);
-      m = fminf(m, a[j][e]);
+      least = fminf(least, a[j][e]);
+      most = fmaxf(most, a[j][e]);
       w[j][e] = weight<GATE>(g[e], a[j][e]);
       if (FOLD) w[j][e] *= x[e];
+      if (PIN) asm volatile("" : "+v"(w[j][e]));
     }
     stretch(j, 2);
   }
-  return __any(m == 0.f);
+  return {(bool)__any(least == 0.f || most > GROWS), most};
+}
+
+// The groups' maps of a channel, from the first to the last (BACK: from the last to the first): the tile's, and the
+// state each group starts from in the place of its H; what is behind the last comes back.
+template <bool GROWN, bool BACK>
+__device__ inline void fold_groups(const float (*sA)[CC], const float (*sH)[CC], int ch, float& A, float& H) {
+  constexpr int UNROLL = GROWN ? 1 : NG;
+  A = 1.f, H = 0.f;
+#pragma unroll UNROLL
+  for (int i = 0; i < NG; ++i) {
+    const int k = BACK ? NG - 1 - i : i;
+    H = Maps<GROWN>::next(sA[k][ch], H, sH[k][ch]);
+    A = Maps<GROWN>::product(A, sA[k][ch]);
+    stretch(i, 4);
+  }
+  if constexpr (!GROWN) A = reset(A) ? -0.f : A;
+}
+template <bool GROWN, bool BACK, int GROUPS>
+__device__ inline float start_groups(const float (*sA)[CC], float (*sH)[CC], int ch, int first, float h) {
+  constexpr int UNROLL = GROWN ? 1 : GROUPS;
+#pragma unroll UNROLL
+  for (int i = 0; i < GROUPS; ++i) {
+    const int k = BACK ? first + GROUPS - 1 - i : first + i;
+    const float behind = Maps<GROWN>::next(sA[k][ch], h, sH[k][ch]);
+    sH[k][ch] = h;
+    h = behind;
+    stretch(i, 4);
+  }
+  return h;
 }
 
 // The group's map.
 template <int TPL, bool RESETS>
 __device__ inline void fwd_map(float (*a)[4], const float (*u)[4], float* A, float* H) {
   typedef Gates<RESETS> G;
+  typename G::Product P[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = 0.f;
+  for (int e = 0; e < 4; ++e) H[e] = 0.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = G::marked(a[j][e]);
-      A[e] = G::product(A[e], a[j][e]);
+      P[e].by(a[j][e]);
       H[e] = G::next(a[j][e], H[e], u[j][e]);
     }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) A[e] = P[e].get();
 }
 
 // Outputs are stored non-temporally (as the inputs are loaded), so that what streams through does not push
@@ -355,48 +439,44 @@ __device__ inline void fwd_out(const float (*a)[4], const float (*u)[4], floatx4
 template <typename E, int GATE, int TPL>
 __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
   __shared__ float sA[NG][CC], sH[NG][CC];  // the groups' maps; then sH the groups' start states
-  __shared__ int taken;
+  __shared__ int taken, grows;
   const Jobs jobs(p, chain);
   const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
-  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x));
+  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x)), grows = 0;
   barrier_lds();
   Tile<TPL> tile;
   tile.set(p, chain, jobs, blockIdx.x, __builtin_amdgcn_readfirstlane(taken), false);
   if (tile.none) return;
   float a[TPL][4], u[TPL][4], A[4], H[4];
-  bool resets;
+  Seen seen;
   {
     floatx4 rg[TPL];
     raw4<E> rx[TPL];
     load_tokens<TPL>(p.g + tile.base, tile.w, rg);
     load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
-    resets = weigh<TPL, GATE, true>(rg, rx, a, u);
+    seen = weigh<TPL, GATE, true, GATE == NORM>(rg, rx, a, u);
   }
-  if (resets) fwd_map<TPL, true>(a, u, A, H);
-  else fwd_map<TPL, false>(a, u, A, H);
+  if (seen.special) {
+    if (seen.most > GROWS) grows = 1;
+    fwd_map<TPL, true>(a, u, A, H);
+  } else {
+    fwd_map<TPL, false>(a, u, A, H);
+  }
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   barrier_lds();
   if (tid < CC) {
     const int ch = tile.c0 + tid;
     const bool live = ch < p.D;
-    float TA = 1.f, TH = 0.f;
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      TH = step(sA[k][tid], TH, sH[k][tid]);
-      TA = times(TA, sA[k][tid]);
-      stretch(k, 4);
-    }
+    const bool grown = __builtin_amdgcn_readfirstlane(grows);
+    float TA, TH;
+    fold_groups<false, false>(sA, sH, tid, TA, TH);
+    if (__builtin_expect(grown, 0)) fold_groups<true, false>(sA, sH, tid, TA, TH);
     float h = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                          chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TH,
+                          chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, grown, TA, TH,
                           live && p.h0 && tile.order == 0 ? p.h0[(long)tile.b * p.D + ch] : 0.f);
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      const float behind = step(sA[k][tid], h, sH[k][tid]);
-      sH[k][tid] = h;
-      h = behind;
-      stretch(k, 4);
-    }
+    if (__builtin_expect(grown, 0)) h = start_groups<true, false, NG>(sA, sH, tid, 0, h);
+    else h = start_groups<false, false, NG>(sA, sH, tid, 0, h);
     if (live && p.h_final && tile.order == chain.tiles - 1) p.h_final[(long)tile.b * p.D + ch] = h;
   }
   barrier_lds();
@@ -410,7 +490,7 @@ __global__ __launch_bounds__(WG) void glr_fwd_kernel(GlrParams p, Chain chain) {
   }
   E* out = static_cast<E*>(p.O) + tile.base;
   const int stores = tile.w.inside ? TPL : have;
-  if (resets) fwd_out<TPL, true>(a, u, h, out, tile.w, stores);
+  if (seen.special) fwd_out<TPL, true>(a, u, h, out, tile.w, stores);
   else fwd_out<TPL, false>(a, u, h, out, tile.w, stores);
 }
 
@@ -422,8 +502,9 @@ template <int TPL, bool RESETS, typename R>
 __device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, const R* rd, float* A, float* H,
                                float* F) {
   typedef Gates<RESETS> G;
+  typename G::Product P[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) A[e] = 1.f, H[e] = F[e] = 0.f;
+  for (int e = 0; e < 4; ++e) H[e] = F[e] = 0.f;
 #pragma unroll
   for (int j = 0; j < TPL; ++j) {
     float x[4];
@@ -431,11 +512,13 @@ __device__ inline void bwd_map(float (*a)[4], const float (*w)[4], const R* rx, 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[j][e] = G::marked(a[j][e]);
-      A[e] = G::product(A[e], a[j][e]);
+      P[e].by(a[j][e]);
       H[e] = G::next(a[j][e], H[e], w[j][e] * x[e]);
     }
     stretch(j, 4);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) A[e] = P[e].get();
 #pragma unroll
   for (int j = TPL - 1; j >= 0; --j) {
     float d[4];
@@ -487,10 +570,10 @@ template <typename E, int GATE>
 __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
   constexpr int TPL = TPL_BWD, GPC = GLR_CHUNK / TPL;  // groups per kept state
   __shared__ float sA[NG][CC], sH[NG][CC], sF[NG][CC];
-  __shared__ int taken;
+  __shared__ int taken, grows;
   const Jobs jobs(p, chain);
   const int tid = threadIdx.x, grp = tid / LPR, col = tid % LPR * 4;
-  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x));
+  if (tid == 0) taken = take_tile(chain, jobs.chain(blockIdx.x)), grows = 0;
   barrier_lds();
   Tile<TPL> tile;
   tile.set(p, chain, jobs, blockIdx.x, __builtin_amdgcn_readfirstlane(taken), true);
@@ -501,9 +584,13 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
   load_tokens<TPL>(static_cast<const E*>(p.x) + tile.base, tile.w, rx);
   load_tokens<TPL>(static_cast<const E*>(p.dO) + tile.base, tile.w, rd);
   float a[TPL][4], w[TPL][4], A[4], H[4], F[4];
-  const bool resets = weigh<TPL, GATE, false>(rg, rx, a, w);
-  if (resets) bwd_map<TPL, true>(a, w, rx, rd, A, H, F);
-  else bwd_map<TPL, false>(a, w, rx, rd, A, H, F);
+  const Seen seen = weigh<TPL, GATE, false>(rg, rx, a, w);
+  if (seen.special) {
+    if (seen.most > GROWS) grows = 1;
+    bwd_map<TPL, true>(a, w, rx, rd, A, H, F);
+  } else {
+    bwd_map<TPL, false>(a, w, rx, rd, A, H, F);
+  }
   *reinterpret_cast<floatx4*>(&sA[grp][col]) = floatx4{A[0], A[1], A[2], A[3]};
   *reinterpret_cast<floatx4*>(&sH[grp][col]) = floatx4{H[0], H[1], H[2], H[3]};
   *reinterpret_cast<floatx4*>(&sF[grp][col]) = floatx4{F[0], F[1], F[2], F[3]};
@@ -517,34 +604,20 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
       const int chunk = tile.tile0 / GLR_CHUNK + n;
       start[n] = live && chunk < nc ? p.states[((long)tile.b * nc + chunk) * p.D + ch] : 0.f;
     }
-    float TA = 1.f, TF = 0.f;
-#pragma unroll
-    for (int k = NG - 1; k >= 0; --k) {
-      TF = step(sA[k][tid], TF, sF[k][tid]);
-      TA = times(TA, sA[k][tid]);
-      stretch(k, 4);
-    }
+    const bool grown = __builtin_amdgcn_readfirstlane(grows);
+    float TA, TF;
+    fold_groups<false, true>(sA, sF, tid, TA, TF);
+    if (__builtin_expect(grown, 0)) fold_groups<true, true>(sA, sF, tid, TA, TF);
     float flow = chain_state(chain, ((long)tile.b * chain.tiles + tile.order) * p.D + ch, p.D,
-                             chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, TA, TF,
+                             chain.flag + (long)tile.chain * chain.row + 1 + tile.order, tile.order, live, grown, TA, TF,
                              live && p.dh_final && tile.order == 0 ? p.dh_final[(long)tile.b * p.D + ch] : 0.f);
-#pragma unroll
-    for (int k = NG - 1; k >= 0; --k) {
-      const float behind = step(sA[k][tid], flow, sF[k][tid]);
-      sF[k][tid] = flow;
-      flow = behind;
-      stretch(k, 4);
-    }
+    if (__builtin_expect(grown, 0)) flow = start_groups<true, true, NG>(sA, sF, tid, 0, flow);
+    else flow = start_groups<false, true, NG>(sA, sF, tid, 0, flow);
     if (live && p.dh0 && tile.order == chain.tiles - 1) p.dh0[(long)tile.b * p.D + ch] = flow;
 #pragma unroll
     for (int n = 0; n < NG / GPC; ++n) {
-      float h = start[n];
-#pragma unroll
-      for (int k = n * GPC; k < (n + 1) * GPC; ++k) {
-        const float behind = step(sA[k][tid], h, sH[k][tid]);
-        sH[k][tid] = h;
-        h = behind;
-        stretch(k, 4);
-      }
+      if (__builtin_expect(grown, 0)) start_groups<true, false, GPC>(sA, sH, tid, n * GPC, start[n]);
+      else start_groups<false, false, GPC>(sA, sH, tid, n * GPC, start[n]);
     }
   }
   barrier_lds();
@@ -556,7 +629,7 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
   for (int j = 0; j < TPL; ++j) again(rx[j]), again(rd[j]);
   float* dx = p.dx + tile.base;
   float* dg = p.dg + tile.base;
-  if (resets) bwd_out<TPL, GATE, true>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
+  if (seen.special) bwd_out<TPL, GATE, true>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
   else bwd_out<TPL, GATE, false>(a, w, rx, rd, tile.w, h, flow, dx, dg, stores);
 }
 

@@ -37,7 +37,9 @@ enum {
  *     a_t = exp(g_t),   h_t = a_t h_{t-1} + w_t x_t,   o_t = h_t
  *
  * the diagonal counterpart of the delta rule's matrix state, with the same layout, log gates and
- * float32 state.  g_t <= 0 is expected (a positive value is computed as given); g_t = -inf, or any
+ * float32 state.  g_t <= 0 is expected; a positive value is computed as given, also where a product
+ * of several a_t, which no state takes part in, would leave float32's range.  What such a product of up
+ * to 128 factors takes below 2^-126 of its value counts as 0.  g_t = -inf, or any
  * g_t whose exp is 0 in float32 (below about -87), is the hard reset: h_t = w_t x_t exactly, whatever
  * h_{t-1} holds (also infinities and NaN), so packed sequences do not see each other.  Other NaN and
  * infinite inputs propagate.

@@ -105,3 +105,94 @@ def test_rmsnorm_quant_products_past_float32(rms, weight, eps, W, group):
     check("scale", sc, scale, rel * scale + 1e-38)
     full = np.repeat(host(sc), group or W, axis=1)[:, :W]
     check("y8 * scale", host(y8) * full, y, np.abs(y) * (2.0 ** -4 + 2 * rel) + full * 2.0 ** -10 + 1e-38)
+
+
+# ---- gates above 1 ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [20, 33, 64, 65, 128, 129, 400, 3000])
+def test_glr_growing_gates_keep_a_zero_state(L, dtype):
+    """g = +1 everywhere: a product of many gates is infinite, the state, and the gradient that flows back,
+    stay exactly 0."""
+    x, g = to_dev(draw(220, (2, L, 1, 48), dtype), dtype), torch.ones((2, L, 1, 48), device="cuda")
+    zero = torch.zeros_like(x)
+    for gate, xs in (("norm", x), ("none", zero), ("complement", zero)):
+        say("growing", L, dtype, gate)
+        O, h, st = D.fwd_glr(xs, g, input_gate=gate, want_states=True)
+        assert (O == 0).all() and (h == 0).all() and (st == 0).all()
+        G = D.bwd_glr(xs, g, st, zero, input_gate=gate)
+        assert all((G[n] == 0).all() for n in ("dx", "dg_log", "dh0"))
+
+
+def growing_bounds(x, g, h0, gate):
+    """fwd_bounds of test_block_gpu for gates on both sides of 1.  There w = 1 - a with a > 1.4 carries the
+    relative error of a, (2 + 2|g|) u, times a / (a - 1), and one rounding more."""
+    x, g = x.astype(np.float64), g.astype(np.float64)
+    w, _ = Bk.glr_weight(g, gate)
+    fin = np.where(np.isneginf(g), 0.0, g)
+    a, u, da = np.exp(g), np.abs(w * x), np.where(np.isneginf(g), 0.0, (2 + 2 * np.abs(fin)) * U)
+    dw = np.maximum(12 * U, np.where(fin > 0.35, da * a / np.maximum(a - 1, 0.4) + U, 0.0)) \
+        if gate == "complement" else np.full_like(g, 12 * U)
+    M = np.abs(h0).astype(np.float64)
+    E, Es, Ms = np.zeros_like(M), [np.zeros_like(M)], [M]
+    for t in range(x.shape[1]):
+        E = a[:, t] * (E + (da[:, t] + 2 * U) * M) + (dw[:, t] + U) * u[:, t]
+        M = a[:, t] * M + u[:, t]
+        E = E + U * M
+        Es.append(E)
+        Ms.append(M)
+    return 2 * np.stack(Es, 1), np.stack(Ms, 1), dw
+
+
+def burst(L, B, H, d, at, count, step, channels, resets=()):
+    """Slow gates, and in `channels` from token `at` on `count` gates of +step (e^135 and more together), then as
+    many that decay by e^-70 together (a product of float32's range, as the header asks).  No inputs before and in
+    the burst: the state grows from 1e-30, the gradient that flows back decays from 1 and grows again, so that both
+    stay in float32's range though the burst's product does not."""
+    g = np.maximum(log_gates(230, (B, L, H, d)), np.float32(-1e-3))
+    g[:, at:at + count, :, channels] = step
+    g[:, at + count:at + 2 * count, :, channels] = -70.0 / count
+    for t in resets:
+        g[:, t] = -np.inf
+    x, dO = draw(231, (B, L, H, d)), draw(232, (B, L, H, d))
+    x[:, :at + 2 * count], dO[:, :at + 2 * count] = 0.0, 0.0
+    return x, g, 1e-30 * draw(233, (B, H, d)), dO, draw(234, (B, H, d))
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("L,at,count,step,resets", [
+    (290, 10, 100, 1.4, ()), (700, 100, 100, 1.4, ()), (1300, 513, 100, 1.4, (300,)), (300, 1, 5, 28.0, ()),
+    (600, 250, 5, 28.0, (249, 400)), (64, 3, 5, 28.0, ()), (32, 3, 5, 28.0, ()), (3000, 1500, 300, 0.45, ()),
+])
+def test_glr_gates_above_one_as_given(L, at, count, step, resets, gate):
+    """A burst of gates above 1 whose product leaves float32's range, and as much decay behind it, computed as
+    given: within a group of tokens, a tile, across tiles; in a few channels, the others as ever."""
+    say("burst", L, at, count, step, resets, gate)
+    B, H, d = 2, 2, 48
+    x, g, h0, dO, dh = burst(L, B, H, d, at, count, step, slice(3, 40, 4), resets)
+    x[..., 0], dO[..., 0] = draw(235, (B, L, H)), draw(236, (B, L, H))       # a channel with inputs throughout
+    xd, gd = to_dev(x, "f32"), to_dev(g, "f32")
+    O, h, st = D.fwd_glr(xd, gd, to_dev(h0, "f32"), input_gate=gate, want_states=True)
+    Or, hr, sr = Bk.glr_fwd(x, g, h0, gate)
+    E, M, dw = growing_bounds(x, g, h0, gate)
+    check("O", O, Or, E[:, 1:] + U * (np.abs(Or) + E[:, 1:]) + 1e-38)
+    check("h_final", h, hr, E[:, -1] + 1e-38)
+    check("states", st, sr, E[:, :-1:64] + 1e-38)
+    G = D.bwd_glr(xd, gd, st, to_dev(dO, "f32"), to_dev(dh, "f32"), input_gate=gate)
+    dx, dg, dh0 = Bk.glr_bwd(x, g, h0, dO, dh, gate)
+    a, (w, sl) = np.exp(g.astype(np.float64)), Bk.glr_weight(g, gate)
+    nxt = np.concatenate([g[:, 1:], np.zeros_like(g[:, :1])], 1)
+    Eb, Mb, _ = growing_bounds(dO[:, ::-1], nxt[:, ::-1], dh, "none")
+    Eb, Mb = Eb[:, :0:-1], Mb[:, :0:-1]
+    q = np.abs(sl * x) + a * M[:, :-1]
+    fin = np.abs(np.where(np.isneginf(g), 0, g))
+    Eq = a * (E[:, :-1] + (4 + 2 * fin) * U * M[:, :-1]) + (24 + 4 * fin) * U * np.abs(sl * x) + 2 * U * q
+    check("dx", G["dx"], dx, np.abs(w) * Eb + (dw + 2 * U) * np.abs(w) * Mb + 1e-38)
+    check("dg_log", G["dg_log"], dg, Eq * (Mb + Eb) + Eb * q + 2 * U * q * Mb + 1e-38)
+    check("dh0", G["dh0"], dh0, a[:, 0] * Eb[:, 0] + (4 + 2 * fin[:, 0]) * U * a[:, 0] * Mb[:, 0] + 1e-38)
+    one = D.fwd_glr(xd[1:].contiguous(), gd[1:].contiguous(), to_dev(h0[1:], "f32"), input_gate=gate, want_states=True)
+    assert torch.equal(one[0], O[1:]) and torch.equal(one[1], h[1:]) and torch.equal(one[2], st[1:])
+    g1 = D.bwd_glr(xd[1:].contiguous(), gd[1:].contiguous(), one[2], to_dev(dO[1:], "f32"), to_dev(dh[1:], "f32"), input_gate=gate)
+    assert all(torch.equal(g1[n], G[n][1:]) for n in g1)
+    again = D.bwd_glr(xd, gd, st, to_dev(dO, "f32"), to_dev(dh, "f32"), input_gate=gate)
+    assert all(torch.equal(again[n], G[n]) for n in again)
