@@ -275,7 +275,7 @@ def layer_rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, group: i
 
 @functools.lru_cache(maxsize=1024)
 def rmsnorm_bwd_workspace_bytes(rows, width, dtype=BF16) -> int:
-    """Workspace of layer_rmsnorm_bwd for this shape."""
+    """Workspace of layer_rmsnorm_bwd for this shape (none is used without dweight)."""
     return _bytes("delta_layer_rmsnorm_bwd_workspace_bytes", rows, width, dtype)
 
 
@@ -293,7 +293,8 @@ def layer_rmsnorm_bwd(dy, s, weight, dsum=None, *, eps: float = 1e-6, want_dweig
         dx, pdx = _out(dx, "dx", shp, s.dtype, dev, s)
         if dweight is not None or want_dweight:
             dweight, pdw = _out(dweight, "dweight", (width,), _f32, dev, weight)
-        ws, nws, keep = _workspace(workspace, rmsnorm_bwd_workspace_bytes(rows, width, code), dev)
+        need = 0 if pdw is None else rmsnorm_bwd_workspace_bytes(rows, width, code)
+        ws, nws, keep = _workspace(workspace, need, dev)
         rc = _load().delta_layer_rmsnorm_bwd(rows, width, code, eps, pdy, ps, pw, pds, pdx, pdw, ws, nws, _raw(dev))
     _check(rc, "delta_layer_rmsnorm_bwd")
     return dx, dweight

@@ -354,8 +354,8 @@ int delta_layer_rmsnorm_bwd(int64_t rows, int32_t width, int32_t dtype, float ep
   int rc = rows_shape(rows, width, dtype, eps);
   if (rc) return rc;
   if (rows > 0 && (!dy || !s || !weight || !dx)) return DELTA_ERR_NULL_ARG;
-  size_t need = 0;
-  delta_layer_rmsnorm_bwd_workspace_bytes(rows, width, dtype, &need);
+  size_t need = 0;  // the workspace holds the parts of dweight
+  if (dweight) delta_layer_rmsnorm_bwd_workspace_bytes(rows, width, dtype, &need);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DELTA_ERR_WORKSPACE;
   const void* ptrs[] = {dy, s, weight, dsum, dx, dweight, workspace};
   for (const void* ptr : ptrs)

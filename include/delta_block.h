@@ -136,7 +136,8 @@ int delta_layer_rmsnorm_quant(int64_t rows, int32_t width, int32_t dtype, float 
  *   dsum    [rows, width] dtype      gradient reaching s from the residual path, or NULL for zero
  *   dx      [rows, width] dtype      written
  *   dweight [width] float32          written, or NULL
- *   workspace   at least delta_layer_rmsnorm_bwd_workspace_bytes bytes, 16-byte aligned
+ *   workspace   at least delta_layer_rmsnorm_bwd_workspace_bytes bytes, 16-byte aligned; not used where
+ *               dweight is NULL
  * Outputs may not overlap the inputs, each other or the workspace.
  */
 int delta_layer_rmsnorm_bwd_workspace_bytes(int64_t rows, int32_t width, int32_t dtype, size_t* bytes);
