@@ -158,8 +158,9 @@ int delta_layer_rmsnorm_bwd(int64_t rows, int32_t width, int32_t dtype, float ep
  *          No other overlap between outputs, or between an output and a gradient (a tensor may
  *          not be listed twice).
  *   max_norm >= 0, eps >= 0
- *   workspace   at least delta_grad_norm_workspace_bytes bytes (a function of the total number
- *               of elements), 16-byte aligned
+ *   workspace   at least delta_grad_norm_workspace_bytes bytes, 16-byte aligned.  The size depends on
+ *               how many tensors there are and on each one's size, not on their total alone; it never
+ *               falls when a tensor is added or one grows
  */
 int delta_grad_norm_workspace_bytes(int32_t n, const int64_t* sizes, size_t* bytes);
 int delta_grad_norm(int32_t n, const void* const* grads, const int64_t* sizes, const int32_t* dtypes, float* norm,
