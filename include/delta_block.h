@@ -67,8 +67,8 @@ int delta_fwd_glr(const delta_shape* s, int32_t input_gate, const void* x, const
  *
  *     dx_t = w_t lambda_t,  dg_t = lambda_t (a_t h_{t-1} + w'_t x_t),  dh0 = a_1 lambda_1,
  *
- * w' = dw/dg = 0, -a or -a^2 / w (taken as 0 where w = 0).  h is recomputed from `states`, so its
- * float32 values are the forward pass's own.  At a hard reset dg = 0 and nothing flows back.
+ * w' = dw/dg = 0, -a or -a^2 / w (taken as 0 where w = 0).  h is recomputed from `states` and equals
+ * the forward pass's to within float32 rounding.  At a hard reset dg = 0 and nothing flows back.
  *   x, g_log, states             as passed to and written by delta_fwd_glr
  *   dO       [B, L, H, dv]       dtype
  *   dh_final [B, H, dv]          float32   or NULL for zero
