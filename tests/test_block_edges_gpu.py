@@ -196,3 +196,39 @@ def test_glr_gates_above_one_as_given(L, at, count, step, resets, gate):
     assert all(torch.equal(g1[n], G[n][1:]) for n in g1)
     again = D.bwd_glr(xd, gd, st, to_dev(dO, "f32"), to_dev(dh, "f32"), input_gate=gate)
     assert all(torch.equal(again[n], G[n]) for n in again)
+
+
+# ---- rows that workgroups walk over -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,W", [(8195, 300), (65539, 24), (600, 8200), (515, 16392), (4099, 700)])
+def test_rmsnorm_walks_over_rows(N, W, dtype):
+    """More rows than the launch's workgroups take in one step, the last step ragged."""
+    T.test_rmsnorm(N, W, dtype)
+    if W != 16392:
+        T.test_rmsnorm_quant(N, W, dtype, 0 if dtype == "f32" else 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,W", [(300, 16392), (600, 8200), (1500, 1003), (2051, 300), (32771, 24)])
+def test_rmsnorm_bwd_walks_over_rows(N, W, dtype):
+    """The same backward, where a workgroup's part of dweight holds several rows (past 16384 channels read back
+    for each)."""
+    T.test_rmsnorm_bwd(N, W, dtype)
+
+
+def test_clip_takes_the_gradients_of_the_delta_rule():
+    """The dict that bwd returns, as it is, with and without its optional gradients, and those of the mixers
+    together."""
+    B, L, H, d = 2, 130, 2, 64
+    q, k, v = (to_dev(draw(250 + i, (B, L, H, d), "bf16"), "bf16") for i in range(3))
+    k = (k.float() / k.float().norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    beta, gl = torch.rand((B, L, H), device="cuda"), -torch.rand((B, L, H), device="cuda")
+    for kw in ({"g_log": gl}, {"want_dS0": False}):
+        G = D.bwd(q, k, v, beta, dO=v, **kw)
+        assert (G["dg_log"] is None) == ("g_log" not in kw)
+        ref, outs = Bk.clip([host(t) for t in G.values() if t is not None], 0.5, 1e-6)
+        n = D.clip_grads(G, 0.5)
+        assert abs(float(n) - ref) <= 2 * U * ref
+        for t, r in zip([t for t in G.values() if t is not None], outs):
+            check("clipped", t, r, 6 * U * np.abs(r) + 1e-38)
