@@ -753,11 +753,13 @@ const char* delta_strerror(int code) {
   switch (code) {
     case DELTA_OK: return "ok";
     case DELTA_ERR_NULL_ARG: return "a required pointer argument is NULL";
-    case DELTA_ERR_BAD_SHAPE: return "bad shape (negative size, n_h < 1, chunk not a multiple of n_h, or too large)";
+    case DELTA_ERR_BAD_SHAPE: return "bad shape (negative size, n_h < 1, chunk not a multiple of n_h, or too large), or a negative or NaN "
+             "eps or max_norm";
     case DELTA_ERR_UNSUPPORTED_DIM:
       return "unsupported dimension (dk in {16,32,64,128}, dv a multiple of 16 in [16,256], chunk in "
-             "{16,32,48,64}, dtype f32 or bf16)";
-    case DELTA_ERR_MISALIGNED: return "a tensor pointer is misaligned (16 bytes; 4 for beta and g_log)";
+             "{16,32,48,64}, dtype f32 or bf16), or an unknown input gate or scale group";
+    case DELTA_ERR_MISALIGNED: return "a tensor pointer is misaligned (16 bytes; 4 for beta, the g_log of the delta rule and scales; a "
+             "clipped gradient to its element)";
     case DELTA_ERR_WORKSPACE: return "workspace missing or smaller than the entry point's workspace size";
     case DELTA_ERR_ALIAS: return "an output overlaps an input or another output";
     case DELTA_ERR_HIP: return "HIP launch or runtime error";

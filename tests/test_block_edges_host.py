@@ -33,3 +33,10 @@ def test_clip_workspace_goes_by_the_tensors(lib):  # noqa: F811
         i = rng.randrange(len(sizes))
         more = sizes[:i] + [sizes[i] + rng.choice([1, 16384, 10 ** 7])] + sizes[i + 1:]
         assert need(sizes) <= need(more) and need(sizes) <= need(sizes + [rng.choice([0, 3, 10 ** 6])])
+
+
+def test_error_texts_name_what_these_entry_points_refuse():
+    """delta_fwd_glr refuses a g_log at 4 bytes, delta_clip_grads a negative max_norm, and so on."""
+    assert "max_norm" in D.strerror(-2) and "eps" in D.strerror(-2)
+    assert "input gate" in D.strerror(-3) and "group" in D.strerror(-3)
+    assert "g_log of the delta rule" in D.strerror(-4) and "gradient" in D.strerror(-4)
