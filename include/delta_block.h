@@ -102,7 +102,9 @@ int delta_decode_glr(const delta_shape* s, int32_t input_gate, const void* x, co
  *   sum      [rows, width] dtype, written with s; may equal x or residual exactly
  *   y        [rows, width] dtype, written
  * The norm is that of the rounded s, the value the next layer adds to and the backward pass
- * reads.  Sums in float32.  16-byte aligned pointers; no other overlap.  eps >= 0.
+ * reads.  Sums in float32, so a row's sum of squares has to be one: of rows longer than 1.8e19 (the
+ * 2-norm) it is infinite and y is 0, and with eps = 0 rows shorter than 1e-19 count as zeros.  16-byte
+ * aligned pointers; no other overlap.  eps >= 0.
  */
 int delta_layer_rmsnorm(int64_t rows, int32_t width, int32_t dtype, float eps, const void* x, const void* residual,
                         const float* weight, void* sum, void* y, void* stream);
