@@ -14,9 +14,10 @@
 //   2. one wavefront, a lane per channel, folds the 16 groups' maps into the tile's, publishes it,
 //      waits for a predecessor's state (below) and publishes the state behind the tile;
 //   3. each group runs its tokens again from its start state, writing outputs.
-// Tiles of one channel block and sequence form a chain.  A tile's predecessors publish their map as
-// soon as they have read their tokens and the state behind them as soon as they know it; a tile
-// starts from the nearest state it finds among its 64 predecessors and folds in the maps between.
+// Tiles of one channel block and sequence form a chain (a scan with decoupled look-back).  A tile's
+// predecessors publish their map as soon as they have read their tokens and the state behind them as soon as
+// they know it; a tile starts from the nearest state it finds among its 64 predecessors and folds in the maps
+// between.
 // The fold is the same left fold whichever state it starts from, so the result does not depend on
 // timing.  Waiting reads one flag per predecessor (a lane each, a cache line in all).  A flag is only a
 // hint: a published word carries its own readiness, since the workspace starts as all ones, a NaN that
@@ -25,9 +26,10 @@
 // wait ends (and is bounded besides: past POLLS polls, as can only happen if two calls share a
 // workspace, the tile goes on with NaN).
 //
-// Measured, bf16, 2048 channels: 512 sequences of 128 tokens (no chain) 169 us, 6.4 TB/s; one of 64K tokens
-// 205 us, 5.2 TB/s: clearing the workspace (5 us) and waiting along the chain cost the rest; backward
-// 2 x 8K tokens 114 us, 4.7 TB/s.  HBM traffic is what the formulas need plus 7% (forward) and 6%.
+// Measured, 2048 channels, time on the card, bf16: 512 sequences of 128 tokens (no chain) 182 us, 5.9 TB/s; one of
+// 64K tokens 205 us, 5.2 TB/s: clearing the workspace (6 us) and waiting along the chain cost the rest; backward
+// 256 x 64 tokens (no chain) 96 us, 5.7 TB/s, 2 x 8K tokens 114 us, 4.7 TB/s.  float32, 2 x 8K: forward 82 us,
+// 4.9 TB/s, backward 130 us, 5.2 TB/s.  HBM traffic is what the formulas need plus 7% (forward) and 6%.
 // Tried and slower: workgroups that stay and load their next tile while they wait (its map is published a
 // tile too late: 288 us); one counter for all chains (6 us more at the start of every call); a workgroup per
 // narrow channel block that walks the whole sequence (its scans across lanes: 23 us for 4 x 2K x 1024
@@ -48,7 +50,8 @@ enum { NONE = 0, COMPLEMENT = 1, NORM = 2 };
 __device__ inline unsigned bits(float x) { return __builtin_bit_cast(unsigned, x); }
 __device__ inline float from_bits(unsigned x) { return __builtin_bit_cast(float, x); }
 
-// a = exp(g).  a = 0 (g = -inf, or an exp that underflows) is the hard reset.  Where a product of gates
+// a = exp(g), as 2 to a rounded product: good to (2 + 2|g|) half steps of float32; subnormal results are 0.
+// a = 0 (g = -inf, or an exp that underflows) is the hard reset.  Where a product of gates
 // could underflow too, the sign bit, which no exp has (a NaN loses it here), marks a reset: products
 // carry the mark along.
 __device__ inline float factor(float g) { return fabsf(gate_exp(g)); }
@@ -107,7 +110,8 @@ struct Gates {
 // w(g), from a = exp(g).  1 - a and 1 - a^2 cancel near g = 0, where a series takes over.  For 1 - a it is
 // that of 1 - exp(g) to g^7 (|g| < 0.35: the first dropped term is below 0.35^7 / 8! = 2e-8 of the result);
 // for 1 - a^2 = -2 a sinh(g) that of sinh, two terms shorter (|g| < 0.25: 0.25^6 / 7! = 5e-8).  Beyond,
-// the difference is good to a dozen units of 2^-24.
+// the difference is good to a dozen units of 2^-24.  Root and reciprocal (in dw/dg) are the hardware's, good to a
+// unit in the last place.
 template <int GATE>
 __device__ inline float weight(float g, float a) {
   if constexpr (GATE == NONE) {
@@ -160,10 +164,10 @@ __device__ inline void unpack4(u32x2 r, float* v) {
 
 constexpr int WG = 256, LPR = 16, NG = WG / LPR, CC = 4 * LPR;  // lanes per row, groups, channels of a tile
 // Tokens of a lane.  Fewer leave registers for more wavefronts, more make fewer and shorter chains.
-// Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 265, 8: 206,
-// 16: 235; backward 4: 115, 8: 124.  Forward with clearing, 4 x 2K x 1024: 27, 20 and 21; 32 x 512 x 2048: 62,
-// 55 and 59; 3 x 1237 x 240 in float32: 11.4, 10.5 and 12.1.  A sequence of up to 64 tokens is one tile of TPL_SHORT tokens a lane
-// with none left over (256 x 64 x 2048: 47.5 us, 64 with 8).
+// Measured on one 64K x 2048 sequence (forward) and 2 x 8K x 2048 (backward), us: forward 4: 263, 8: 206,
+// 16: 228; backward 4: 113.5, 8: 119.  Forward with clearing, 4 x 2K x 1024: 27.4, 20.1 and 21.7; 32 x 512 x 2048:
+// 63.6, 55.8 and 60.5; 3 x 1237 x 240 in float32: 11.4, 10.7 and 12.4.  A sequence of up to 64 tokens is one tile of
+// TPL_SHORT tokens a lane with none left over (256 x 64 x 2048: 47.5 us, 64 with 8).
 constexpr int TPL_FWD = 8, TPL_BWD = 4, TPL_SHORT = 4;
 constexpr int BATCH = 8, POLLS = 1 << 20;
 static_assert(NG * TPL_FWD % GLR_CHUNK == 0 && NG * TPL_BWD % GLR_CHUNK == 0, "a tile starts at a kept state");
@@ -412,8 +416,9 @@ __device__ inline void fwd_map(float (*a)[4], const float (*u)[4], float* A, flo
 }
 
 // Outputs are stored non-temporally (as the inputs are loaded), so that what streams through does not push
-// out the chain's words: 512 x 128 x 2048 forward 169 us (6.4 TB/s) against 202, one 64K sequence 206
-// against 214, backward 2 x 8K 115 against 117.
+// out the chain's words: 4 x 2K x 1024 forward 20.1 us against 21.6 with ordinary stores, 512 x 32 x 2048 backward
+// 116 against 126, one 64K sequence the same.  The other way round are 512 x 128 x 2048 forward, 184 against 179,
+// and backward 2 x 8K, 113.5 against 110.
 template <typename E>
 __device__ inline void store_out(E* p, floatx4 h) {
   E v[4];
@@ -635,8 +640,9 @@ __global__ __launch_bounds__(WG) void glr_bwd_kernel(GlrParams p, Chain chain) {
 
 // Sequences of up to SHORT tokens: a lane runs its 4 channels from the first token to the last, STEP at a
 // time, where a tile would leave most of its groups without tokens.  Nothing is shared between lanes.
-// Measured at 2048 channels, bf16: 512 sequences of 32 tokens here 53 us (backward 113), of 33 tokens in
-// tiles 78 us (124); 4 of 64 tokens would take 19 us here (37), 11.5 in tiles (13).
+// Measured at 2048 channels, bf16: 512 sequences of 32 tokens here 53.5 us (backward 116), of 33 tokens in tiles
+// 77 us (132) and here 57 (125); but 256 of 64 tokens 49 us in tiles (95) and 56 here (124), 4 of 64 tokens 4.9 us
+// (6.3) and 21.6 (41).
 constexpr int SHORT = 32, STEP = 8;
 
 // Sequence, first channel and the lane's place in every [B, L, D] tensor; false past the last lane.

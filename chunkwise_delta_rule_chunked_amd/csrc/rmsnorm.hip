@@ -9,10 +9,12 @@
 // at any element: the same wide accesses at element alignment, which gfx950 allows, with the row's last
 // vector in three pieces.  Rows past 32768 channels (backward 16384) take a kernel that reads them twice.
 //
-// Measured, bf16: 16384 rows of 2048, forward 44 us (6.1 TB/s), with y in 8 bits 44, backward 51 us (5.3
-// TB/s; 5 of it for adding up dweight's parts); 65536 x 512 forward 43.4 us (6.2 TB/s); 32768 x 1003
-// forward 51 us (5.1 TB/s: accesses that cross their natural alignment), x 1008 47 us; 64 x 2048 in 8 bits
-// 3.3 us, the latency of two rounds to memory and a launch.  Non-temporal stores made no difference to 3% worse.
+// Measured, time on the card, bf16: 16384 rows of 2048, forward 44.5 us (6.0 TB/s), with y in 8 bits 43.5, backward
+// 50 to 57 us by where its tensors lie in memory (5.3 to 4.7 TB/s; 5 us for adding up dweight's parts); 65536 x 512
+// forward 44.4 us (6.0 TB/s); 32768 x 1003 forward 52 us (5.0 TB/s: accesses that cross their natural alignment),
+// x 1008 47 us; 8192 x 1024 backward 20.5 us (3.3 TB/s); 64 x 2048 in 8 bits 3.4 us, the latency of two rounds to
+// memory and a launch.  float32, 8192 x 2048: forward 51 us (5.2 TB/s), backward 55.7 us (4.8).  Non-temporal stores
+// made no difference to 3% worse.
 #include <hip/hip_runtime.h>
 
 #include "block_kernels.h"
@@ -564,12 +566,11 @@ __global__ __launch_bounds__(DW_THREADS) void rmsnorm_dweight_kernel(const float
 
 // Lanes and vectors per lane of a row (0: the kernels for any width), and the workgroups that walk over
 // the rows where those are many: as many as the card holds, 2048 lanes on each of 256 compute units.  One
-// vector per lane leaves the registers for all of them, which is worth more than rows that need no barrier;
-// measured, bf16, us, to y / to y8 per row: 16384 x 2048, 256 lanes 43.4 / 43.8, 64 lanes of 4 vectors
-// 47.2 / 45.5 (64 rows: 2.9 / 3.6, 4.3 / 5.1); 32768 x 1003, 128 lanes 51.3 / 49.6, 64 of 2 57.6 / 55.8;
-// 8192 x 4096, 512 lanes 44.1 / 44.4, 256 of 2 50.5 / 47.8.  Half or twice the workgroups: 32768 x 1003 66.7
-// and 58.3.  4096 x 8192: 512 of 2 46.0 / 50.8, 1024 lanes 43.6 / 58.4, 256 of 4 48.8 / 55.3; with half the
-// workgroups 50.2 / 46.8.
+// vector per lane leaves the registers for all of them, which is worth as much as rows that need no barrier, and
+// more for few rows; measured side by side, bf16, us, to y / to y8 per row: 16384 x 2048, 256 lanes 45.3 / 46.0, 64
+// lanes of 4 vectors 49.2 / 46.5 (64 rows: 2.9 / 3.7, 4.4 / 5.3); 32768 x 1003, 128 lanes 54.5 / 52.0, 64 of 2
+// 53.7 / 51.1, half the workgroups 68 / 71, twice 60 / 59; 8192 x 4096, 512 lanes 45.1 / 46.1, 256 of 2 46.8 / 46.8;
+// 4096 x 8192, 512 of 2 46.5 / 45.1, 1024 lanes 44.8 / 60.5, 256 of 4 49.6 / 55.6, half the workgroups 51.3 / 49.2.
 struct Split {
   int lanes, j, most;
 };
@@ -587,9 +588,9 @@ Split split(int width) {
   return {0, 0, 0};
 }
 // Backward, with its sums for dweight in registers and a part of it per workgroup to add up, 16 wavefronts
-// on a compute unit.  With dsum and dweight, us: 16384 x 2048, 256 lanes 55.0, 128 of 2 vectors 55.7 (64
-// rows: 5.8 and 6.9); 8192 x 4096, 512 lanes 56.0, 256 of 2 59.5; but 32768 x 1003, 128 lanes 73.6, 64 of 2,
-// which need no barrier, 65.8.
+// on a compute unit.  With dsum and dweight, us, side by side: 16384 x 2048, 256 lanes 56.9, 128 of 2 vectors 57.3
+// (64 rows: 5.7 and 7.0); 8192 x 4096, 512 lanes 56.9, 256 of 2 60.9; but 32768 x 1003, 128 lanes 74.4, 64 of 2,
+// which need no barrier, 66.3.
 Split split_bwd(int width) {
   if (width <= 64) return {8, 1, 512};
   if (width <= 128) return {16, 1, 512};
@@ -663,8 +664,9 @@ hipError_t launch_rmsnorm(const RmsnormParams& p, bool bf16_in, hipStream_t st) 
   return bf16_in ? launch_quant<bf16>(p, st) : launch_quant<float>(p, st);
 }
 
-// As many as the card holds: 2 workgroups of 512 threads on each of 256 compute units, or 1 of 1024.  16K
-// rows of 2048 channels, us: 256 threads 57.5, 512 56.4, 1024 61.8; twice the workgroups 60, 64.
+// As many as the card holds: 2 workgroups of 512 threads on each of 256 compute units, or 1 of 1024.  Side by
+// side, us, 16384 x 2048: 256 threads 56.5, 512 56.9, 1024 64.4, twice the workgroups 59; 32768 x 1003: 102, 66.3
+// and 71.9.
 int rmsnorm_bwd_parts(long rows, int width) {
   const Split s = split_bwd(width);
   return (int)workgroups(rows, s, bwd_threads(s.lanes));
