@@ -44,7 +44,8 @@ enum {
  * h_{t-1} holds (also infinities and NaN), so packed sequences do not see each other.  Other NaN and
  * infinite inputs propagate.
  *   s->n_h must be 1; s->dk, s->chunk and s->scale are ignored; input_gate is DELTA_GLR_*; at most
- *   2^20 channels and 2^30 tokens.  A sequence's results do not depend on the batch it is in.
+ *   2^20 channels and 2^30 tokens.  A channel's results do not depend on the batch it is in or on other
+ *   channels.
  *   x       [B, L, H, dv]       dtype
  *   g_log   [B, L, H, dv]       float32
  *   h0      [B, H, dv]          float32   initial state, or NULL for zeros

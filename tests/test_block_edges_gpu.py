@@ -198,6 +198,28 @@ def test_glr_gates_above_one_as_given(L, at, count, step, resets, gate):
     assert all(torch.equal(again[n], G[n]) for n in again)
 
 
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("L", [64, 200, 1500])
+def test_glr_channels_do_not_see_each_other(L, gate):
+    """Resets and gates above 1 in some channels leave every other channel's bits as they were."""
+    say("channels", L, gate)
+    B, H, d = 2, 1, 48
+    x, g, h0, dO, dh = draw(260, (B, L, H, d)), log_gates(261, (B, L, H, d)), draw(262, (B, H, d)), draw(263, (B, L, H, d)), \
+        draw(264, (B, H, d))
+    other = g.copy()
+    other[:, 5:60, :, 3::4] = 2.0
+    other[:, 9::7, :, 1::4] = -np.inf
+
+    def both(gates):
+        xd, gd = to_dev(x, "f32"), to_dev(gates, "f32")
+        O, h, st = D.fwd_glr(xd, gd, to_dev(h0, "f32"), input_gate=gate, want_states=True)
+        return {"O": O, "h": h, "states": st, **D.bwd_glr(xd, gd, st, to_dev(dO, "f32"), to_dev(dh, "f32"), input_gate=gate)}
+
+    a, b = both(g), both(other)
+    for n in a:
+        assert torch.equal(a[n][..., 0::2], b[n][..., 0::2]), n
+
+
 # ---- rows that workgroups walk over -----------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
