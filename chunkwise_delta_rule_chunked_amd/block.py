@@ -125,10 +125,15 @@ def _gate(name):
         raise ValueError("input_gate must be one of %s, got %r" % (", ".join(INPUT_GATES), name)) from None
 
 
-def _bytes(fn, *args):
+def _bytes_of(lib, fn, *args):
+    """The size that a workspace function of the loaded library gives."""
     n = ctypes.c_size_t(0)
-    _check(getattr(_load(), fn)(*args, ctypes.byref(n)), fn)
+    _check(getattr(lib, fn)(*args, ctypes.byref(n)), fn)
     return n.value
+
+
+def _bytes(fn, *args):
+    return _bytes_of(_load(), fn, *args)
 
 
 @functools.lru_cache(maxsize=1024)

@@ -6,6 +6,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "../../include/delta.h"
 
 namespace delta {
@@ -55,6 +57,32 @@ inline bool env_is(const char* name, const char* value) {
 }
 inline bool validate_on() { return env_is("DELTA_VALIDATE", "1"); }
 inline int launch_guard() { return env_is("DELTA_FAULT", "launch") ? DELTA_ERR_HIP : DELTA_OK; }
+
+// True if an output overlaps an input or another output.
+template <int NI, int NO>
+bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+
+// DELTA_VALIDATE: log gates finite or -inf, read back in pieces (no allocation).
+inline int validate_gates(const float* g, size_t n, hipStream_t st) {
+  constexpr size_t PIECE = 8192;
+  float buf[PIECE];
+  for (size_t i = 0; i < n; i += PIECE) {
+    const size_t m = std::min(PIECE, n - i);
+    if (hipMemcpyAsync(buf, g + i, m * 4, hipMemcpyDeviceToHost, st) != hipSuccess) return DELTA_ERR_HIP;
+    if (hipStreamSynchronize(st) != hipSuccess) return DELTA_ERR_HIP;
+    for (size_t k = 0; k < m; ++k)
+      if (buf[k] != buf[k] || buf[k] == __builtin_inff()) return DELTA_ERR_BAD_VALUE;
+  }
+  return DELTA_OK;
+}
 
 }  // namespace abi
 }  // namespace delta

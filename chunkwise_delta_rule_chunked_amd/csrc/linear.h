@@ -1,0 +1,70 @@
+// Launch interface between the linear attention entry points (linear_abi.cpp) and their kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace delta {
+
+enum { LIN_GATE_NONE = 0, LIN_GATE_TOKEN = 1, LIN_GATE_HEAD = 2 };
+
+constexpr int LIN_SLAB = 128;  // value columns of a workgroup at most: 16 for each of 8 wavefronts
+
+// Tokens of a chunk: float32 tiles are twice as large, and their products run at a sixteenth of the rate.
+constexpr int lin_chunk(bool bf16) { return bf16 ? 64 : 32; }
+
+// One operand of a chain: [B, L, heads, width], head h of the chain reading head h / (H / heads).
+struct LinRole {
+  const void* p;
+  int heads, width;
+};
+
+// One chain over chunks (linear.hip has the formulas).  The state's rows are x's and y's width, its
+// columns z's; it is stored [rows][cols], or [cols][rows] where `flip`.
+struct LinChain {
+  int B, L, H, NT, P, NS;  // chunks in all, segments, chunks of a segment
+  int run;                 // segments of this launch: P, or fewer for a summary whose end nobody asks for
+  LinRole x, y, z, w;      // w: what the hook takes the inner product with
+  const float* g;          // [B, L, H], [H] or nullptr
+  int gate;
+  float outer, inner, write;  // scales of the state's share of out, of the chunk's share, of what the state takes in
+  const float* start;      // [B, H] states before the first segment in the chain's order, or nullptr
+  float* segs;             // P > 1: [B, H, P] states, the summary's results and then each segment's start
+  double* decay;           // P > 1: [B, H, P] sums of log gates
+  float* end;              // [B, H] states behind the last segment, or nullptr
+  bool flip;
+  void* out;               // [B, L, H, z.width] in the inputs' type, or float32
+  bool out_f32;
+  float* tok;              // hook: [B, H, NT chunks] a value per token
+};
+
+// Gradients of the log gates from the per-token sums of the two backward chains.
+struct LinGates {
+  int B, L, H, C, NT, P, NS;
+  size_t state;            // elements of one state
+  const float *e, *f;      // [B, H, NT * C]
+  const float *S0, *dS0;   // [B, H] states and their gradients before the first token (S0 nullptr: no such term)
+  const float *segs, *gsegs;  // P > 1: start states of the forward and of the reverse chain
+  const float* g;
+  int gate;
+  float* dg;               // [B, L, H], or [H] through `part`
+  double* part;            // gate HEAD: [B, H, P]
+};
+
+struct LinDecode {
+  int B, H, Hk, DK, DV, gate;
+  float scale;
+  const void *q, *k, *v;
+  const float* g;
+  float* S;
+  void* O;
+};
+
+void lin_split(int B, int L, int H, int dv, bool bf16, int& NT, int& P, int& NS);
+hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int hook, hipStream_t st);
+hipError_t launch_lin_summary(const LinChain& c, bool bf16, bool reverse, hipStream_t st);
+hipError_t launch_lin_gates(const LinGates& p, hipStream_t st);
+hipError_t launch_lin_share(const float* part, void* out, long rows, int heads, int share, int width, bool bf16, hipStream_t st);
+hipError_t launch_lin_decode(const LinDecode& p, bool bf16, hipStream_t st);
+
+}  // namespace delta

@@ -1,0 +1,267 @@
+// C ABI of linear attention with a decay for each head (include/delta_linear.h): argument validation,
+// workspace layout and the order of the launches.  Nothing here throws or allocates.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "../../include/delta_linear.h"
+#include "abi_common.h"
+#include "linear.h"
+
+using delta::LinChain;
+using delta::LinDecode;
+using delta::LinGates;
+using delta::LinRole;
+using namespace delta::abi;
+
+static_assert((int)DELTA_LIN_GATE_TOKEN == (int)delta::LIN_GATE_TOKEN && (int)DELTA_LIN_GATE_HEAD == (int)delta::LIN_GATE_HEAD,
+              "gate kinds");
+
+namespace {
+
+struct Lin {
+  int B, L, H, Hk, dk, dv, gate, NT, P, NS;
+  bool bf16;
+  float scale;
+  size_t nqk, nv, ng, state;  // bytes of q, of v, of the gates, of the states
+};
+
+int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, Lin& n) {
+  const int rc = check_shape(s);
+  if (rc) return rc;
+  if (s->n_h != 1 || qk_heads < 1 || s->H % qk_heads != 0 || s->L > (1 << 30)) return DELTA_ERR_BAD_SHAPE;
+  if (gate != DELTA_LIN_GATE_NONE && gate != DELTA_LIN_GATE_TOKEN && gate != DELTA_LIN_GATE_HEAD) return DELTA_ERR_UNSUPPORTED_DIM;
+  if ((long long)s->H * (s->dk > s->dv ? s->dk : s->dv) > (1LL << 20)) return DELTA_ERR_BAD_SHAPE;
+  n.B = s->B, n.L = s->L, n.H = s->H, n.Hk = qk_heads, n.dk = s->dk, n.dv = s->dv, n.gate = gate;
+  n.bf16 = s->dtype == DELTA_BF16, n.scale = s->scale;
+  delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, n.NT, n.P, n.NS);
+  const size_t tokens = (size_t)n.B * n.L, e = esize(s->dtype);
+  n.nqk = n.H ? tokens * n.Hk * n.dk * e : 0, n.nv = tokens * n.H * n.dv * e;
+  n.ng = 4 * (gate == DELTA_LIN_GATE_TOKEN ? tokens * n.H : gate == DELTA_LIN_GATE_HEAD ? (size_t)n.H : 0);
+  n.state = (size_t)n.B * n.H * n.dk * n.dv * 4;
+  return DELTA_OK;
+}
+
+// Regions of a workspace, each on its own 256 bytes; with a null base only their total is formed.
+struct Carve {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t bytes) {
+    T* p = base && bytes ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += align_up(bytes);
+    return p;
+  }
+};
+
+struct FwdSpace {
+  float* segs;
+  double* decay;
+};
+size_t carve(const Lin& n, void* base, FwdSpace& w) {
+  Carve c{static_cast<char*>(base)};
+  const bool split = n.P > 1;
+  w.segs = c.take<float>(split ? n.state * n.P : 0);
+  w.decay = c.take<double>(split ? (size_t)n.B * n.H * n.P * 8 : 0);
+  return c.used;
+}
+
+struct BwdSpace {
+  float *segs, *gsegs;
+  double *decay, *part;
+  float *e, *f, *dS0, *shared;
+};
+size_t carve(const Lin& n, void* base, BwdSpace& w) {
+  Carve c{static_cast<char*>(base)};
+  const bool split = n.P > 1, gates = n.gate != DELTA_LIN_GATE_NONE;
+  const size_t heads = (size_t)n.B * n.H, tokens = heads * n.NT * delta::lin_chunk(n.bf16) * 4;
+  w.segs = c.take<float>(split ? n.state * n.P : 0);
+  w.gsegs = c.take<float>(split ? n.state * n.P : 0);
+  w.decay = c.take<double>(split ? heads * n.P * 8 : 0);
+  w.part = c.take<double>(n.gate == DELTA_LIN_GATE_HEAD ? heads * n.P * 8 : 0);
+  w.e = c.take<float>(gates ? tokens : 0);
+  w.f = c.take<float>(gates ? tokens : 0);
+  w.dS0 = c.take<float>(gates && n.L > 0 ? n.state : 0);  // where the caller wants none
+  w.shared = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);
+  return c.used;
+}
+
+// Pointers that have to be there, and every alignment.
+template <int N>
+int check_pointers(const void* const (&needed)[N], bool work) {
+  for (const void* p : needed)
+    if (work && !p) return DELTA_ERR_NULL_ARG;
+  return DELTA_OK;
+}
+template <int N>
+int check_aligned(const void* const (&ptrs)[N], const float* g, const float* dg) {
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return DELTA_ERR_MISALIGNED;
+  return aligned(g, 4) && aligned(dg, 4) ? DELTA_OK : DELTA_ERR_MISALIGNED;
+}
+
+Range span(const void* p, size_t bytes) { return range(p, p ? bytes : 0); }
+
+LinChain chain_of(const Lin& n, const float* g) {
+  LinChain c;
+  memset(&c, 0, sizeof(c));
+  c.B = n.B, c.L = n.L, c.H = n.H, c.NT = n.NT, c.P = n.P, c.NS = n.NS, c.run = n.P;
+  c.g = g, c.gate = n.gate;
+  c.outer = c.inner = c.write = 1.f;
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+int delta_fwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, size_t* bytes) {
+  Lin n;
+  const int rc = lin_shape(s, qk_heads, DELTA_LIN_GATE_NONE, n);
+  if (rc) return rc;
+  if (!bytes) return DELTA_ERR_NULL_ARG;
+  FwdSpace w;
+  *bytes = carve(n, nullptr, w);
+  return DELTA_OK;
+}
+
+int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const void* q, const void* k, const void* v,
+                  const float* g_log, const float* S0, void* O, float* S_final, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  Lin n;
+  int rc = lin_shape(s, qk_heads, gate, n);
+  if (rc) return rc;
+  if ((rc = check_pointers({q, k, v, O}, n.nv > 0))) return rc;
+  if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
+  FwdSpace w;
+  const size_t need = carve(n, nullptr, w);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return DELTA_ERR_WORKSPACE;
+  if ((rc = check_aligned({q, k, v, S0, O, S_final, workspace}, g_log, nullptr))) return rc;
+  const bool in_place = S0 && S0 == S_final;
+  const Range in[] = {span(q, n.nqk), span(k, n.nqk), span(v, n.nv), span(g_log, n.ng), span(in_place ? nullptr : S0, n.state)};
+  const Range out[] = {span(O, n.nv), span(S_final, n.state), span(workspace, need)};
+  if (any_overlap(in, out)) return DELTA_ERR_ALIAS;
+  if (n.state == 0 || (n.L == 0 && !S_final)) return DELTA_OK;
+  if ((rc = launch_guard())) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (g_log && validate_on() && (rc = validate_gates(g_log, n.ng / 4, st))) return rc;
+  carve(n, workspace, w);
+  LinChain c = chain_of(n, g_log);
+  c.x = LinRole{q, n.Hk, n.dk}, c.y = LinRole{k, n.Hk, n.dk}, c.z = LinRole{v, n.H, n.dv};
+  c.start = S0, c.end = S_final, c.segs = w.segs, c.decay = w.decay;
+  c.outer = c.inner = n.scale;
+  c.out = O, c.out_f32 = !n.bf16;
+  if (n.P != 1) {  // P = 0: no tokens, the state as it is
+    c.run = S_final ? n.P : n.P - 1;
+    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, false, st))) || n.P == 0) return rc;
+    c.run = n.P;
+  }
+  return hip_status(delta::launch_lin_chain(c, n.bf16, false, 0, st));
+}
+
+int delta_bwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, int32_t gate, size_t* bytes) {
+  Lin n;
+  const int rc = lin_shape(s, qk_heads, gate, n);
+  if (rc) return rc;
+  if (!bytes) return DELTA_ERR_NULL_ARG;
+  BwdSpace w;
+  *bytes = carve(n, nullptr, w);
+  return DELTA_OK;
+}
+
+int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const void* q, const void* k, const void* v,
+                  const float* g_log, const float* S0, const void* dO, const float* dS_final, void* dq, void* dk, void* dv,
+                  float* dg_log, float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+  Lin n;
+  int rc = lin_shape(s, qk_heads, gate, n);
+  if (rc) return rc;
+  if ((rc = check_pointers({q, k, v, dO, dq, dk, dv}, n.nv > 0))) return rc;
+  if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
+  if (gate == DELTA_LIN_GATE_NONE && dg_log) return DELTA_ERR_UNSUPPORTED_DIM;
+  BwdSpace w;
+  const size_t need = carve(n, nullptr, w);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return DELTA_ERR_WORKSPACE;
+  if ((rc = check_aligned({q, k, v, S0, dO, dS_final, dq, dk, dv, dS0, workspace}, g_log, dg_log))) return rc;
+  const Range in[] = {span(q, n.nqk),    span(k, n.nqk),   span(v, n.nv),           span(g_log, n.ng),
+                      span(S0, n.state), span(dO, n.nv), span(dS_final, n.state)};
+  const Range out[] = {span(dq, n.nqk), span(dk, n.nqk), span(dv, n.nv), span(dg_log, n.ng), span(dS0, n.state), span(workspace, need)};
+  if (any_overlap(in, out)) return DELTA_ERR_ALIAS;
+  const bool sum_only = gate == DELTA_LIN_GATE_HEAD && dg_log && n.H > 0;  // no tokens, and a gradient to clear
+  if ((n.state == 0 || (n.L == 0 && !dS0)) && !sum_only) return DELTA_OK;
+  if ((rc = launch_guard())) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (g_log && validate_on() && (rc = validate_gates(g_log, n.ng / 4, st))) return rc;
+  carve(n, workspace, w);
+
+  LinGates gp;
+  memset(&gp, 0, sizeof(gp));
+  gp.B = n.B, gp.L = n.L, gp.H = n.H, gp.C = delta::lin_chunk(n.bf16), gp.NT = n.NT, gp.P = n.P, gp.NS = n.NS;
+  gp.state = (size_t)n.dk * n.dv, gp.e = w.e, gp.f = w.f, gp.S0 = S0, gp.segs = w.segs, gp.gsegs = w.gsegs;
+  gp.g = g_log, gp.gate = gate, gp.dg = dg_log, gp.part = w.part;
+  if (dg_log && S0 && !dS0) dS0 = w.dS0;
+  gp.dS0 = dS0;
+  if (n.state == 0 || n.L == 0) {
+    if (n.state > 0 && dS0) {
+      LinChain c = chain_of(n, g_log);
+      c.y.width = n.dk, c.z.width = n.dv, c.run = 0, c.start = dS_final, c.end = dS0;
+      if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, true, st)))) return rc;
+    }
+    gp.B = 0;
+    return sum_only ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
+  }
+
+  const LinRole rq{q, n.Hk, n.dk}, rk{k, n.Hk, n.dk}, rv{v, n.H, n.dv}, ro{dO, n.H, n.dv};
+  const bool shared = n.H != n.Hk;
+  const long rows = (long)n.B * n.L;
+  // S: states from the start on, and dq = scale chain(dO, v, k) with the state transposed
+  LinChain c = chain_of(n, g_log);
+  c.segs = w.segs, c.decay = w.decay, c.start = S0;
+  if (n.P > 1) {
+    c.y = rk, c.z = rv, c.run = n.P - 1;
+    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, false, st)))) return rc;
+    c.run = n.P;
+  }
+  c.x = ro, c.y = rv, c.z = rk, c.w = rq, c.flip = true;
+  c.outer = c.inner = n.scale;
+  c.out = shared ? w.shared : dq, c.out_f32 = shared || !n.bf16, c.tok = w.e;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, false, dg_log ? 1 : 0, st)))) return rc;
+  if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dq, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
+  // G: their gradients from the end on, and dv = chain(k, q, dO), dk = chain(v, dO, q)
+  c = chain_of(n, g_log);
+  c.segs = w.gsegs, c.decay = w.decay, c.start = dS_final, c.write = c.inner = n.scale;
+  c.y = rq, c.z = ro, c.end = dS0;
+  if (n.P > 1) {
+    c.run = dS0 ? n.P : n.P - 1;
+    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, true, st)))) return rc;
+    c.run = n.P;
+  }
+  c.x = rk, c.out = dv, c.out_f32 = !n.bf16;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, 0, st)))) return rc;
+  c.x = rv, c.y = ro, c.z = rq, c.w = rk, c.flip = true, c.end = nullptr;
+  c.out = shared ? w.shared : dk, c.out_f32 = shared || !n.bf16, c.tok = w.f;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, dg_log ? 2 : 0, st)))) return rc;
+  if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dk, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
+  return dg_log ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
+}
+
+int delta_decode_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const void* q, const void* k, const void* v,
+                     const float* g_log, float* S, void* O, void* stream) {
+  Lin n;
+  int rc = lin_shape(s, qk_heads, gate, n);
+  if (rc) return rc;
+  if (s->L != 1) return DELTA_ERR_BAD_SHAPE;
+  if ((rc = check_pointers({q, k, v, S, O}, n.nv > 0))) return rc;
+  if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
+  if ((rc = check_aligned({q, k, v, S, O}, g_log, nullptr))) return rc;
+  const Range in[] = {span(q, n.nqk), span(k, n.nqk), span(v, n.nv), span(g_log, n.ng)};
+  const Range out[] = {span(S, n.state), span(O, n.nv)};
+  if (any_overlap(in, out)) return DELTA_ERR_ALIAS;
+  if (n.state == 0) return DELTA_OK;
+  if ((rc = launch_guard())) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (g_log && validate_on() && (rc = validate_gates(g_log, n.ng / 4, st))) return rc;
+  const LinDecode p{n.B, n.H, n.Hk, n.dk, n.dv, gate, n.scale, q, k, v, g_log, S, O};
+  return hip_status(delta::launch_lin_decode(p, n.bf16, st));
+}
+
+}  // extern "C"
