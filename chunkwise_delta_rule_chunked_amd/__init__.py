@@ -24,7 +24,8 @@ from typing import Optional
 __all__ = ["fwd", "fwd_noalloc", "NOALLOC_MAX_BYTES", "bwd", "bwd_workspace_bytes", "layer_prologue", "layer_prologue_step", "layer_epilogue", "fwd_intra", "fwd_inter", "decode", "decode_kda", "fwd_kda", "fwd_kda_chunked", "kda_chunked_workspace_bytes", "chunk_wy", "workspace_bytes", "strerror", "DeltaError", "lib_path",
            "load_library", "F32", "BF16", "fwd_glr", "bwd_glr", "decode_glr", "glr_workspace_bytes", "bwd_glr_workspace_bytes",
            "layer_rmsnorm", "layer_rmsnorm_quant", "layer_rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "grad_norm",
-           "clip_grads", "fwd_lin", "bwd_lin", "decode_lin", "lin_workspace_bytes", "bwd_lin_workspace_bytes"]
+           "clip_grads", "fwd_lin", "bwd_lin", "decode_lin", "lin_workspace_bytes", "bwd_lin_workspace_bytes",
+           "layer_dropout", "layer_layernorm", "layer_layernorm_bwd", "layernorm_bwd_workspace_bytes"]
 
 F32, BF16 = 0, 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -508,12 +509,13 @@ _BLOCK = ("fwd_glr", "bwd_glr", "decode_glr", "glr_workspace_bytes", "bwd_glr_wo
 
 
 _LINEAR = ("fwd_lin", "bwd_lin", "decode_lin", "lin_workspace_bytes", "bwd_lin_workspace_bytes")
+_LAYERNORM = ("layer_dropout", "layer_layernorm", "layer_layernorm_bwd", "layernorm_bwd_workspace_bytes")
 
 
 def __getattr__(name):
-    """The operators of include/delta_block.h (block.py) and include/delta_linear.h (linear.py), imported at
-    their first use: this module itself does not import torch."""
-    for names, module in ((_BLOCK, "block"), (_LINEAR, "linear")):
+    """The operators of include/delta_block.h (block.py), delta_linear.h (linear.py) and delta_layernorm.h
+    (layernorm.py), imported at their first use: this module itself does not import torch."""
+    for names, module in ((_BLOCK, "block"), (_LINEAR, "linear"), (_LAYERNORM, "layernorm")):
         if name in names:
             import importlib
             module = importlib.import_module("." + module, __name__)
