@@ -8,7 +8,10 @@ namespace delta {
 
 enum { LIN_GATE_NONE = 0, LIN_GATE_TOKEN = 1, LIN_GATE_HEAD = 2 };
 
-constexpr int LIN_SLAB = 128;  // value columns of a workgroup at most: 16 for each of 8 wavefronts
+constexpr int LIN_SLAB = 128;  // columns of a workgroup's state at most
+
+// What a chain forms beside its outputs (linear_chain.h)
+enum { LIN_PLAIN = 0, LIN_PAIRS = 1, LIN_SUMS = 2, LIN_STATE = 3 };
 
 // Tokens of a chunk: float32 tiles are twice as large, and their products run at a sixteenth of the rate.
 constexpr int lin_chunk(bool bf16) { return bf16 ? 64 : 32; }
@@ -24,18 +27,18 @@ struct LinRole {
 struct LinChain {
   int B, L, H, NT, P, NS;  // chunks in all, segments, chunks of a segment
   int run;                 // segments of this launch: P, or fewer for a summary whose end nobody asks for
-  LinRole x, y, z, w;      // w: what the hook takes the inner product with
+  LinRole x, y, z, w;      // w: PAIRS and SUMS only
   const float* g;          // [B, L, H], [H] or nullptr
   int gate;
   float outer, inner, write;  // scales of the state's share of out, of the chunk's share, of what the state takes in
   const float* start;      // [B, H] states before the first segment in the chain's order, or nullptr
   float* segs;             // P > 1: [B, H, P] states, the summary's results and then each segment's start
   double* decay;           // P > 1: [B, H, P] sums of log gates
-  float* end;              // [B, H] states behind the last segment, or nullptr
+  float* end;              // [B, H] states behind the last segment: form STATE, or the summary's (or nullptr)
   bool flip;
   void* out;               // [B, L, H, z.width] in the inputs' type, or float32
   bool out_f32;
-  float* tok;              // hook: [B, H, NT chunks] a value per token
+  float* tok;              // PAIRS, SUMS: [B, H, NT chunks] a value per token
 };
 
 // Gradients of the log gates from the per-token sums of the two backward chains.
@@ -61,7 +64,7 @@ struct LinDecode {
 };
 
 void lin_split(int B, int L, int H, int dv, bool bf16, int& NT, int& P, int& NS);
-hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int hook, hipStream_t st);
+hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st);
 hipError_t launch_lin_summary(const LinChain& c, bool bf16, bool reverse, hipStream_t st);
 hipError_t launch_lin_gates(const LinGates& p, hipStream_t st);
 hipError_t launch_lin_share(const float* part, void* out, long rows, int heads, int share, int width, bool bf16, hipStream_t st);

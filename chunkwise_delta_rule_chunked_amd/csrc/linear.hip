@@ -7,8 +7,8 @@
 
 namespace delta {
 namespace lin {
-hipError_t chain_bf16(const LinChain& c, bool reverse, int hook, hipStream_t st);
-hipError_t chain_f32(const LinChain& c, bool reverse, int hook, hipStream_t st);
+hipError_t chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
+hipError_t chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
 hipError_t summary_bf16(const LinChain& c, bool reverse, hipStream_t st);
 hipError_t summary_f32(const LinChain& c, bool reverse, hipStream_t st);
 }  // namespace lin
@@ -247,8 +247,8 @@ void lin_split(int B, int L, int H, int dv, bool bf16, int& NT, int& P, int& NS)
   P = (NT + NS - 1) / NS;
 }
 
-hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int hook, hipStream_t st) {
-  return bf16 ? lin::chain_bf16(c, reverse, hook, st) : lin::chain_f32(c, reverse, hook, st);
+hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st) {
+  return bf16 ? lin::chain_bf16(c, reverse, form, st) : lin::chain_f32(c, reverse, form, st);
 }
 
 hipError_t launch_lin_summary(const LinChain& c, bool bf16, bool reverse, hipStream_t st) {

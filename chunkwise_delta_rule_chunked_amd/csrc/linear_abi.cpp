@@ -156,7 +156,7 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
     if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, false, st))) || n.P == 0) return rc;
     c.run = n.P;
   }
-  return hip_status(delta::launch_lin_chain(c, n.bf16, false, 0, st));
+  return hip_status(delta::launch_lin_chain(c, n.bf16, false, n.P == 1 && S_final ? delta::LIN_STATE : delta::LIN_PLAIN, st));
 }
 
 int delta_bwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, int32_t gate, size_t* bytes) {
@@ -224,7 +224,7 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   c.x = ro, c.y = rv, c.z = rk, c.w = rq, c.flip = true;
   c.outer = c.inner = n.scale;
   c.out = shared ? w.shared : dq, c.out_f32 = shared || !n.bf16, c.tok = w.e;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, false, dg_log ? 1 : 0, st)))) return rc;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, false, dg_log ? delta::LIN_PAIRS : delta::LIN_PLAIN, st)))) return rc;
   if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dq, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
   // G: their gradients from the end on, and dv = chain(k, q, dO), dk = chain(v, dO, q)
   c = chain_of(n, g_log);
@@ -236,10 +236,10 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
     c.run = n.P;
   }
   c.x = rk, c.out = dv, c.out_f32 = !n.bf16;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, 0, st)))) return rc;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, n.P == 1 && dS0 ? delta::LIN_STATE : delta::LIN_PLAIN, st)))) return rc;
   c.x = rv, c.y = ro, c.z = rq, c.w = rk, c.flip = true, c.end = nullptr;
   c.out = shared ? w.shared : dk, c.out_f32 = shared || !n.bf16, c.tok = w.f;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, dg_log ? 2 : 0, st)))) return rc;
+  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, dg_log ? delta::LIN_SUMS : delta::LIN_PLAIN, st)))) return rc;
   if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dk, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
   return dg_log ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
 }

@@ -14,19 +14,17 @@
 // gates are held in 64 bits, because their differences are what is used (behind a hard reset of -150 a
 // float32 sum has lost 1e-5).
 //
-// A workgroup has a segment of the sequence for one head and up to 128 columns of the state: 8 wavefronts,
-// each with 16 columns and all rows, in MFMA accumulators for the whole segment.  The two row tiles 2u,
+// A workgroup has a segment of the sequence for one head and some columns of the state: each wavefront has
+// CT tiles of 16 columns and all rows, in MFMA accumulators for the whole segment.  The two row tiles 2u,
 // 2u + 1 interleave their rows so that the accumulators of a pair, converted, are the operand of a 32-deep
-// product, in the order in which a 16-byte piece of an x row lies in LDS.  out is formed transposed, so a
-// lane ends with four consecutive columns of a token.
+// product, in the order in which a 16-byte piece of an x row lies in LDS.  out is formed transposed, and a
+// wavefront's tiles interleave their columns, so a lane ends with 4 CT consecutive columns of a token.
 #pragma once
 #include "common.h"
 #include "linear.h"
 
 namespace delta {
 namespace lin {
-
-constexpr int NW = 8, TH = NW * WAVE;
 
 template <typename E>
 struct Frag;  // 8 elements along a product's depth, lane group g the indices 8 g .. 8 g + 7 of 32
@@ -91,7 +89,7 @@ struct Split;
 template <int TERMS>
 struct Split<bf16, TERMS> {
   Frag<bf16> t[TERMS];
-  __device__ inline explicit Split(const float* x) {
+  __device__ inline void set(const float* x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float r = x[i];
@@ -106,7 +104,7 @@ struct Split<bf16, TERMS> {
 template <int TERMS>
 struct Split<float, TERMS> {
   Frag<float> t[1];
-  __device__ inline explicit Split(const float* x) {
+  __device__ inline void set(const float* x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[0].v[i] = x[i];
   }
@@ -121,32 +119,36 @@ struct Int {
   static constexpr int value = N;
 };
 
-// Hooks: 1, with the sum over columns of w_i times the state's share of out_i (e) and, for pairs j < i,
-// M_ij = e^(gc_i - gc_j) (x_i . y_j)(w_i . z_j): e + M's row sums - its column sums per token.  2: e alone.
-template <typename E, int KW, bool REV, int HOOK, bool SUM>
+// What a chain forms beside out.  SUMS: per token the sum over columns of w_i times the state's share of out_i (e).
+// PAIRS: also, for pairs j < i, M_ij = e^(gc_i - gc_j) (x_i . y_j)(w_i . z_j), and per token e + M's row sums - its
+// column sums.  STATE: the state behind the last token.  A state that is an output, or that the gates' gradients are
+// formed from, takes in float32 weights whole (three bf16 terms); one that only out reads, whose products round it to
+// bf16, one term.
+constexpr int PLAIN = LIN_PLAIN, PAIRS = LIN_PAIRS, SUMS = LIN_SUMS, STATE = LIN_STATE;
+constexpr bool hooked(int form) { return form == PAIRS || form == SUMS; }
+
+template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
 struct Config {
-  static constexpr int C = lin_chunk(sizeof(E) == 2), NB = C / 16, VW = LIN_SLAB;
+  static constexpr int C = lin_chunk(sizeof(E) == 2), NB = C / 16, VW = 16 * NW * CT, TH = NW * WAVE;
   static constexpr int NT = KW / 16, NU = KW / 32;
   static constexpr int VEC = 16 / (int)sizeof(E);
   static constexpr int PX = C * KW / VEC, PZ = C * VW / VEC;            // 16-byte pieces of a tile
   static constexpr int NX = (PX + TH - 1) / TH, NZ = (PZ + TH - 1) / TH;  // of a thread
   // LDS, in bytes
   static constexpr int X = 0, Y = X + (SUM ? 0 : C * KW * (int)sizeof(E)), Z = Y + C * KW * (int)sizeof(E),
-                       W = Z + C * VW * (int)sizeof(E), A = W + (HOOK ? C * VW * (int)sizeof(E) : 0),
+                       W = Z + C * VW * (int)sizeof(E), A = W + (hooked(FORM) ? C * VW * (int)sizeof(E) : 0),
                        TAB = A + (SUM ? 0 : C * C * (int)sizeof(E));
   static constexpr int TABLE = 4 * C * 4 + 16;  // sums of log gates (64 bits), x's and y's factors, the chunk's
-  static constexpr int PART = TAB + 2 * TABLE, PARTS = HOOK == 1 ? NW + 2 * NB : HOOK == 2 ? NW : 0;
+  static constexpr int PART = TAB + 2 * TABLE, PARTS = FORM == PAIRS ? NW + 2 * NB : FORM == SUMS ? NW : 0;
   static constexpr int LDS = PART + PARTS * C * 4;
 };
 
-template <typename E, int KW, bool REV, int HOOK, bool SUM>
-__global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
-  typedef Config<E, KW, REV, HOOK, SUM> K;
-  constexpr int C = K::C, NB = K::NB, VW = K::VW, NT = K::NT, NU = K::NU, VEC = K::VEC;
-  constexpr int INT = terms<E>(HOOK ? 3 : 1);
-  // A state that is an output, or that the gates' gradients are formed from, takes float32 weights in whole (three
-  // terms); one that only out reads, whose products round it to bf16, one term.
-  const bool whole_terms = SUM || HOOK || (p.P == 1 && p.end);
+template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
+__global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) == 2 ? 2 : 1) void chain_kernel(LinChain p) {
+  typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
+  constexpr int C = K::C, NB = K::NB, VW = K::VW, NT = K::NT, NU = K::NU, VEC = K::VEC, TH = K::TH;
+  constexpr bool HOOK = hooked(FORM);
+  constexpr int INT = terms<E>(HOOK ? 3 : 1), UPD = terms<E>(SUM || FORM != PLAIN ? 3 : 1);
   typedef Rows<E, KW> RX;
   typedef Rows<E, VW> RZ;
   typedef Rows<E, C> RA;
@@ -159,14 +161,14 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
   float* const part = reinterpret_cast<float*>(smem + K::PART);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g4 = lane >> 4, m = lane & 15;
-  const int tiles = p.z.width / 16, slabs = (tiles + NW - 1) / NW, per = (tiles + slabs - 1) / slabs;
+  const int tiles = p.z.width / 16, slabs = (tiles + NW * CT - 1) / (NW * CT), per = (tiles + slabs - 1) / slabs;
   const int slab = blockIdx.x % slabs, seg = blockIdx.x / slabs % p.run;
   const long bh = blockIdx.x / slabs / p.run;
   const int h = (int)(bh % p.H);
   const long b = bh / p.H;
   const int c0 = 16 * per * slab, cols = min(16 * per, p.z.width - c0);  // columns of this workgroup
-  const bool live = 16 * wave < cols;
+  const int w0 = 16 * CT * wave;  // this wavefront's columns w0 ..: its tile c holds w0 + 4 CT (i / 4) + 4 c + i % 4, i < 16
+  const bool live = w0 < cols;
   // the segments are the same ones in either order
   const int first = (REV ? p.P - 1 - seg : seg) * p.NS, count = min(p.NS, p.NT - first);
   auto chunk_at = [&](int i) { return REV ? first + count - 1 - i : first + i; };
@@ -182,24 +184,31 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
     return Source{static_cast<const E*>(r.p) + (b * p.L * r.heads + head) * r.width + col, r.heads * r.width * (int)sizeof(E),
                   width * (int)sizeof(E)};
   };
-  auto load = [&](auto& regs, const Source& s, int n, auto cpr, int pieces) {
-    constexpr int CPR = decltype(cpr)::value;
+  // Offsets are formed again for every chunk, from a thread index that the optimiser cannot see through: kept, they
+  // spill, and each load then waits for its offset behind the loads before it.
+  auto hidden = [](int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+  };
+  auto load = [&](auto& regs, const Source& s, int n, auto cpr) {
+    constexpr int CPR = decltype(cpr)::value, N = sizeof(regs) / 16;
+    static_assert(TH % CPR == 0 && N * TH == C * CPR, "whole rounds of whole rows");
     const int rows = min(C, p.L - n * C);
     const __amdgpu_buffer_rsrc_t r = buffer_rsrc(
         const_cast<char*>(reinterpret_cast<const char*>(s.base) + (long)n * C * s.stride), rows * s.stride);
+    const int q = hidden(tid), c = q % CPR * 16;
+    // rows past the sequence and columns past the width read 0 (no range reaches 2^30)
+    const int from = q / CPR * s.stride + (c < s.left ? c : 1 << 30);
 #pragma unroll
-    for (int k = 0; k < (int)(sizeof(regs) / 16); ++k) {
-      const int q = tid + k * TH, row = q / CPR, c = q % CPR * 16;
-      // rows past the sequence and columns past the width read 0
-      regs[k] = buffer_load16(r, q < pieces && c < s.left ? row * s.stride + c : 0x7fffffff);
-    }
+    for (int k = 0; k < N; ++k) regs[k] = buffer_load16(r, from + k * (TH / CPR) * s.stride);
   };
-  auto put = [&](const auto& regs, E* tile, auto cpr, int pieces) {
-    constexpr int CPR = decltype(cpr)::value, MASK = pow2_part(CPR) - 1;
+  auto put = [&](const auto& regs, E* tile, auto cpr) {
+    constexpr int CPR = decltype(cpr)::value, MASK = pow2_part(CPR) - 1, N = sizeof(regs) / 16;
+    const int q = hidden(tid);
 #pragma unroll
-    for (int k = 0; k < (int)(sizeof(regs) / 16); ++k) {
-      const int q = tid + k * TH, row = q / CPR, c = q % CPR;
-      if (q < pieces) *reinterpret_cast<u32x4*>(tile + row * CPR * VEC + (c ^ swz_key(row, MASK)) * VEC) = regs[k];
+    for (int k = 0; k < N; ++k) {
+      const int row = q / CPR + k * (TH / CPR), c = q % CPR;
+      *reinterpret_cast<u32x4*>(tile + row * CPR * VEC + (c ^ swz_key(row, MASK)) * VEC) = regs[k];
     }
   };
   typedef Int<KW / VEC> CX;  // 16-byte pieces of a row
@@ -207,18 +216,27 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
   const Source sx = source(p.x, 0, p.x.width), sy = source(p.y, 0, p.y.width), sz = source(p.z, c0, cols),
                sw = source(HOOK ? p.w : p.z, c0, cols);
   u32x4 rx[SUM ? 1 : K::NX], ry[K::NX], rz[K::NZ], rw[HOOK ? K::NZ : 1];
+  const bool keeper = wave == NW - 1;  // forms the gate tables
+  auto gate_of = [&](int i) {
+    const int tok = chunk_at(i) * C + lane;
+    if (p.gate == LIN_GATE_NONE || lane >= C || tok >= p.L) return 0.f;
+    return p.gate == LIN_GATE_TOKEN ? p.g[(b * p.L + tok) * p.H + h] : p.g[h];
+  };
+  float gate = 0.f;  // of this lane's token of the chunk after the one in the registers (keeper)
   auto load_all = [&](int i) {
     const int n = chunk_at(i);
-    if constexpr (!SUM) load(rx, sx, n, CX{}, K::PX);
-    load(ry, sy, n, CX{}, K::PX);
-    load(rz, sz, n, CZ{}, K::PZ);
-    if constexpr (HOOK != 0) load(rw, sw, n, CZ{}, K::PZ);
+    if (keeper && i + 1 < count) gate = gate_of(i + 1);
+    if constexpr (!SUM) load(rx, sx, n, CX{});
+    load(ry, sy, n, CX{});
+    load(rz, sz, n, CZ{});
+    if constexpr (HOOK) load(rw, sw, n, CZ{});
   };
   auto put_all = [&]() {
-    if constexpr (!SUM) put(rx, xt, CX{}, K::PX);
-    put(ry, yt, CX{}, K::PX);
-    put(rz, zt, CZ{}, K::PZ);
-    if constexpr (HOOK != 0) put(rw, wt, CZ{}, K::PZ);
+    if constexpr (!SUM) put(rx, xt, CX{});
+    put(ry, yt, CX{});
+    put(rz, zt, CZ{});
+    if constexpr (HOOK) put(rw, wt, CZ{});
+    asm volatile("" : "+v"(gate));  // waited for here, not behind the next chunk's loads
   };
 
   // ---- a chunk's gate tables, by one wavefront: gc log2 e, x's factors, y's factors, the chunk's
@@ -231,13 +249,7 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
     return Table{reinterpret_cast<double*>(t), reinterpret_cast<float*>(t + 8 * C), reinterpret_cast<float*>(t + 12 * C),
                  reinterpret_cast<float*>(t + 16 * C)};
   };
-  const bool keeper = wave == NW - 1;
   double sum = 0.0;  // log gates of the chunks so far (keeper)
-  auto gate_of = [&](int i) {  // this lane's token's
-    const int tok = chunk_at(i) * C + lane;
-    if (p.gate == LIN_GATE_NONE || lane >= C || tok >= p.L) return 0.f;
-    return p.gate == LIN_GATE_TOKEN ? p.g[(b * p.L + tok) * p.H + h] : p.g[h];
-  };
   auto tables = [&](int i, float gl) {
     double a = (double)(gl < LOG_GATE_FLOOR ? LOG_GATE_FLOOR : gl);
 #pragma unroll
@@ -257,43 +269,59 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
     if (lane == 0) *const_cast<float*>(t.whole) = expf((float)last);
   };
 
-  // ---- the state: rows srow(t, 4 g + j) of column m of this wavefront's 16
+  // ---- the state: rows srow(t, 4 g + j) of column m of this wavefront's tiles
   auto srow = [](int t, int r) { return 32 * (t >> 1) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3); };
-  const int width = p.y.width, col = c0 + 16 * wave + m;
-  const long size = (long)width * p.z.width;
-  auto element = [&](int row) { return p.flip ? (long)col * width + row : (long)row * p.z.width + col; };
-  floatx4 S[NT];
+  const int width = p.y.width;
+  const int size = width * p.z.width;
+  floatx4 S[CT][NT];
+  // A lane's four rows of a tile lie next to each other in a flipped state, and are z.width apart in another one.
+  auto each = [&](auto four, auto one) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int row = srow(t, 4 * (lane >> 4)), own = w0 + 4 * CT * ((lane & 15) >> 2) + 4 * c + (lane & 3);
+        const bool in = own < cols && row < width;
+        if (p.flip) {
+          four(c, t, in ? ((c0 + own) * width + row) * 4 : 1 << 30);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) one(c, t, j, in ? ((row + j) * p.z.width + c0 + own) * 4 : 1 << 30);
+        }
+      }
+  };
   const float* from = SUM ? nullptr : p.P > 1 ? p.segs + (bh * p.P + seg) * size : p.start ? p.start + bh * size : nullptr;
+  const __amdgpu_buffer_rsrc_t start = buffer_rsrc(const_cast<float*>(from), from ? size * 4 : 0);  // else all 0
+  if constexpr (SUM) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = srow(t, 4 * g4 + j);
-      S[t][j] = from && live && row < width ? from[element(row)] : 0.f;
-    }
+      for (int t = 0; t < NT; ++t) S[c][t] = floatx4{};
+  } else {
+    each([&](int c, int t, int i) { S[c][t] = __builtin_bit_cast(floatx4, buffer_load16(start, i)); },
+         [&](int c, int t, int j, int i) { S[c][t][j] = buffer_load4(start, i); });
+  }
 
   // what is never written again: blocks of A past the diagonal, hooks' slots of wavefronts without columns
   if constexpr (!SUM)
     for (int i = tid; i < C * C; i += TH) at[i] = (E)0.f;
   for (int i = tid; i < K::PARTS * C; i += TH) part[i] = 0.f;
 
-  float gnext = 0.f;
-  if (keeper) {
-    tables(0, gate_of(0));
-    if (count > 1) gnext = gate_of(1);
-  }
+  if (keeper) tables(0, gate_of(0));
   load_all(0);
   put_all();
+  float next = gate;  // gates of the chunk whose tables come next
   if (count > 1) load_all(1);
   barrier_lds();
 
   for (int i = 0; i < count; ++i) {
     const int n = chunk_at(i);
     const Table tab = table(i);
-    if (keeper && i + 1 < count) {
-      tables(i + 1, gnext);
-      if (i + 2 < count) gnext = gate_of(i + 2);
-    }
+    // LDS addresses are formed again in every chunk, from a lane that the optimiser cannot see through: hoisted
+    // out of the loop they take a hundred registers
+    const int ln = hidden(lane);
+    const int g4 = ln >> 4, m = ln & 15;
+    if (keeper && i + 1 < count) tables(i + 1, next);
 
     // A = inner Gamma (x y^T), block by block: rows j of the product are y's tokens, so a lane has four
     // consecutive j of one token i
@@ -307,11 +335,12 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
           floatx4 d = {}, d2 = {};
 #pragma unroll
           for (int u = 0; u < NU; ++u)
-            d = mma(RX::row(yt, 16 * jb + m, 32 * u + 8 * g4), RX::row(xt, 16 * ib + m, 32 * u + 8 * g4), d);
-          if constexpr (HOOK == 1) {
+            d = mma(RX::row(yt + 16 * jb * KW, m, 32 * u + 8 * g4), RX::row(xt + 16 * ib * KW, m, 32 * u + 8 * g4), d);
+          if constexpr (FORM == PAIRS) {
 #pragma unroll
-            for (int u = 0; u < VW / 32; ++u)
-              if (32 * u < cols) d2 = mma(RZ::row(zt, 16 * jb + m, 32 * u + 8 * g4), RZ::row(wt, 16 * ib + m, 32 * u + 8 * g4), d2);
+            for (int u = 0; u < (VW + 31) / 32; ++u)
+              if (32 * u < cols)
+                d2 = mma(RZ::row(zt + 16 * jb * VW, m, 32 * u + 8 * g4), RZ::row(wt + 16 * ib * VW, m, 32 * u + 8 * g4), d2);
           }
           const int ti = 16 * ib + m, tj = 16 * jb + 4 * g4;
           const double gi = tab.gc[ti];
@@ -320,14 +349,15 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
           for (int r = 0; r < 4; ++r) {
             const double e = REV ? tab.gc[tj + r] - gi : gi - tab.gc[tj + r];
             const bool on = REV ? tj + r >= ti : tj + r <= ti;
-            v[r] = on ? d[r] * p.inner * __builtin_amdgcn_exp2f((float)e) : 0.f;
-            if constexpr (HOOK == 1) {
+            const float factor = p.inner * __builtin_amdgcn_exp2f(on ? (float)e : -INFINITY);
+            v[r] = on ? d[r] * factor : 0.f;
+            if constexpr (FORM == PAIRS) {
               d2[r] = tj + r == ti ? 0.f : v[r] * d2[r];
               row += d2[r];
             }
           }
           store4<E>(at + RA::at(ti, tj), v[0], v[1], v[2], v[3]);
-          if constexpr (HOOK == 1) {
+          if constexpr (FORM == PAIRS) {
             row += __shfl_xor(row, 16, WAVE);
             row += __shfl_xor(row, 32, WAVE);
             if (g4 == 0) part[(NW + jb) * C + ti] = row;
@@ -342,71 +372,91 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
       }
     }
 
-    Frag<E> zf[C / 32];
+    [[maybe_unused]] floatx4 out[CT][NB];
+    Frag<E> zf[CT][C / 32];
+    if (live) {
 #pragma unroll
-    for (int s = 0; s < C / 32; ++s) zf[s] = RZ::col(zt, 32 * s, 16 * wave, 4, lane);
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int s = 0; s < C / 32; ++s) zf[c][s] = RZ::col(zt, 32 * s, w0 + 4 * c, 4 * CT, ln);
 
-    // the state's share of out
-    [[maybe_unused]] floatx4 out[NB];
-    if constexpr (!SUM) {
+      // the state's share of out
+      if constexpr (!SUM) {
 #pragma unroll
-      for (int ib = 0; ib < NB; ++ib) out[ib] = floatx4{};
-      if (live) {
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int ib = 0; ib < NB; ++ib) out[c][ib] = floatx4{};
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-          float s8[8];
+          Split<E, INT> sf[CT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s8[j] = S[2 * u][j], s8[4 + j] = S[2 * u + 1][j];
-          const Split<E, INT> sf(s8);
+          for (int c = 0; c < CT; ++c) {
+            float s8[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s8[j] = S[c][2 * u][j], s8[4 + j] = S[c][2 * u + 1][j];
+            sf[c].set(s8);
+          }
 #pragma unroll
           for (int ib = 0; ib < NB; ++ib) {
-            const Frag<E> xf = RX::row(xt, 16 * ib + m, 32 * u + 8 * g4);
+            const Frag<E> xf = RX::row(xt + 16 * ib * KW, m, 32 * u + 8 * g4);
 #pragma unroll
-            for (int k = INT - 1; k >= 0; --k) out[ib] = mma(sf.t[k], xf, out[ib]);
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int k = INT - 1; k >= 0; --k) out[c][ib] = mma(sf[c].t[k], xf, out[c][ib]);
           }
         }
 #pragma unroll
         for (int ib = 0; ib < NB; ++ib) {
-          out[ib] *= tab.fx[16 * ib + m];
-          if constexpr (HOOK != 0) {
-            const E* wr = wt + RZ::at(16 * ib + m, 16 * wave + 4 * g4);
+          const float fx = tab.fx[16 * ib + m];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) out[c][ib] *= fx;
+          if constexpr (HOOK) {
             float e = 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) e += out[ib][r] * to_float(wr[r]);
+            for (int c = 0; c < CT; ++c) {
+              const E* wr = wt + RZ::at(16 * ib + m, w0 + 4 * CT * g4 + 4 * c);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) e += out[c][ib][r] * to_float(wr[r]);
+            }
             e += __shfl_xor(e, 16, WAVE);
             e += __shfl_xor(e, 32, WAVE);
             if (g4 == 0) part[wave * C + 16 * ib + m] = e;
           }
         }
       }
-    }
 
-    // the state behind the chunk
-    const float whole = *tab.whole;
+      // the state behind the chunk
+      const float whole = *tab.whole;
+      const int lu = hidden(lane);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) S[t] *= whole;
-    auto update = [&](auto n) {
-      constexpr int UPD = terms<E>(decltype(n)::value);
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) S[c][t] *= whole;
 #pragma unroll
       for (int s = 0; s < C / 32; ++s) {
-        float z8[8];
+        Split<E, UPD> zw[CT];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) z8[k] = to_float((E)zf[s].v[k]) * tab.fy[32 * s + 8 * g4 + k];
-        const Split<E, UPD> zw(z8);
+        for (int c = 0; c < CT; ++c) {
+          float z8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) z8[k] = to_float((E)zf[c][s].v[k]) * tab.fy[32 * s + 8 * g4 + k];
+          zw[c].set(z8);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const Frag<E> yf = RX::col(yt, 32 * s, 32 * (t >> 1) + 4 * (t & 1), 8, lane);
+          const Frag<E> yf = RX::col(yt + 32 * s * KW, 0, 32 * (t >> 1) + 4 * (t & 1), 8, lu);
 #pragma unroll
-          for (int k = UPD - 1; k >= 0; --k) S[t] = mma(yf, zw.t[k], S[t]);
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int k = UPD - 1; k >= 0; --k) S[c][t] = mma(yf, zw[c].t[k], S[c][t]);
         }
       }
-    };
-    if (whole_terms) update(Int<3>{});
-    else update(Int<1>{});
+    }
     barrier_lds();  // A is whole; the tiles have been read
 
     if (i + 1 < count) {
       put_all();
+      next = gate;
       if (i + 2 < count) load_all(i + 2);
     }
     if constexpr (!SUM) {
@@ -416,28 +466,39 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
         for (int s = 0; s < C / 32; ++s)
 #pragma unroll
           for (int ib = 0; ib < NB; ++ib)
-            if (REV ? 2 * s + 1 >= ib : 2 * s <= ib) out[ib] = mma(zf[s], RA::row(at, 16 * ib + m, 32 * s + 8 * g4), out[ib]);
-        const int rows = min(C, p.L - n * C);
+            if (REV ? 2 * s + 1 >= ib : 2 * s <= ib) {
+              const Frag<E> af = RA::row(at + 16 * ib * C, m, 32 * s + 8 * g4);
+#pragma unroll
+              for (int c = 0; c < CT; ++c) out[c][ib] = mma(zf[c][s], af, out[c][ib]);
+            }
+        const int rows = min(C, p.L - n * C), stride = p.H * p.z.width;
         const long head = (b * p.L + (long)n * C) * p.H + h;
-        const int stride = p.H * p.z.width;
-        if (sizeof(E) == 2 && !p.out_f32) {
-          const __amdgpu_buffer_rsrc_t r = buffer_rsrc(static_cast<bf16*>(p.out) + head * p.z.width, rows * stride * 2);
+        const int size_of = sizeof(E) == 2 && !p.out_f32 ? 2 : 4;
+        const __amdgpu_buffer_rsrc_t r = buffer_rsrc(static_cast<char*>(p.out) + head * p.z.width * size_of, rows * stride * size_of);
+        const int own = w0 + 4 * CT * g4, to = own < cols ? m * stride + c0 + own : 1 << 28;  // past every range
 #pragma unroll
-          for (int ib = 0; ib < NB; ++ib)
-            buffer_store8(r, ((16 * ib + m) * stride + c0 + 16 * wave + 4 * g4) * 2,
-                          bf16x4{(bf16)out[ib][0], (bf16)out[ib][1], (bf16)out[ib][2], (bf16)out[ib][3]});
-        } else {
-          const __amdgpu_buffer_rsrc_t r = buffer_rsrc(static_cast<float*>(p.out) + head * p.z.width, rows * stride * 4);
+        for (int ib = 0; ib < NB; ++ib) {
+          const int at = (to + 16 * ib * stride) * size_of;
+          if (size_of == 4) {
 #pragma unroll
-          for (int ib = 0; ib < NB; ++ib) buffer_store16(r, ((16 * ib + m) * stride + c0 + 16 * wave + 4 * g4) * 4, out[ib]);
+            for (int c = 0; c < CT; ++c) buffer_store16(r, at + 16 * c, out[c][ib]);
+          } else if constexpr (CT == 2) {
+            bf16x8 v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = (bf16)out[0][ib][k], v[4 + k] = (bf16)out[1][ib][k];
+            buffer_store16(r, at, __builtin_bit_cast(floatx4, v));
+          } else {
+            const floatx4 o = out[0][ib];
+            buffer_store8(r, at, bf16x4{(bf16)o[0], (bf16)o[1], (bf16)o[2], (bf16)o[3]});
+          }
         }
       }
-      if constexpr (HOOK != 0) {
+      if constexpr (HOOK) {
         if (wave == 0 && lane < C) {
           float e = 0.f;
 #pragma unroll
           for (int k = 0; k < NW; ++k) e += part[k * C + lane];
-          if constexpr (HOOK == 1) {
+          if constexpr (FORM == PAIRS) {
             float row = 0.f, down = 0.f;
 #pragma unroll
             for (int k = 0; k < NB; ++k) row += part[(NW + k) * C + lane], down += part[(NW + NB + k) * C + lane];
@@ -450,50 +511,60 @@ __global__ __launch_bounds__(TH) void chain_kernel(LinChain p) {
     barrier_lds();
   }
 
-  float* to = SUM ? p.segs + (bh * p.P + seg) * size : p.P == 1 && p.end ? p.end + bh * size : nullptr;
-  if (to && live)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = srow(t, 4 * g4 + j);
-        if (row < width) to[element(row)] = S[t][j];
-      }
+  float* to = SUM ? p.segs + (bh * p.P + seg) * size : FORM == STATE ? p.end + bh * size : nullptr;
+  if (to) {
+    const __amdgpu_buffer_rsrc_t end = buffer_rsrc(to, size * 4);
+    each([&](int c, int t, int i) { buffer_store16(end, i, S[c][t]); },
+         [&](int c, int t, int j, int i) { buffer_store4(end, i, S[c][t][j]); });
+  }
   if (SUM && keeper && slab == 0 && lane == 0) p.decay[bh * p.P + seg] = sum;
 }
 
-template <typename E, int KW, bool REV, int HOOK, bool SUM>
+template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
 hipError_t run(const LinChain& c, hipStream_t st) {
-  typedef Config<E, KW, REV, HOOK, SUM> K;
+  typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
   static_assert(K::LDS <= 160 * 1024, "a workgroup's LDS");
-  const int tiles = c.z.width / 16, slabs = (tiles + NW - 1) / NW;
-  hipLaunchKernelGGL((chain_kernel<E, KW, REV, HOOK, SUM>), dim3((unsigned)((long)c.B * c.H * c.run * slabs)), dim3(TH), K::LDS,
-                     st, c);
+  const int tiles = c.z.width / 16, slabs = (tiles + NW * CT - 1) / (NW * CT);
+  hipLaunchKernelGGL((chain_kernel<E, KW, NW, CT, REV, FORM, SUM>), dim3((unsigned)((long)c.B * c.H * c.run * slabs)), dim3(K::TH),
+                     K::LDS, st, c);
   return hipGetLastError();
 }
 
-template <typename E, bool REV, int HOOK, bool SUM>
+// Workgroups of 64 or 128 columns, four wavefronts with one tile or two each; rows of 256 leave the registers of a
+// wavefront room for one tile.
+template <typename E, int KW, bool REV, int FORM, bool SUM>
+hipError_t by_columns(const LinChain& c, hipStream_t st) {
+  if constexpr (KW == 256) return run<E, KW, 8, 1, REV, FORM, SUM>(c, st);
+  else return c.z.width <= 64 ? run<E, KW, 4, 1, REV, FORM, SUM>(c, st) : run<E, KW, 4, 2, REV, FORM, SUM>(c, st);
+}
+
+template <typename E, bool REV, int FORM, bool SUM>
 hipError_t by_width(const LinChain& c, hipStream_t st) {
   const int w = c.y.width;
-  if (w <= 32) return run<E, 32, REV, HOOK, SUM>(c, st);
-  if (w <= 64) return run<E, 64, REV, HOOK, SUM>(c, st);
-  if (w <= 128) return run<E, 128, REV, HOOK, SUM>(c, st);
-  if constexpr (!SUM) return run<E, 256, REV, HOOK, SUM>(c, st);
+  if (w <= 32) return by_columns<E, 32, REV, FORM, SUM>(c, st);
+  if (w <= 64) return by_columns<E, 64, REV, FORM, SUM>(c, st);
+  if (w <= 128) return by_columns<E, 128, REV, FORM, SUM>(c, st);
+  if constexpr (!SUM) return by_columns<E, 256, REV, FORM, SUM>(c, st);
   return hipErrorInvalidValue;
 }
 
 template <typename E>
-hipError_t chain(const LinChain& c, bool reverse, int hook, hipStream_t st) {
-  if (reverse) return hook ? by_width<E, true, 2, false>(c, st) : by_width<E, true, 0, false>(c, st);
-  return hook ? by_width<E, false, 1, false>(c, st) : by_width<E, false, 0, false>(c, st);
+hipError_t chain(const LinChain& c, bool reverse, int form, hipStream_t st) {
+  switch (form) {
+    case PLAIN: return reverse ? by_width<E, true, PLAIN, false>(c, st) : by_width<E, false, PLAIN, false>(c, st);
+    case STATE: return reverse ? by_width<E, true, STATE, false>(c, st) : by_width<E, false, STATE, false>(c, st);
+    case PAIRS: return by_width<E, false, PAIRS, false>(c, st);
+    case SUMS: return by_width<E, true, SUMS, false>(c, st);
+    default: return hipErrorInvalidValue;
+  }
 }
 template <typename E>
 hipError_t summary(const LinChain& c, bool reverse, hipStream_t st) {
-  return reverse ? by_width<E, true, 0, true>(c, st) : by_width<E, false, 0, true>(c, st);
+  return reverse ? by_width<E, true, PLAIN, true>(c, st) : by_width<E, false, PLAIN, true>(c, st);
 }
 
-hipError_t chain_bf16(const LinChain& c, bool reverse, int hook, hipStream_t st);
-hipError_t chain_f32(const LinChain& c, bool reverse, int hook, hipStream_t st);
+hipError_t chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
+hipError_t chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
 hipError_t summary_bf16(const LinChain& c, bool reverse, hipStream_t st);
 hipError_t summary_f32(const LinChain& c, bool reverse, hipStream_t st);
 

@@ -4,7 +4,7 @@
 namespace delta {
 namespace lin {
 
-hipError_t chain_f32(const LinChain& c, bool reverse, int hook, hipStream_t st) { return chain<float>(c, reverse, hook, st); }
+hipError_t chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st) { return chain<float>(c, reverse, form, st); }
 hipError_t summary_f32(const LinChain& c, bool reverse, hipStream_t st) { return summary<float>(c, reverse, st); }
 
 }  // namespace lin
