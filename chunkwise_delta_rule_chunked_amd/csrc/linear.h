@@ -16,6 +16,9 @@ enum { LIN_PLAIN = 0, LIN_PAIRS = 1, LIN_SUMS = 2, LIN_STATE = 3 };
 // Tokens of a chunk: float32 tiles are twice as large, and their products run at a sixteenth of the rate.
 constexpr int lin_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
+// Inner products of states are left in parts of 256 elements.
+constexpr int lin_parts(int dk, int dv) { return dk * dv / 256; }
+
 // One operand of a chain: [B, L, heads, width], head h of the chain reading head h / (H / heads).
 struct LinRole {
   const void* p;
@@ -41,13 +44,12 @@ struct LinChain {
   float* tok;              // PAIRS, SUMS: [B, H, NT chunks] a value per token
 };
 
-// Gradients of the log gates from the per-token sums of the two backward chains.
+// Gradients of the log gates from what the two backward chains left.
 struct LinGates {
-  int B, L, H, C, NT, P, NS;
-  size_t state;            // elements of one state
+  int B, L, H, C, NT, P, NS, dk, dv;
   const float *e, *f;      // [B, H, NT * C]
-  const float *S0, *dS0;   // [B, H] states and their gradients before the first token (S0 nullptr: no such term)
-  const float *segs, *gsegs;  // P > 1: start states of the forward and of the reverse chain
+  const double* bounds;    // P > 1: [B, H, P, lin_parts] parts of <S, G> before each segment
+  const float *S0, *dS0;   // P = 1: [B, H] states and their gradients before the first token (nullptr: no such term)
   const float* g;
   int gate;
   float* dg;               // [B, L, H], or [H] through `part`
@@ -63,11 +65,35 @@ struct LinDecode {
   void* O;
 };
 
-void lin_split(int B, int L, int H, int dv, bool bf16, int& NT, int& P, int& NS);
-hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st);
-hipError_t launch_lin_summary(const LinChain& c, bool bf16, bool reverse, hipStream_t st);
+void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS);
+// bf16 inputs in one file, float32 in another
+hipError_t lin_chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
+hipError_t lin_chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
+hipError_t lin_summary_bf16(const LinChain* forward, const LinChain* reverse, hipStream_t st);
+hipError_t lin_summary_f32(const LinChain* forward, const LinChain* reverse, hipStream_t st);
+hipError_t lin_backward_bf16(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, hipStream_t st);
+hipError_t lin_backward_f32(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, hipStream_t st);
+
+inline hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st) {
+  return bf16 ? lin_chain_bf16(c, reverse, form, st) : lin_chain_f32(c, reverse, form, st);
+}
+// Each segment's state from zero, `forward` and `reverse` in one launch (either may be nullptr, and have run = 0).
+inline hipError_t launch_lin_summary(const LinChain* forward, const LinChain* reverse, bool bf16, hipStream_t st) {
+  return bf16 ? lin_summary_bf16(forward, reverse, st) : lin_summary_f32(forward, reverse, st);
+}
+// The three chains of a backward pass in one launch, forms PAIRS, PLAIN and SUMS, or all PLAIN without `gates`; dv's STATE
+// with `state`.  Only for values of up to 128 channels.
+inline hipError_t launch_lin_backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, bool bf16,
+                                      hipStream_t st) {
+  return bf16 ? lin_backward_bf16(dq, dv, dk, gates, state, st) : lin_backward_f32(dq, dv, dk, gates, state, st);
+}
+// The segments' results become their starts, of both chains (either nullptr); with both also, where `bounds`, the parts of
+// <S, G> before each segment (before the first only if both states are there: forward's start, reverse's end).
+hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, double* bounds, hipStream_t st);
 hipError_t launch_lin_gates(const LinGates& p, hipStream_t st);
-hipError_t launch_lin_share(const float* part, void* out, long rows, int heads, int share, int width, bool bf16, hipStream_t st);
+// The parts of dq and of dk, each [rows, heads, share, width], added up over `share`.
+hipError_t launch_lin_share(const float* dq_part, const float* dk_part, void* dq, void* dk, long rows, int heads, int share, int width,
+                            bool bf16, hipStream_t st);
 hipError_t launch_lin_decode(const LinDecode& p, bool bf16, hipStream_t st);
 
 }  // namespace delta

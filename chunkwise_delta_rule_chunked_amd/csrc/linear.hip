@@ -1,49 +1,93 @@
 // Linear attention with a decay for each head: the launches around the chain kernel (linear_chain.h), and
 // the step for one token.
 #include <hip/hip_runtime.h>
+#include <math.h>
 
 #include "common.h"
 #include "linear.h"
 
 namespace delta {
-namespace lin {
-hipError_t chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
-hipError_t chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
-hipError_t summary_bf16(const LinChain& c, bool reverse, hipStream_t st);
-hipError_t summary_f32(const LinChain& c, bool reverse, hipStream_t st);
-}  // namespace lin
-
 namespace {
-
-// Each segment's result becomes its start: start_{p+1} = e^decay_p start_p + result_p, four elements a lane.
-__global__ __launch_bounds__(256) void combine_kernel(int P, long quads, long all, const floatx4* start, floatx4* segs,
-                                                      const double* decay, floatx4* end) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x, bh = i / quads, q = i % quads;
-  if (i >= all) return;
-  floatx4 s = start ? start[bh * quads + q] : floatx4{};
-  floatx4* at = segs + bh * P * quads + q;
-  const int n = end ? P : P - 1;  // without an end the last segment has no result
-  constexpr int AHEAD = 8;        // results loaded at a time
-  for (int p0 = 0; p0 < n; p0 += AHEAD) {
-    floatx4 r[AHEAD];
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (p0 + k < n) r[k] = at[(p0 + k) * quads];
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (p0 + k < n) {
-        at[(p0 + k) * quads] = s;
-        s = s * expf((float)decay[bh * P + p0 + k]) + r[k];
-      }
-  }
-  if (end) end[bh * quads + q] = s;
-  else if (P > 0) at[(P - 1) * quads] = s;
-}
 
 __device__ inline double wave_total(double x) {
 #pragma unroll
   for (int o = WAVE / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, WAVE);
   return x;
+}
+
+// One chain's states of one place, four elements a lane, from segment to segment: a segment's result becomes its start,
+// start_{p+1} = e^decay_p start_p + result_p.  BOUNDS: and the parts of the inner products with the other chain's starts
+// (segment p of the reverse chain starts behind segment P - 1 - p of the other).
+struct Walk {
+  const floatx4* start;
+  floatx4 *segs, *end;
+  const double* decay;
+};
+template <bool BOUNDS>
+__device__ inline void walk(const Walk& w, int P, long quads, long bh, long q, const floatx4* other, const floatx4* other0,
+                            double* bounds) {
+  auto dot = [](const floatx4& a, const floatx4& b) {
+    double x = 0.0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x += (double)a[k] * b[k];
+    return x;
+  };
+  auto bound = [&](int place, double x) {
+    x = wave_total(x);
+    if (threadIdx.x % WAVE == 0) bounds[((bh * P + place) * quads + q) / WAVE] = x;
+  };
+  floatx4 s = w.start ? w.start[bh * quads + q] : floatx4{};
+  floatx4* at = w.segs + bh * P * quads + q;
+  const floatx4* ot = other + bh * P * quads + q;
+  const int n = w.end ? P : P - 1;  // without an end the last segment has no result
+  constexpr int AHEAD = 8;          // results loaded at a time
+  for (int p0 = 0; p0 < n; p0 += AHEAD) {
+    floatx4 r[AHEAD], o[BOUNDS ? AHEAD : 1];
+    double x[AHEAD] = {};
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (p0 + k < n) {
+        r[k] = at[(p0 + k) * quads];
+        if constexpr (BOUNDS)
+          if (p0 + k > 0) o[k] = ot[(P - p0 - k) * quads];
+      }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (p0 + k < n) {
+        at[(p0 + k) * quads] = s;
+        if constexpr (BOUNDS)
+          if (p0 + k > 0) x[k] = dot(s, o[k]);
+        s = s * expf((float)w.decay[bh * P + p0 + k]) + r[k];
+      }
+    if constexpr (BOUNDS) {
+#pragma unroll
+      for (int o2 = WAVE / 2; o2 > 0; o2 >>= 1)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) x[k] += __shfl_xor(x[k], o2, WAVE);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (p0 + k > 0 && p0 + k < n && threadIdx.x % WAVE == 0) bounds[((bh * P + P - p0 - k) * quads + q) / WAVE] = x[k];
+    }
+  }
+  if (w.end) {
+    w.end[bh * quads + q] = s;
+    if constexpr (BOUNDS) bound(0, other0 ? dot(s, other0[bh * quads + q]) : 0.0);
+  } else if (P > 0) {
+    at[(P - 1) * quads] = s;
+    if constexpr (BOUNDS) {
+      bound(1, dot(s, ot[quads]));
+      bound(0, 0.0);
+    }
+  }
+}
+
+template <bool FORWARD, bool REVERSE, bool BOUNDS>
+__global__ __launch_bounds__(256) void combine_kernel(int P, long quads, long all, Walk forward, Walk reverse, double* bounds) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x, bh = i / quads, q = i % quads;
+  if (i >= all) return;  // whole wavefronts: a state is a multiple of 256 elements
+  if constexpr (FORWARD) walk<false>(forward, P, quads, bh, q, nullptr, nullptr, nullptr);
+  // the forward chain's starts are this lane's own
+  if constexpr (REVERSE) walk<BOUNDS>(reverse, P, quads, bh, q, forward.segs, forward.start, bounds);
 }
 
 // d log g of the tokens of one segment.  With b the inner product of the state before a chunk and its
@@ -60,26 +104,25 @@ __global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
   const long bh = blockIdx.x / p.P;
   const int h = (int)(bh % p.H);
   const long b = bh / p.H;
-  const float *S = nullptr, *G = nullptr;
-  if (seg > 0) {
-    S = p.segs + (bh * p.P + seg) * p.state;
-    G = p.gsegs + (bh * p.P + p.P - seg) * p.state;  // behind segment seg - 1, the reverse chain's P - seg
-  } else if (p.S0) {
-    S = p.S0 + bh * p.state;
-    G = p.dS0 + bh * p.state;
-  }
-  double x = 0.0;
-  if (S)
-    for (size_t i = 4 * tid; i < p.state; i += 4 * GATE_TH) {
-      const floatx4 s = *reinterpret_cast<const floatx4*>(S + i), d = *reinterpret_cast<const floatx4*>(G + i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x += (double)s[k] * d[k];
-    }
-  x = wave_total(x);
-  if (lane == 0) sums[wave] = x;
-  __syncthreads();
   double before = 0.0, all = 0.0;
-  for (int k = 0; k < GATE_WAVES; ++k) before += sums[k];
+  if (p.P > 1) {
+    const int parts = lin_parts(p.dk, p.dv);
+    for (int k = lane; k < parts; k += WAVE) before += p.bounds[(bh * p.P + seg) * parts + k];
+    before = wave_total(before);
+  } else if (p.S0) {
+    const int size = p.dk * p.dv;
+    for (int i = 4 * tid; i < size; i += 4 * GATE_TH) {
+      const floatx4 s = *reinterpret_cast<const floatx4*>(p.S0 + bh * size + i), d = *reinterpret_cast<const floatx4*>(p.dS0 + bh * size + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) before += (double)s[k] * d[k];
+    }
+    before = wave_total(before);
+    if (lane == 0) sums[wave] = before;
+    __syncthreads();
+    before = 0.0;
+    for (int k = 0; k < GATE_WAVES; ++k) before += sums[k];
+    __syncthreads();
+  }
   const int first = seg * p.NS, count = min(p.NS, p.NT - first);
   auto token = [&](int n) { return n * p.C + lane; };
   auto gate = [&](int n) {
@@ -154,14 +197,16 @@ __global__ __launch_bounds__(WAVE) void gate_heads_kernel(int B, int H, int P, c
 
 // The gradient of rows that `share` consecutive heads read: their float32 parts added up in order, rounded once.
 template <typename E>
-__global__ __launch_bounds__(256) void share_kernel(const float* part, E* out, long quads, int share, int width) {
-  const long q = (long)blockIdx.x * 256 + threadIdx.x;
-  if (q >= quads) return;
-  const long i = q * 4, row = i / width;
-  const float* from = part + row * share * width + i % width;
+__global__ __launch_bounds__(256) void share_kernel(const float* dq_part, const float* dk_part, E* dq, E* dk, long quads, int share,
+                                                    int width) {
+  const long t = (long)blockIdx.x * 256 + threadIdx.x;
+  if (t >= 2 * quads) return;
+  const bool second = t >= quads;
+  const long i = (second ? t - quads : t) * 4, row = i / width;
+  const float* from = (second ? dk_part : dq_part) + row * share * width + i % width;
   floatx4 s = *reinterpret_cast<const floatx4*>(from);
   for (int k = 1; k < share; ++k) s += *reinterpret_cast<const floatx4*>(from + (long)k * width);
-  store4<E>(out + i, s[0], s[1], s[2], s[3]);
+  store4<E>((second ? dk : dq) + i, s[0], s[1], s[2], s[3]);
 }
 
 // One token: S <- a S + k v^T, o = scale S^T q.  Bound by the state, read and written once: a workgroup has
@@ -232,34 +277,50 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 
 }  // namespace
 
-// Segments of a sequence: about two workgroups of a chain for each of 256 compute units, none split where the
-// sequences and heads alone fill the card.
-void lin_split(int B, int L, int H, int dv, bool bf16, int& NT, int& P, int& NS) {
+// Segments of a sequence, of NS chunks each.  A segment's chunks follow one another, so a call takes some time for each
+// chunk of a segment; and it moves four states (backward: twelve, three chains being side by side) for each segment of
+// each sequence and head.  The sum of the two is least where NS goes with the square root of (heads x chunks); the
+// factors are measured (us, 128 x 128 states, NS under and over the rule's in brackets): forward 4 x 8 heads of 2K tokens
+// 59 (2: 66, 8: 78), 2 x 16 of 8K 125 (4: 174, 16: 156); backward 4 x 8 of 2K 129 (4: 129, 16: 203), 8 x 8 of 777 130
+// (4: 140, 13: 138), 8 x 16 of 512 94 (4: 132), 1 of 4K 65 (1: 80, 4: 74).  A forward chain's workgroups all run at once,
+// two to a compute unit (float32: one): more would take a second round (64K tokens of 16 heads, 512 workgroups 417, 1024
+// 528), and where heads alone fill the compute units a summary is not worth its reads (256 heads of 1K 111, split in two 132).
+void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS) {
   const int C = lin_chunk(bf16);
   NT = (L + C - 1) / C;
-  const long units = (long)B * H * ((dv + LIN_SLAB - 1) / LIN_SLAB);
-  if (NT == 0 || units == 0 || units >= 256) {
+  const long units = (long)B * H * (backward ? 1 : (dv + LIN_SLAB - 1) / LIN_SLAB);
+  if (NT == 0 || units == 0 || (!backward && units >= 256)) {
     P = NT > 0, NS = NT;
     return;
   }
-  const long want = (512 + units - 1) / units;
-  NS = (int)((NT + want - 1) / want);
+  const double ns = sqrt((double)units * NT / (backward ? 16 : 64));
+  NS = ns >= NT ? NT : ns < 1.5 ? 1 : (int)(ns + 0.5);
+  if (!backward) {
+    const long most = (bf16 ? 512 : 256) / units;  // at least 1
+    if ((NT + NS - 1) / NS > most) NS = (int)((NT + most - 1) / most);
+  }
+  P = (NT + NS - 1) / NS;
+  NS = (NT + P - 1) / P;  // as even as that many segments can be
   P = (NT + NS - 1) / NS;
 }
 
-hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st) {
-  return bf16 ? lin::chain_bf16(c, reverse, form, st) : lin::chain_f32(c, reverse, form, st);
-}
-
-hipError_t launch_lin_summary(const LinChain& c, bool bf16, bool reverse, hipStream_t st) {
-  if (c.run > 0) {
-    const hipError_t e = bf16 ? lin::summary_bf16(c, reverse, st) : lin::summary_f32(c, reverse, st);
-    if (e != hipSuccess) return e;
-  }
+hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, double* bounds, hipStream_t st) {
+  const LinChain& c = forward ? *forward : *reverse;
   const long quads = (long)c.y.width * c.z.width / 4, all = quads * c.B * c.H;
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, st, c.P, quads, all,
-                     reinterpret_cast<const floatx4*>(c.start), reinterpret_cast<floatx4*>(c.segs), c.decay,
-                     reinterpret_cast<floatx4*>(c.end));
+  const dim3 grid((unsigned)((all + 255) / 256));
+  auto of = [](const LinChain* c) {
+    Walk w = {};
+    if (c) {
+      w.start = reinterpret_cast<const floatx4*>(c->start), w.segs = reinterpret_cast<floatx4*>(c->segs);
+      w.end = reinterpret_cast<floatx4*>(c->end), w.decay = c->decay;
+    }
+    return w;
+  };
+  const Walk f = of(forward), r = of(reverse);
+  if (!reverse) hipLaunchKernelGGL((combine_kernel<true, false, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
+  else if (!forward) hipLaunchKernelGGL((combine_kernel<false, true, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
+  else if (!bounds) hipLaunchKernelGGL((combine_kernel<true, true, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
+  else hipLaunchKernelGGL((combine_kernel<true, true, true>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
   return hipGetLastError();
 }
 
@@ -273,12 +334,16 @@ hipError_t launch_lin_gates(const LinGates& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_lin_share(const float* part, void* out, long rows, int heads, int share, int width, bool bf16_out,
-                            hipStream_t st) {
+hipError_t launch_lin_share(const float* dq_part, const float* dk_part, void* dq, void* dk, long rows, int heads, int share, int width,
+                            bool bf16_out, hipStream_t st) {
   const long quads = rows * heads * width / 4;
-  const dim3 grid((unsigned)((quads + 255) / 256));
-  if (bf16_out) hipLaunchKernelGGL((share_kernel<bf16>), grid, dim3(256), 0, st, part, static_cast<bf16*>(out), quads, share, width);
-  else hipLaunchKernelGGL((share_kernel<float>), grid, dim3(256), 0, st, part, static_cast<float*>(out), quads, share, width);
+  const dim3 grid((unsigned)((2 * quads + 255) / 256));
+  if (bf16_out)
+    hipLaunchKernelGGL((share_kernel<bf16>), grid, dim3(256), 0, st, dq_part, dk_part, static_cast<bf16*>(dq), static_cast<bf16*>(dk),
+                       quads, share, width);
+  else
+    hipLaunchKernelGGL((share_kernel<float>), grid, dim3(256), 0, st, dq_part, dk_part, static_cast<float*>(dq), static_cast<float*>(dk),
+                       quads, share, width);
   return hipGetLastError();
 }
 

@@ -26,7 +26,7 @@ struct Lin {
   size_t nqk, nv, ng, state;  // bytes of q, of v, of the gates, of the states
 };
 
-int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, Lin& n) {
+int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, bool backward, Lin& n) {
   const int rc = check_shape(s);
   if (rc) return rc;
   if (s->n_h != 1 || qk_heads < 1 || s->H % qk_heads != 0 || s->L > (1 << 30)) return DELTA_ERR_BAD_SHAPE;
@@ -34,7 +34,7 @@ int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, Lin& n) {
   if ((long long)s->H * (s->dk > s->dv ? s->dk : s->dv) > (1LL << 20)) return DELTA_ERR_BAD_SHAPE;
   n.B = s->B, n.L = s->L, n.H = s->H, n.Hk = qk_heads, n.dk = s->dk, n.dv = s->dv, n.gate = gate;
   n.bf16 = s->dtype == DELTA_BF16, n.scale = s->scale;
-  delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, n.NT, n.P, n.NS);
+  delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, backward, n.NT, n.P, n.NS);
   const size_t tokens = (size_t)n.B * n.L, e = esize(s->dtype);
   n.nqk = n.H ? tokens * n.Hk * n.dk * e : 0, n.nv = tokens * n.H * n.dv * e;
   n.ng = 4 * (gate == DELTA_LIN_GATE_TOKEN ? tokens * n.H : gate == DELTA_LIN_GATE_HEAD ? (size_t)n.H : 0);
@@ -68,8 +68,8 @@ size_t carve(const Lin& n, void* base, FwdSpace& w) {
 
 struct BwdSpace {
   float *segs, *gsegs;
-  double *decay, *part;
-  float *e, *f, *dS0, *shared;
+  double *decay, *gdecay, *part, *bounds;
+  float *e, *f, *dS0, *dq, *dk;
 };
 size_t carve(const Lin& n, void* base, BwdSpace& w) {
   Carve c{static_cast<char*>(base)};
@@ -78,11 +78,14 @@ size_t carve(const Lin& n, void* base, BwdSpace& w) {
   w.segs = c.take<float>(split ? n.state * n.P : 0);
   w.gsegs = c.take<float>(split ? n.state * n.P : 0);
   w.decay = c.take<double>(split ? heads * n.P * 8 : 0);
+  w.gdecay = c.take<double>(split ? heads * n.P * 8 : 0);
   w.part = c.take<double>(n.gate == DELTA_LIN_GATE_HEAD ? heads * n.P * 8 : 0);
   w.e = c.take<float>(gates ? tokens : 0);
   w.f = c.take<float>(gates ? tokens : 0);
+  w.bounds = c.take<double>(gates && split ? heads * n.P * delta::lin_parts(n.dk, n.dv) * 8 : 0);
   w.dS0 = c.take<float>(gates && n.L > 0 ? n.state : 0);  // where the caller wants none
-  w.shared = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);
+  w.dq = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);  // parts of the heads that share
+  w.dk = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);
   return c.used;
 }
 
@@ -117,7 +120,7 @@ extern "C" {
 
 int delta_fwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, size_t* bytes) {
   Lin n;
-  const int rc = lin_shape(s, qk_heads, DELTA_LIN_GATE_NONE, n);
+  const int rc = lin_shape(s, qk_heads, DELTA_LIN_GATE_NONE, false, n);
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
   FwdSpace w;
@@ -129,7 +132,7 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
                   const float* g_log, const float* S0, void* O, float* S_final, void* workspace, size_t workspace_bytes,
                   void* stream) {
   Lin n;
-  int rc = lin_shape(s, qk_heads, gate, n);
+  int rc = lin_shape(s, qk_heads, gate, false, n);
   if (rc) return rc;
   if ((rc = check_pointers({q, k, v, O}, n.nv > 0))) return rc;
   if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
@@ -153,7 +156,8 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   c.out = O, c.out_f32 = !n.bf16;
   if (n.P != 1) {  // P = 0: no tokens, the state as it is
     c.run = S_final ? n.P : n.P - 1;
-    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, false, st))) || n.P == 0) return rc;
+    if (n.P > 0 && (rc = hip_status(delta::launch_lin_summary(&c, nullptr, n.bf16, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_combine(&c, nullptr, nullptr, st))) || n.P == 0) return rc;
     c.run = n.P;
   }
   return hip_status(delta::launch_lin_chain(c, n.bf16, false, n.P == 1 && S_final ? delta::LIN_STATE : delta::LIN_PLAIN, st));
@@ -161,7 +165,7 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
 
 int delta_bwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, int32_t gate, size_t* bytes) {
   Lin n;
-  const int rc = lin_shape(s, qk_heads, gate, n);
+  const int rc = lin_shape(s, qk_heads, gate, true, n);
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
   BwdSpace w;
@@ -173,7 +177,7 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
                   const float* g_log, const float* S0, const void* dO, const float* dS_final, void* dq, void* dk, void* dv,
                   float* dg_log, float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
   Lin n;
-  int rc = lin_shape(s, qk_heads, gate, n);
+  int rc = lin_shape(s, qk_heads, gate, true, n);
   if (rc) return rc;
   if ((rc = check_pointers({q, k, v, dO, dq, dk, dv}, n.nv > 0))) return rc;
   if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
@@ -196,15 +200,15 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   LinGates gp;
   memset(&gp, 0, sizeof(gp));
   gp.B = n.B, gp.L = n.L, gp.H = n.H, gp.C = delta::lin_chunk(n.bf16), gp.NT = n.NT, gp.P = n.P, gp.NS = n.NS;
-  gp.state = (size_t)n.dk * n.dv, gp.e = w.e, gp.f = w.f, gp.S0 = S0, gp.segs = w.segs, gp.gsegs = w.gsegs;
-  gp.g = g_log, gp.gate = gate, gp.dg = dg_log, gp.part = w.part;
+  gp.dk = n.dk, gp.dv = n.dv, gp.e = w.e, gp.f = w.f, gp.bounds = w.bounds;
   if (dg_log && S0 && !dS0) dS0 = w.dS0;
-  gp.dS0 = dS0;
+  gp.S0 = S0, gp.dS0 = dS0;
+  gp.g = g_log, gp.gate = gate, gp.dg = dg_log, gp.part = w.part;
   if (n.state == 0 || n.L == 0) {
     if (n.state > 0 && dS0) {
       LinChain c = chain_of(n, g_log);
-      c.y.width = n.dk, c.z.width = n.dv, c.run = 0, c.start = dS_final, c.end = dS0;
-      if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, true, st)))) return rc;
+      c.y.width = n.dk, c.z.width = n.dv, c.start = dS_final, c.end = dS0;
+      if ((rc = hip_status(delta::launch_lin_combine(nullptr, &c, nullptr, st)))) return rc;
     }
     gp.B = 0;
     return sum_only ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
@@ -213,41 +217,40 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   const LinRole rq{q, n.Hk, n.dk}, rk{k, n.Hk, n.dk}, rv{v, n.H, n.dv}, ro{dO, n.H, n.dv};
   const bool shared = n.H != n.Hk;
   const long rows = (long)n.B * n.L;
-  // S: states from the start on, and dq = scale chain(dO, v, k) with the state transposed
-  LinChain c = chain_of(n, g_log);
-  c.segs = w.segs, c.decay = w.decay, c.start = S0;
+  // S: the states from the start on; dq = scale chain(dO, v, k) with them transposed.  G: their gradients from the end on;
+  // dv = chain(k, q, dO), and dk = chain(v, dO, q) with them transposed.
+  LinChain dqc = chain_of(n, g_log), dvc = dqc;
+  dqc.y = rk, dqc.z = rv, dqc.segs = w.segs, dqc.decay = w.decay, dqc.start = S0;
+  dvc.y = rq, dvc.z = ro, dvc.segs = w.gsegs, dvc.decay = w.gdecay, dvc.start = dS_final, dvc.end = dS0;
+  dvc.write = dvc.inner = n.scale;
   if (n.P > 1) {
-    c.y = rk, c.z = rv, c.run = n.P - 1;
-    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, false, st)))) return rc;
-    c.run = n.P;
+    dqc.run = n.P - 1, dvc.run = dS0 ? n.P : n.P - 1;
+    if ((rc = hip_status(delta::launch_lin_summary(&dqc, &dvc, n.bf16, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_combine(&dqc, &dvc, dg_log ? w.bounds : nullptr, st)))) return rc;
+    dqc.run = dvc.run = n.P;
   }
-  c.x = ro, c.y = rv, c.z = rk, c.w = rq, c.flip = true;
-  c.outer = c.inner = n.scale;
-  c.out = shared ? w.shared : dq, c.out_f32 = shared || !n.bf16, c.tok = w.e;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, false, dg_log ? delta::LIN_PAIRS : delta::LIN_PLAIN, st)))) return rc;
-  if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dq, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
-  // G: their gradients from the end on, and dv = chain(k, q, dO), dk = chain(v, dO, q)
-  c = chain_of(n, g_log);
-  c.segs = w.gsegs, c.decay = w.decay, c.start = dS_final, c.write = c.inner = n.scale;
-  c.y = rq, c.z = ro, c.end = dS0;
-  if (n.P > 1) {
-    c.run = dS0 ? n.P : n.P - 1;
-    if ((rc = hip_status(delta::launch_lin_summary(c, n.bf16, true, st)))) return rc;
-    c.run = n.P;
+  LinChain dkc = dvc;
+  dqc.x = ro, dqc.y = rv, dqc.z = rk, dqc.w = rq, dqc.flip = true, dqc.outer = dqc.inner = n.scale, dqc.tok = w.e;
+  dkc.x = rv, dkc.y = ro, dkc.z = rq, dkc.w = rk, dkc.flip = true, dkc.end = nullptr, dkc.tok = w.f;
+  dvc.x = rk;
+  dqc.out = shared ? w.dq : dq, dkc.out = shared ? w.dk : dk, dvc.out = dv;
+  dqc.out_f32 = dkc.out_f32 = shared || !n.bf16, dvc.out_f32 = !n.bf16;
+  const bool state = n.P == 1 && dS0;
+  if (n.dv <= 128) {
+    if ((rc = hip_status(delta::launch_lin_backward(dqc, dvc, dkc, dg_log != nullptr, state, n.bf16, st)))) return rc;
+  } else {
+    if ((rc = hip_status(delta::launch_lin_chain(dqc, n.bf16, false, dg_log ? delta::LIN_PAIRS : delta::LIN_PLAIN, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_chain(dvc, n.bf16, true, state ? delta::LIN_STATE : delta::LIN_PLAIN, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_chain(dkc, n.bf16, true, dg_log ? delta::LIN_SUMS : delta::LIN_PLAIN, st)))) return rc;
   }
-  c.x = rk, c.out = dv, c.out_f32 = !n.bf16;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, n.P == 1 && dS0 ? delta::LIN_STATE : delta::LIN_PLAIN, st)))) return rc;
-  c.x = rv, c.y = ro, c.z = rq, c.w = rk, c.flip = true, c.end = nullptr;
-  c.out = shared ? w.shared : dk, c.out_f32 = shared || !n.bf16, c.tok = w.f;
-  if ((rc = hip_status(delta::launch_lin_chain(c, n.bf16, true, dg_log ? delta::LIN_SUMS : delta::LIN_PLAIN, st)))) return rc;
-  if (shared && (rc = hip_status(delta::launch_lin_share(w.shared, dk, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
+  if (shared && (rc = hip_status(delta::launch_lin_share(w.dq, w.dk, dq, dk, rows, n.Hk, n.H / n.Hk, n.dk, n.bf16, st)))) return rc;
   return dg_log ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
 }
 
 int delta_decode_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const void* q, const void* k, const void* v,
                      const float* g_log, float* S, void* O, void* stream) {
   Lin n;
-  int rc = lin_shape(s, qk_heads, gate, n);
+  int rc = lin_shape(s, qk_heads, gate, false, n);
   if (rc) return rc;
   if (s->L != 1) return DELTA_ERR_BAD_SHAPE;
   if ((rc = check_pointers({q, k, v, S, O}, n.nv > 0))) return rc;

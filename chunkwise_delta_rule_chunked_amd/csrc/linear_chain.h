@@ -82,23 +82,34 @@ struct Rows {
   }
 };
 
-// Eight float32 values as `terms` operands whose sum they are to within 2^-9 of the last one's step: bf16
-// products of the terms carry float32 values to 2^-17 (two terms) or 2^-26 (three).
+// Eight float32 values as operands whose sum they are: bf16 takes three terms of eight bits of the mantissa each, cut
+// off one after another, which is exact; one term is rounded to nearest.  (Two would be good to 2^-16.)
 template <typename E, int TERMS>
 struct Split;
 template <int TERMS>
 struct Split<bf16, TERMS> {
   Frag<bf16> t[TERMS];
   __device__ inline void set(const float* x) {
+    if constexpr (TERMS == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float r = x[i];
+      for (int i = 0; i < 8; ++i) t[0].v[i] = (bf16)x[i];
+    } else {
+      u32x4 w[TERMS];
 #pragma unroll
-      for (int k = 0; k < TERMS; ++k) {
-        t[k].v[i] = (bf16)r;
-        if (k + 1 < TERMS) r -= (float)t[k].v[i];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a = __builtin_bit_cast(uint32_t, x[2 * i]), b = __builtin_bit_cast(uint32_t, x[2 * i + 1]);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+          w[k][i] = __builtin_amdgcn_perm(b, a, 0x07060302);  // the upper halves
+          if (k + 1 < TERMS) a = rest(a), b = rest(b);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k) t[k].v = __builtin_bit_cast(bf16x8, w[k]);
     }
+  }
+  static __device__ inline uint32_t rest(uint32_t x) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, x) - __builtin_bit_cast(float, x & 0xffff0000u));
   }
 };
 template <int TERMS>
@@ -112,6 +123,22 @@ struct Split<float, TERMS> {
 template <typename E>
 constexpr int terms(int n) {
   return sizeof(E) == 2 ? n : 1;
+}
+
+// The sum of the four lanes l % 16, + 16, + 32, + 48, in each of them: a product with ones, which costs no LDS access.
+__device__ inline float sum_groups(float x) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(1.f, x, floatx4{}, 0, 0, 0)[0];
+}
+// The sum over a group of 16 lanes, in each of them.
+template <int CTRL>
+__device__ inline float add_dpp(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ inline float sum_row(float x) {
+  x = add_dpp<0xb1>(x);    // lanes 1, 0, 3, 2 of each four
+  x = add_dpp<0x4e>(x);    // 2, 3, 0, 1
+  x = add_dpp<0x141>(x);   // mirrored in each eight
+  return add_dpp<0x140>(x);  // and in all sixteen
 }
 
 template <int N>
@@ -138,13 +165,15 @@ struct Config {
   static constexpr int X = 0, Y = X + (SUM ? 0 : C * KW * (int)sizeof(E)), Z = Y + C * KW * (int)sizeof(E),
                        W = Z + C * VW * (int)sizeof(E), A = W + (hooked(FORM) ? C * VW * (int)sizeof(E) : 0),
                        TAB = A + (SUM ? 0 : C * C * (int)sizeof(E));
-  static constexpr int TABLE = 4 * C * 4 + 16;  // sums of log gates (64 bits), x's and y's factors, the chunk's
+  // A chunk's gate tables: sums of log gates (64 bits); x's and y's factors; decays of a token since the block of 16 it
+  // is in, and from it to each later block; the chunk's
+  static constexpr int BACK = 16 * (NB * (NB - 1) / 2), TABLE = 4 * (5 * C + BACK) + 16;
   static constexpr int PART = TAB + 2 * TABLE, PARTS = FORM == PAIRS ? NW + 2 * NB : FORM == SUMS ? NW : 0;
   static constexpr int LDS = PART + PARTS * C * 4;
 };
 
 template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
-__global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) == 2 ? 2 : 1) void chain_kernel(LinChain p) {
+__device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
   constexpr int C = K::C, NB = K::NB, VW = K::VW, NT = K::NT, NU = K::NU, VEC = K::VEC, TH = K::TH;
   constexpr bool HOOK = hooked(FORM);
@@ -162,8 +191,8 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = p.z.width / 16, slabs = (tiles + NW * CT - 1) / (NW * CT), per = (tiles + slabs - 1) / slabs;
-  const int slab = blockIdx.x % slabs, seg = blockIdx.x / slabs % p.run;
-  const long bh = blockIdx.x / slabs / p.run;
+  const int slab = block % slabs, seg = block / slabs % p.run;
+  const long bh = block / slabs / p.run;
   const int h = (int)(bh % p.H);
   const long b = bh / p.H;
   const int c0 = 16 * per * slab, cols = min(16 * per, p.z.width - c0);  // columns of this workgroup
@@ -239,16 +268,17 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
     asm volatile("" : "+v"(gate));  // waited for here, not behind the next chunk's loads
   };
 
-  // ---- a chunk's gate tables, by one wavefront: gc log2 e, x's factors, y's factors, the chunk's
+  // ---- a chunk's gate tables, by one wavefront (gc as a power of two)
   struct Table {
-    const double* gc;
-    const float *fx, *fy, *whole;
+    double* gc;
+    float *fx, *fy, *in, *back, *whole;
   };
   auto table = [&](int i) {
     char* t = smem + K::TAB + (i & 1) * K::TABLE;
-    return Table{reinterpret_cast<double*>(t), reinterpret_cast<float*>(t + 8 * C), reinterpret_cast<float*>(t + 12 * C),
-                 reinterpret_cast<float*>(t + 16 * C)};
+    float* f = reinterpret_cast<float*>(t + 8 * C);
+    return Table{reinterpret_cast<double*>(t), f, f + C, f + 2 * C, f + 3 * C, f + 3 * C + K::BACK};
   };
+  auto back_of = [](int hi) { return 8 * hi * (hi - 1); };  // where the decays to block hi begin
   double sum = 0.0;  // log gates of the chunks so far (keeper)
   auto tables = [&](int i, float gl) {
     double a = (double)(gl < LOG_GATE_FLOOR ? LOG_GATE_FLOOR : gl);
@@ -261,12 +291,19 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
     sum += last;
     const Table t = table(i);
     const float begin = expf((float)a), end = expf((float)(last - a));
+    const double ref = __shfl(a, max(16 * (lane >> 4) - 1, 0), WAVE);
     if (lane < C) {
-      const_cast<double*>(t.gc)[lane] = a * 1.4426950408889634074;
-      const_cast<float*>(t.fx)[lane] = (REV ? end : begin) * p.outer;
-      const_cast<float*>(t.fy)[lane] = (REV ? begin : end) * p.write;
+      t.gc[lane] = a * 1.4426950408889634074;
+      t.fx[lane] = (REV ? end : begin) * p.outer;
+      t.fy[lane] = (REV ? begin : end) * p.write;
+      t.in[lane] = expf((float)(lane < 16 ? a : a - ref));
     }
-    if (lane == 0) *const_cast<float*>(t.whole) = expf((float)last);
+#pragma unroll
+    for (int hi = 1; hi < NB; ++hi) {
+      const float to = expf((float)(__shfl(a, 16 * hi - 1, WAVE) - a));
+      if (lane < 16 * hi) t.back[back_of(hi) + lane] = to;
+    }
+    if (lane == 0) *t.whole = expf((float)last);
   };
 
   // ---- the state: rows srow(t, 4 g + j) of column m of this wavefront's tiles
@@ -290,6 +327,8 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
         }
       }
   };
+  const float first_gate = keeper ? gate_of(0) : 0.f;
+  load_all(0);  // under way while the state is loaded
   const float* from = SUM ? nullptr : p.P > 1 ? p.segs + (bh * p.P + seg) * size : p.start ? p.start + bh * size : nullptr;
   const __amdgpu_buffer_rsrc_t start = buffer_rsrc(const_cast<float*>(from), from ? size * 4 : 0);  // else all 0
   if constexpr (SUM) {
@@ -307,8 +346,7 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
     for (int i = tid; i < C * C; i += TH) at[i] = (E)0.f;
   for (int i = tid; i < K::PARTS * C; i += TH) part[i] = 0.f;
 
-  if (keeper) tables(0, gate_of(0));
-  load_all(0);
+  if (keeper) tables(0, first_gate);
   put_all();
   float next = gate;  // gates of the chunk whose tables come next
   if (count > 1) load_all(1);
@@ -343,30 +381,34 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
                 d2 = mma(RZ::row(zt + 16 * jb * VW, m, 32 * u + 8 * g4), RZ::row(wt + 16 * ib * VW, m, 32 * u + 8 * g4), d2);
           }
           const int ti = 16 * ib + m, tj = 16 * jb + 4 * g4;
-          const double gi = tab.gc[ti];
-          float v[4], row = 0.f;
+          float v[4];
+          if (hi == lo) {
+            const double gi = tab.gc[ti];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const double e = REV ? tab.gc[tj + r] - gi : gi - tab.gc[tj + r];
-            const bool on = REV ? tj + r >= ti : tj + r <= ti;
-            const float factor = p.inner * __builtin_amdgcn_exp2f(on ? (float)e : -INFINITY);
-            v[r] = on ? d[r] * factor : 0.f;
-            if constexpr (FORM == PAIRS) {
-              d2[r] = tj + r == ti ? 0.f : v[r] * d2[r];
-              row += d2[r];
+            for (int r = 0; r < 4; ++r) {
+              const double e = REV ? tab.gc[tj + r] - gi : gi - tab.gc[tj + r];
+              const bool on = REV ? tj + r >= ti : tj + r <= ti;
+              const float factor = p.inner * __builtin_amdgcn_exp2f(on ? (float)e : -INFINITY);
+              v[r] = on ? d[r] * factor : 0.f;
+              if constexpr (FORM == PAIRS) d2[r] = tj + r == ti ? 0.f : v[r] * d2[r];
+            }
+          } else {  // through the end of the block before hi: two decays
+            const float* back = tab.back + back_of(hi);
+            const float fi = p.inner * (REV ? back[ti] : tab.in[ti]);
+            const floatx4 fj = *reinterpret_cast<const floatx4*>((REV ? tab.in : back) + tj);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              v[r] = d[r] * (fi * fj[r]);
+              if constexpr (FORM == PAIRS) d2[r] *= v[r];
             }
           }
           store4<E>(at + RA::at(ti, tj), v[0], v[1], v[2], v[3]);
           if constexpr (FORM == PAIRS) {
-            row += __shfl_xor(row, 16, WAVE);
-            row += __shfl_xor(row, 32, WAVE);
+            const float row = sum_groups((d2[0] + d2[1]) + (d2[2] + d2[3]));
             if (g4 == 0) part[(NW + jb) * C + ti] = row;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-#pragma unroll
-              for (int o = 1; o < 16; o <<= 1) d2[r] += __shfl_xor(d2[r], o, WAVE);
-              if (m == 0) part[(NW + NB + ib) * C + tj + r] = d2[r];
-            }
+            for (int r = 0; r < 4; ++r) d2[r] = sum_row(d2[r]);
+            if (m == 0) *reinterpret_cast<floatx4*>(part + (NW + NB + ib) * C + tj) = d2;
           }
         }
       }
@@ -418,8 +460,7 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
 #pragma unroll
               for (int r = 0; r < 4; ++r) e += out[c][ib][r] * to_float(wr[r]);
             }
-            e += __shfl_xor(e, 16, WAVE);
-            e += __shfl_xor(e, 32, WAVE);
+            e = sum_groups(e);
             if (g4 == 0) part[wave * C + 16 * ib + m] = e;
           }
         }
@@ -520,53 +561,127 @@ __global__ __launch_bounds__(NW * WAVE, NW * CT == 8 && KW <= 128 && sizeof(E) =
   if (SUM && keeper && slab == 0 && lane == 0) p.decay[bh * p.P + seg] = sum;
 }
 
-template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
+// Wavefronts on a SIMD that the registers are shared out for: bf16 chains of up to 128 rows and 128 columns fit twice on
+// a compute unit.
+template <typename E, int KW, int NW, int CT>
+constexpr int waves() {
+  return NW * CT == 8 && KW <= 128 && sizeof(E) == 2 ? 2 : 1;
+}
+
+template <typename E, int KW, int NW, int CT, bool REV, int FORM>
+__global__ __launch_bounds__(NW * WAVE, (waves<E, KW, NW, CT>())) void chain_kernel(LinChain p) {
+  walk<E, KW, NW, CT, REV, FORM, false>(p, blockIdx.x);
+}
+
+// The summaries of one chain, or of a chain and one in the other order behind it.
+template <typename E, int KW, int CT>
+__global__ __launch_bounds__(4 * WAVE, (waves<E, KW, 4, CT>())) void summary_kernel(LinChain forward, LinChain reverse, unsigned split) {
+  if (blockIdx.x < split) walk<E, KW, 4, CT, false, PLAIN, true>(forward, blockIdx.x);
+  else walk<E, KW, 4, CT, true, PLAIN, true>(reverse, blockIdx.x - split);
+}
+
+// The three chains of a backward pass side by side: workgroups bound by products run next to ones bound by memory, and
+// there is one tail.  KQ, KV: the rows for q's and k's width, and for v's; LAST: dv's form, which may leave its state.
+template <typename E, int KQ, int KV, bool GATES, int LAST>
+__global__ __launch_bounds__(4 * WAVE, sizeof(E) == 2 ? 2 : 1) void backward_kernel(LinChain dq, LinChain dv, LinChain dk, unsigned first,
+                                                                               unsigned second) {
+  constexpr int CQ = KQ == 128 ? 2 : 1, CV = KV == 128 ? 2 : 1;
+  if (blockIdx.x < first) walk<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>(dq, blockIdx.x);
+  else if (blockIdx.x < second) walk<E, KV, 4, CQ, true, GATES ? SUMS : PLAIN, false>(dk, blockIdx.x - first);
+  else walk<E, KQ, 4, CV, true, LAST, false>(dv, blockIdx.x - second);
+}
+
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
+
+// Workgroups of a chain with 16 NW CT columns each.
+inline unsigned blocks(const LinChain& c, int tiles_each) {
+  const int tiles = c.z.width / 16;
+  return (unsigned)((long)c.B * c.H * c.run * ((tiles + tiles_each - 1) / tiles_each));
+}
+
+template <typename E, int KW, int NW, int CT, bool REV, int FORM>
 hipError_t run(const LinChain& c, hipStream_t st) {
-  typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
+  typedef Config<E, KW, NW, CT, REV, FORM, false> K;
   static_assert(K::LDS <= 160 * 1024, "a workgroup's LDS");
-  const int tiles = c.z.width / 16, slabs = (tiles + NW * CT - 1) / (NW * CT);
-  hipLaunchKernelGGL((chain_kernel<E, KW, NW, CT, REV, FORM, SUM>), dim3((unsigned)((long)c.B * c.H * c.run * slabs)), dim3(K::TH),
-                     K::LDS, st, c);
+  hipLaunchKernelGGL((chain_kernel<E, KW, NW, CT, REV, FORM>), dim3(blocks(c, NW * CT)), dim3(K::TH), K::LDS, st, c);
   return hipGetLastError();
 }
 
-// Workgroups of 64 or 128 columns, four wavefronts with one tile or two each; rows of 256 leave the registers of a
-// wavefront room for one tile.
-template <typename E, int KW, bool REV, int FORM, bool SUM>
+// Workgroups of 64 or 128 columns, four wavefronts with one tile or two each; states of 256 rows (the backward pass of
+// values of more than 128 channels) leave the registers of a wavefront room for one tile.
+template <typename E, int KW, bool REV, int FORM>
 hipError_t by_columns(const LinChain& c, hipStream_t st) {
-  if constexpr (KW == 256) return run<E, KW, 8, 1, REV, FORM, SUM>(c, st);
-  else return c.z.width <= 64 ? run<E, KW, 4, 1, REV, FORM, SUM>(c, st) : run<E, KW, 4, 2, REV, FORM, SUM>(c, st);
+  // a reverse chain alone is one of more columns than the three together take
+  if constexpr (!REV)
+    if (c.z.width <= 64) return run<E, KW, 4, 1, REV, FORM>(c, st);
+  return run<E, KW, 4, 2, REV, FORM>(c, st);
 }
 
-template <typename E, bool REV, int FORM, bool SUM>
+template <typename E, bool REV, int FORM>
 hipError_t by_width(const LinChain& c, hipStream_t st) {
   const int w = c.y.width;
-  if (w <= 32) return by_columns<E, 32, REV, FORM, SUM>(c, st);
-  if (w <= 64) return by_columns<E, 64, REV, FORM, SUM>(c, st);
-  if (w <= 128) return by_columns<E, 128, REV, FORM, SUM>(c, st);
-  if constexpr (!SUM) return by_columns<E, 256, REV, FORM, SUM>(c, st);
-  return hipErrorInvalidValue;
+  if (w <= 32) return by_columns<E, 32, REV, FORM>(c, st);
+  return w <= 64 ? by_columns<E, 64, REV, FORM>(c, st) : by_columns<E, 128, REV, FORM>(c, st);
 }
 
 template <typename E>
 hipError_t chain(const LinChain& c, bool reverse, int form, hipStream_t st) {
+  if (c.y.width > 128) {
+    switch (form) {
+      case PLAIN: return reverse ? run<E, 256, 8, 1, true, PLAIN>(c, st) : run<E, 256, 8, 1, false, PLAIN>(c, st);
+      case PAIRS: return run<E, 256, 8, 1, false, PAIRS>(c, st);
+      case SUMS: return run<E, 256, 8, 1, true, SUMS>(c, st);
+      default: return hipErrorInvalidValue;
+    }
+  }
   switch (form) {
-    case PLAIN: return reverse ? by_width<E, true, PLAIN, false>(c, st) : by_width<E, false, PLAIN, false>(c, st);
-    case STATE: return reverse ? by_width<E, true, STATE, false>(c, st) : by_width<E, false, STATE, false>(c, st);
-    case PAIRS: return by_width<E, false, PAIRS, false>(c, st);
-    case SUMS: return by_width<E, true, SUMS, false>(c, st);
+    case PLAIN: return reverse ? by_width<E, true, PLAIN>(c, st) : by_width<E, false, PLAIN>(c, st);
+    case STATE: return reverse ? by_width<E, true, STATE>(c, st) : by_width<E, false, STATE>(c, st);
     default: return hipErrorInvalidValue;
   }
 }
+
+template <typename E, int KW, int CT>
+hipError_t run_summary(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
+  const unsigned split = forward ? blocks(*forward, 4 * CT) : 0, all = split + (reverse ? blocks(*reverse, 4 * CT) : 0);
+  if (all == 0) return hipSuccess;
+  hipLaunchKernelGGL((summary_kernel<E, KW, CT>), dim3(all), dim3(4 * WAVE), (Config<E, KW, 4, CT, false, PLAIN, true>::LDS), st,
+                     forward ? *forward : *reverse, reverse ? *reverse : *forward, split);
+  return hipGetLastError();
+}
 template <typename E>
-hipError_t summary(const LinChain& c, bool reverse, hipStream_t st) {
-  return reverse ? by_width<E, true, PLAIN, true>(c, st) : by_width<E, false, PLAIN, true>(c, st);
+hipError_t summary(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
+  const LinChain& c = forward ? *forward : *reverse;
+  const int w = c.y.width;
+  const bool wide = c.z.width > 64;
+  if (w <= 32) return wide ? run_summary<E, 32, 2>(forward, reverse, st) : run_summary<E, 32, 1>(forward, reverse, st);
+  if (w <= 64) return wide ? run_summary<E, 64, 2>(forward, reverse, st) : run_summary<E, 64, 1>(forward, reverse, st);
+  return wide ? run_summary<E, 128, 2>(forward, reverse, st) : run_summary<E, 128, 1>(forward, reverse, st);
 }
 
-hipError_t chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
-hipError_t chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
-hipError_t summary_bf16(const LinChain& c, bool reverse, hipStream_t st);
-hipError_t summary_f32(const LinChain& c, bool reverse, hipStream_t st);
+template <typename E, int KQ, int KV, bool GATES, int LAST>
+hipError_t run_backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, hipStream_t st) {
+  constexpr int CQ = KQ == 128 ? 2 : 1, CV = KV == 128 ? 2 : 1;
+  constexpr int LDS = max_of(Config<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>::LDS, Config<E, KQ, 4, CV, true, LAST, false>::LDS);
+  const unsigned first = blocks(dq, 4 * CQ), second = first + blocks(dk, 4 * CQ);
+  hipLaunchKernelGGL((backward_kernel<E, KQ, KV, GATES, LAST>), dim3(second + blocks(dv, 4 * CV)), dim3(4 * WAVE), LDS, st, dq, dv,
+                     dk, first, second);
+  return hipGetLastError();
+}
+template <typename E, bool GATES, int LAST, int KQ>
+hipError_t backward_by_values(const LinChain& dq, const LinChain& dv, const LinChain& dk, hipStream_t st) {
+  if (dv.z.width <= 32) return run_backward<E, KQ, 32, GATES, LAST>(dq, dv, dk, st);
+  return dv.z.width <= 64 ? run_backward<E, KQ, 64, GATES, LAST>(dq, dv, dk, st) : run_backward<E, KQ, 128, GATES, LAST>(dq, dv, dk, st);
+}
+template <typename E, bool GATES, int LAST>
+hipError_t backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, hipStream_t st) {
+  if (dq.z.width <= 32) return backward_by_values<E, GATES, LAST, 32>(dq, dv, dk, st);
+  return dq.z.width <= 64 ? backward_by_values<E, GATES, LAST, 64>(dq, dv, dk, st) : backward_by_values<E, GATES, LAST, 128>(dq, dv, dk, st);
+}
+template <typename E, bool GATES>
+hipError_t backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool state, hipStream_t st) {
+  return state ? backward<E, GATES, STATE>(dq, dv, dk, st) : backward<E, GATES, PLAIN>(dq, dv, dk, st);
+}
 
 }  // namespace lin
 }  // namespace delta
