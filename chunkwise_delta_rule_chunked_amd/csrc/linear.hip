@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void combine_kernel(int P, long quads, long al
 //     b = X + sum e,   b' = X + sum f,   d log g_t = X + sum_{r < t} f_r + sum_{r >= t} e_r
 // (e with the pairs' row and column sums, which cancel over a chunk).  b is formed from the states at the
 // segment's start and carried on from chunk to chunk; a chunk that lets nothing through has X = 0.
-constexpr int GATE_TH = 256, GATE_WAVES = GATE_TH / WAVE, GATE_CHUNKS = 64;
+constexpr int GATE_TH = 1024, GATE_WAVES = GATE_TH / WAVE, GATE_CHUNKS = 64;
 __global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
   __shared__ double sums[GATE_WAVES], se[GATE_CHUNKS], sf[GATE_CHUNKS];
   __shared__ bool shut[GATE_CHUNKS];
