@@ -43,6 +43,15 @@ struct Dropper {
   uint64_t seed, offset, per_row;
   __device__ inline Dropper(const DropRule& r, int width)
       : drop(r.drop), scale(r.scale), seed(r.seed), offset(r.offset + (r.step ? *r.step : 0)), per_row((width + V - 1) / V) {}
+  // the kept channels of a vector, a bit each, and what becomes of one
+  __device__ inline unsigned mask(long row, int vec) const {
+    const Bits b = random_bits(row * per_row + vec, offset, seed);
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) m |= b.keep(e, drop) ? 1u << e : 0u;
+    return m;
+  }
+  __device__ inline float apply(unsigned mask, int e, float v) const { return mask >> e & 1 ? v * scale : 0.f; }
   __device__ inline void operator()(long row, int vec, float* v) const {
     const Bits b = random_bits(row * per_row + vec, offset, seed);
 #pragma unroll
@@ -50,8 +59,10 @@ struct Dropper {
   }
 };
 
-// N sums over the LANES lanes of a row; `slot`: which row of the workgroup's.  All slots of a workgroup take
-// every step together; `lds` has a place per sum and wavefront.
+// N sums over the LANES lanes of a row; `slot`: which row of the workgroup's.  All slots of a workgroup take every
+// step together; `lds` has a place per sum and wavefront and is another one for each of a row's steps, so that one
+// barrier does: a place is written again behind the barrier of the step that came after its reads.  The barriers wait
+// for LDS alone, not for the loads and stores of rows.
 template <int LANES, int N, int W>
 __device__ inline void row_totals(float (&x)[N], int slot, float (*lds)[W]) {
 #pragma unroll
@@ -59,11 +70,10 @@ __device__ inline void row_totals(float (&x)[N], int slot, float (*lds)[W]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] += __shfl_xor(x[i], o, WAVE);
   if constexpr (LANES > WAVE) {
-    __syncthreads();
     if (threadIdx.x % WAVE == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) lds[i][threadIdx.x / WAVE] = x[i];
-    __syncthreads();
+    barrier_lds();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       x[i] = 0.f;
@@ -88,7 +98,7 @@ template <typename E, int LANES, int J, bool DROP>
 __global__ __launch_bounds__(threads(LANES)) void layernorm_kernel(LayernormParams p) {
   constexpr int T = threads(LANES), RPW = T / LANES;
   constexpr bool KEEP = J == 1;  // weight and bias stay in registers
-  __shared__ float lds[2][T / WAVE];
+  __shared__ float lds[3][T / WAVE];
   const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
   const Dropper dropper(p.rule, p.width);
   float w[KEEP ? J : 1][V], b[KEEP ? J : 1][V] = {};
@@ -101,18 +111,27 @@ __global__ __launch_bounds__(threads(LANES)) void layernorm_kernel(LayernormPara
     const long row = row0 + slot, base = row * p.width;
     const bool ok = row < p.rows;
     float s[J][V], total[1] = {0.f};
+    Raw8<E> x[J], r[J];
+    unsigned keep[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
-      load8<true>(static_cast<const E*>(p.x) + base + i, n, s[j]);
-      float r[V] = {};
-      if (p.res) load8<true>(static_cast<const E*>(p.res) + base + i, n, r);
-      if constexpr (DROP) dropper(row, lane + j * LANES, s[j]);
-      if (p.sum) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[j][e] = to_float(to_elem<E>(s[j][e] + r[e]));
-      }
+      x[j].load(static_cast<const E*>(p.x) + base + i, n);
+      r[j].load(static_cast<const E*>(p.res) + base + i, p.res ? n : 0);
     }
+    if constexpr (DROP) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) keep[j] = dropper.mask(row, lane + j * LANES);  // while the loads are under way
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s[j][e] = x[j][e];
+        if constexpr (DROP) s[j][e] = dropper.apply(keep[j], e, s[j][e]);
+        if (p.sum) s[j][e] = to_float(to_elem<E>(s[j][e] + r[j][e]));
+      }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
@@ -133,7 +152,7 @@ __global__ __launch_bounds__(threads(LANES)) void layernorm_kernel(LayernormPara
         sums[1] += s[j][e] * s[j][e];
       }
     }
-    row_totals<LANES>(sums, slot, lds);
+    row_totals<LANES>(sums, slot, lds + 1);
     const Stats t(sums[0], sums[1], p.width, p.eps);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -153,7 +172,7 @@ __global__ __launch_bounds__(threads(LANES)) void layernorm_kernel(LayernormPara
 template <typename E, bool DROP>
 __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LayernormParams p) {
   constexpr int T = 1024;
-  __shared__ float lds[2][T / WAVE];
+  __shared__ float lds[3][T / WAVE];
   const Dropper dropper(p.rule, p.width);
   const long row = blockIdx.x, base = row * p.width;
   float total[1] = {0.f};
@@ -184,7 +203,7 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LayernormParams p)
       sums[1] += d * d;
     }
   }
-  row_totals<T>(sums, 0, lds);
+  row_totals<T>(sums, 0, lds + 1);
   const Stats t(sums[0], sums[1], p.width, p.eps);
   for (int i = threadIdx.x * V; i < p.width; i += T * V) {
     float s[V], w[V], b[V] = {};
@@ -201,33 +220,68 @@ constexpr int bwd_threads(int lanes) { return lanes > 512 ? lanes : 512; }
 
 // Workgroup k takes rows k RPW .., then gridDim.x * RPW further on, and stores its parts of dweight and dbias
 // in part[k] and part[gridDim.x + k].  Every part is the sum over a fixed set of rows in a fixed order.
+// WHOLE (rows of whole vectors, 16-byte aligned): the next step's rows are loaded ahead.
 // With z = (s - mean) rstd: ds = dsum + rstd (w dy - mean(w dy) - z mean(w dy z)), dweight = sum dy z,
 // dbias = sum dy.
-template <typename E, int LANES, int J, bool DROP>
-__global__ __launch_bounds__(bwd_threads(LANES)) void layernorm_bwd_kernel(LayernormParams p) {
+template <typename E, int LANES, int J, bool DROP, bool WHOLE>
+__global__ __launch_bounds__(bwd_threads(LANES), 4) void layernorm_bwd_kernel(LayernormParams p) {
   constexpr int T = bwd_threads(LANES), RPW = T / LANES, COLS = LANES * J * V;
   constexpr bool KEEP = J == 1;
-  __shared__ float lds[3][T / WAVE];
+  __shared__ float lds[5][T / WAVE];
   const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
   const Dropper dropper(p.rule, p.width);
   float w[KEEP ? J : 1][V], accw[J][V] = {}, accb[J][V] = {};
   if constexpr (KEEP) load8<false>(p.weight + lane * V, p.width - lane * V, w[0]);
-  for (long row0 = (long)blockIdx.x * RPW; row0 < p.rows; row0 += (long)gridDim.x * RPW) {
-    const long row = row0 + slot, base = row * p.width;
-    const bool ok = row < p.rows;
+  struct Row {
     Raw8<E> s[J], d[J], o[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
-      s[j].load(static_cast<const E*>(p.x) + base + i, n);
-      d[j].load(static_cast<const E*>(p.dy) + base + i, n);
-    }
-    if (p.dsum) {
+  };
+  // WHOLE: the rows of a step as one range of bytes; what is past it reads 0 and is not stored.  Without branches
+  // around them the loads of the next step's rows are under way while this one's sums meet and are waited for by count
+  // (16384 x 2048 bf16 69 to 62 us, 8192 x 2048 float32 63 to 53).
+  const int off = lane * V < p.width ? (slot * p.width + lane * V) * (int)sizeof(E) : 1 << 30;
+  auto window = [&](const void* q, long row0) {
+    const long left = p.rows - row0, n = q ? (left < RPW ? (left > 0 ? left : 0) : RPW) : 0;
+    return buffer_rsrc(static_cast<E*>(const_cast<void*>(q)) + row0 * p.width, (int)(n * p.width) * (int)sizeof(E));
+  };
+  auto fetch = [&](Row& r, long row0) {
+    if constexpr (WHOLE) {
+      r.s[0].load(window(p.x, row0), off);
+      r.d[0].load(window(p.dy, row0), off);
+      r.o[0].load(window(p.dsum, row0), off);
+    } else {
+      const long row = row0 + slot, base = row * p.width;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int i = (lane + j * LANES) * V;
-        o[j].load(static_cast<const E*>(p.dsum) + base + i, ok ? p.width - i : 0);
+        const int i = (lane + j * LANES) * V, n = row < p.rows ? p.width - i : 0;
+        r.s[j].load(static_cast<const E*>(p.x) + base + i, n);
+        r.d[j].load(static_cast<const E*>(p.dy) + base + i, n);
+        r.o[j].load(static_cast<const E*>(p.dsum) + base + i, p.dsum ? n : 0);
       }
+    }
+  };
+  const long stride = (long)gridDim.x * RPW;
+  Row now, next;
+  if constexpr (WHOLE) fetch(next, (long)blockIdx.x * RPW);
+  for (long row0 = (long)blockIdx.x * RPW; row0 < p.rows; row0 += stride) {
+    const long row = row0 + slot, base = row * p.width;
+    const bool ok = row < p.rows;
+    if constexpr (WHOLE) {
+      now = next;
+      fetch(next, row0 + stride);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      fetch(now, row0);
+    }
+    Raw8<E>(&s)[J] = now.s, (&d)[J] = now.d, (&o)[J] = now.o;
+    auto store = [&](void* q, int i, const float* v) {
+      if constexpr (WHOLE) buffer_store8(window(q, row0), off, v, E{});
+      else store8(static_cast<E*>(q) + base + i, ok ? p.width - i : 0, v);
+    };
+    unsigned keep[J];
+    if constexpr (DROP) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) keep[j] = dropper.mask(row, lane + j * LANES);  // while the loads are under way
+      __builtin_amdgcn_sched_barrier(0);
     }
     float first[2] = {0.f, 0.f};  // of s and of w dy
 #pragma unroll
@@ -238,6 +292,7 @@ __global__ __launch_bounds__(bwd_threads(LANES)) void layernorm_bwd_kernel(Layer
         first[0] += s[j][e];
         first[1] += w[0][e] * d[j][e];
       }
+      if constexpr (J > 1) s[j].again(), d[j].again();
     }
     row_totals<LANES>(first, slot, lds);
     const float mean = first[0] / p.width;
@@ -253,28 +308,30 @@ __global__ __launch_bounds__(bwd_threads(LANES)) void layernorm_bwd_kernel(Layer
         sums[1] += c * c;
         sums[2] += w[0][e] * d[j][e] * c;
       }
+      if constexpr (J > 1) s[j].again(), d[j].again();
     }
-    row_totals<LANES>(sums, slot, lds);
+    row_totals<LANES>(sums, slot, lds + 2);
     const Stats t(sums[0], sums[1], p.width, p.eps);
     const float c1 = first[1] / p.width, c2 = t.rstd * ((sums[2] - t.shift * first[1]) / p.width);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int i = (lane + j * LANES) * V, n = ok ? p.width - i : 0;
+      const int i = (lane + j * LANES) * V;
       if constexpr (!KEEP) load8<false>(p.weight + i, p.width - i, w[0]);
       float v[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float z = (s[j][e] - mean - t.shift) * t.rstd;
-        v[e] = (p.dsum ? o[j][e] : 0.f) + t.rstd * (w[0][e] * d[j][e] - c1 - z * c2);
+        v[e] = o[j][e] + t.rstd * (w[0][e] * d[j][e] - c1 - z * c2);
         if (ok) {  // a missing row's rstd is infinite for eps = 0
           accw[j][e] += d[j][e] * z;
           accb[j][e] += d[j][e];
         }
       }
-      store8(static_cast<E*>(p.dres) + base + i, n, v);
+      store(p.dres, i, v);
       if constexpr (DROP) {
-        dropper(row, lane + j * LANES, v);
-        store8(static_cast<E*>(p.dx) + base + i, n, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = dropper.apply(keep[j], e, v[e]);
+        store(p.dx, i, v);
       }
     }
   }
@@ -311,7 +368,7 @@ __global__ __launch_bounds__(bwd_threads(LANES)) void layernorm_bwd_kernel(Layer
 template <typename E, bool DROP>
 __global__ __launch_bounds__(1024) void layernorm_bwd_wide_kernel(LayernormParams p) {
   constexpr int T = 1024;
-  __shared__ float lds[3][T / WAVE];
+  __shared__ float lds[5][T / WAVE];
   const Dropper dropper(p.rule, p.width);
   float *partw = p.part + (long)blockIdx.x * p.width, *partb = p.part + ((long)gridDim.x + blockIdx.x) * p.width;
   bool begin = true;
@@ -342,7 +399,7 @@ __global__ __launch_bounds__(1024) void layernorm_bwd_wide_kernel(LayernormParam
         sums[2] += w[e] * d[e] * c;
       }
     }
-    row_totals<T>(sums, 0, lds);
+    row_totals<T>(sums, 0, lds + 2);
     const Stats t(sums[0], sums[1], p.width, p.eps);
     const float c1 = first[1] / p.width, c2 = t.rstd * ((sums[2] - t.shift * first[1]) / p.width);
     for (int i = threadIdx.x * V; i < p.width; i += T * V) {
@@ -434,31 +491,37 @@ __global__ __launch_bounds__(DROP_TH) void dropout_kernel(DropoutParams p) {
 }
 
 // Lanes and vectors per lane of a row (0: the kernels for any width), and the workgroups that walk over the rows
-// where those are many.
+// where those are many: enough that they do not all read, then all compute, then all write.  Forward with the mask,
+// at 2048 / 6144 of them: 16384 x 2048 bf16 55.0 / 46.4 us, 32768 x 1003 69.5 / 59.3 us; without it 48.4 / 46.5 and
+// 54.1 / 56.6.  Rows of 4096, at 1024 / 1536: 55.4 / 47.1 us.  Of two vectors a lane more do not help (52.0 / 54.4).
 struct RowSplit {
   int lanes, j, most;
 };
 RowSplit split(int width) {
-  if (width <= 64) return {8, 1, 2048};
-  if (width <= 128) return {16, 1, 2048};
-  if (width <= 256) return {32, 1, 2048};
-  if (width <= 512) return {64, 1, 2048};
-  if (width <= 1024) return {128, 1, 4096};
-  if (width <= 2048) return {256, 1, 2048};
-  if (width <= 4096) return {512, 1, 1024};
+  if (width <= 64) return {8, 1, 6144};
+  if (width <= 128) return {16, 1, 6144};
+  if (width <= 256) return {32, 1, 6144};
+  if (width <= 512) return {64, 1, 6144};
+  if (width <= 1024) return {128, 1, 12288};
+  if (width <= 2048) return {256, 1, 6144};
+  if (width <= 4096) return {512, 1, 1536};
   if (width <= 8192) return {512, 2, 1024};
   if (width <= 16384) return {1024, 2, 512};
   return {0, 0, 0};
 }
+// The backward pass keeps its parts of dweight and dbias for a workgroup's whole walk, so it has as many as the card
+// runs at once (16384 x 2048 bf16: 512 62 us, 384 71, 768 68).  One vector a lane as far as a workgroup reaches: two
+// leave no registers for the next row (4096 x 8192 bf16 in 1024 lanes 71 us, in 512 88; 3711 x 1003 float32 in 128
+// lanes 24 us, in 64 33).
 RowSplit split_bwd(int width) {
   if (width <= 64) return {8, 1, 512};
   if (width <= 128) return {16, 1, 512};
   if (width <= 256) return {32, 1, 512};
   if (width <= 512) return {64, 1, 512};
-  if (width <= 1024) return {64, 2, 512};
+  if (width <= 1024) return {128, 1, 512};
   if (width <= 2048) return {256, 1, 512};
   if (width <= 4096) return {512, 1, 512};
-  if (width <= 8192) return {512, 2, 512};
+  if (width <= 8192) return {1024, 1, 256};
   if (width <= 16384) return {1024, 2, 256};
   return {0, 0, 256};
 }
@@ -483,9 +546,10 @@ hipError_t launch_rows(const LayernormParams& p, hipStream_t st) {
   case L * 16 + J:                                                                                  \
     hipLaunchKernelGGL((layernorm_kernel<E, L, J, DROP>), grid, dim3(threads(L)), 0, st, p);        \
     break;
-#define DELTA_ROWS_CASES(M) M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(256, 1) M(512, 1) M(512, 2) M(1024, 2)
-    DELTA_ROWS_CASES(DELTA_ROWS_CASE)
-    DELTA_ROWS_CASE(128, 1)
+#define DELTA_ROWS_ONES(M) M(8, 1) M(16, 1) M(32, 1) M(64, 1) M(128, 1) M(256, 1) M(512, 1)
+    DELTA_ROWS_ONES(DELTA_ROWS_CASE)
+    DELTA_ROWS_CASE(512, 2)
+    DELTA_ROWS_CASE(1024, 2)
 #undef DELTA_ROWS_CASE
     default: return hipErrorInvalidValue;
   }
@@ -496,15 +560,26 @@ template <typename E, bool DROP>
 hipError_t launch_rows_bwd(const LayernormParams& p, hipStream_t st) {
   const RowSplit s = split_bwd(p.width);
   const dim3 grid((unsigned)layernorm_bwd_parts(p.rows, p.width));
-  switch (s.lanes * 16 + s.j) {
-#define DELTA_ROWS_CASE(L, J)                                                                           \
-  case L * 16 + J:                                                                                      \
-    hipLaunchKernelGGL((layernorm_bwd_kernel<E, L, J, DROP>), grid, dim3(bwd_threads(L)), 0, st, p);    \
+  const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.dy | (uintptr_t)p.dsum | (uintptr_t)p.dres | (uintptr_t)p.dx;
+  // within a wavefront there is no barrier to wait at, and the next row's registers cost more than they give
+  // (65536 x 512 bf16: 51 us as it is, 55 with them)
+  const bool whole = p.width % V == 0 && at % 16 == 0 && s.lanes > WAVE && s.j == 1;
+  switch ((s.lanes * 16 + s.j) * 2 + whole) {
+#define DELTA_ROWS_CASE(L, J, W)                                                                          \
+  case (L * 16 + J) * 2 + W:                                                                              \
+    hipLaunchKernelGGL((layernorm_bwd_kernel<E, L, J, DROP, W>), grid, dim3(bwd_threads(L)), 0, st, p);   \
     break;
-    DELTA_ROWS_CASES(DELTA_ROWS_CASE)
-    DELTA_ROWS_CASE(64, 2)
+#define DELTA_ROWS_ONE(L, J) DELTA_ROWS_CASE(L, J, false)
+    DELTA_ROWS_ONES(DELTA_ROWS_ONE)
+    DELTA_ROWS_CASE(128, 1, true)
+    DELTA_ROWS_CASE(256, 1, true)
+    DELTA_ROWS_CASE(512, 1, true)
+    DELTA_ROWS_CASE(1024, 1, true)
+    DELTA_ROWS_CASE(1024, 1, false)
+    DELTA_ROWS_CASE(1024, 2, false)
+#undef DELTA_ROWS_ONE
 #undef DELTA_ROWS_CASE
-#undef DELTA_ROWS_CASES
+#undef DELTA_ROWS_ONES
     case 0: hipLaunchKernelGGL((layernorm_bwd_wide_kernel<E, DROP>), grid, dim3(1024), 0, st, p); break;
     default: return hipErrorInvalidValue;
   }

@@ -110,6 +110,19 @@ __device__ inline void store8(float* p, int n, const float* v) {
     store_part(p, n, r);
   }
 }
+// eight channels at a byte of a range, outside of which nothing is stored
+__device__ inline void buffer_store8(__amdgpu_buffer_rsrc_t b, int off, const float* v, bf16) {
+  bf16 r[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) r[e] = to_elem<bf16>(v[e]);
+  floatx4 q;
+  __builtin_memcpy(&q, r, 16);
+  buffer_store16(b, off, q);
+}
+__device__ inline void buffer_store8(__amdgpu_buffer_rsrc_t b, int off, const float* v, float) {
+  buffer_store16(b, off, floatx4{v[0], v[1], v[2], v[3]});
+  buffer_store16(b, off + 16, floatx4{v[4], v[5], v[6], v[7]});
+}
 __device__ inline void store8_e4m3(uint8_t* p, int n, const float* v) {
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
@@ -167,6 +180,7 @@ struct Raw8;
 template <>
 struct Raw8<bf16> {
   u32x4 r;
+  __device__ inline void load(__amdgpu_buffer_rsrc_t b, int off) { r = buffer_load16(b, off); }
   __device__ inline void load(const bf16* p, int n) {
     r = u32x4{};
     if (n >= V) {
@@ -190,6 +204,14 @@ struct Raw8<bf16> {
 template <>
 struct Raw8<float> {
   float v[V];
+  __device__ inline void load(__amdgpu_buffer_rsrc_t b, int off) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const floatx4 q = __builtin_bit_cast(floatx4, buffer_load16(b, off + 16 * h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * h + e] = q[e];
+    }
+  }
   __device__ inline void load(const float* p, int n) { load8<true>(p, n, v); }
   __device__ inline float operator[](int e) const { return v[e]; }
   __device__ inline void again() {}
