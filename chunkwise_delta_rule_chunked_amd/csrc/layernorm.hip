@@ -174,45 +174,47 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LayernormParams p)
   constexpr int T = 1024;
   __shared__ float lds[3][T / WAVE];
   const Dropper dropper(p.rule, p.width);
-  const long row = blockIdx.x, base = row * p.width;
-  float total[1] = {0.f};
-  for (int i = threadIdx.x * V; i < p.width; i += T * V) {
-    float s[V], r[V] = {};
-    load8<false>(static_cast<const E*>(p.x) + base + i, p.width - i, s);
-    if (p.res) load8<false>(static_cast<const E*>(p.res) + base + i, p.width - i, r);
-    if constexpr (DROP) dropper(row, i / V, s);
-    if (p.sum) {
+  for (long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const long base = row * p.width;
+    float total[1] = {0.f};
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float s[V], r[V] = {};
+      load8<false>(static_cast<const E*>(p.x) + base + i, p.width - i, s);
+      if (p.res) load8<false>(static_cast<const E*>(p.res) + base + i, p.width - i, r);
+      if constexpr (DROP) dropper(row, i / V, s);
+      if (p.sum) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[e] = to_float(to_elem<E>(s[e] + r[e]));
-      store8(static_cast<E*>(p.sum) + base + i, p.width - i, s);
+        for (int e = 0; e < V; ++e) s[e] = to_float(to_elem<E>(s[e] + r[e]));
+        store8(static_cast<E*>(p.sum) + base + i, p.width - i, s);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) total[0] += i + e < p.width ? s[e] : 0.f;
     }
+    row_totals<T>(total, 0, lds);
+    const float mean = total[0] / p.width;
+    const E* s0 = static_cast<const E*>(p.sum ? p.sum : p.x) + base;  // what this thread itself wrote
+    float sums[2] = {0.f, 0.f};
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float s[V];
+      load8<false>(s0 + i, p.width - i, s);
 #pragma unroll
-    for (int e = 0; e < V; ++e) total[0] += i + e < p.width ? s[e] : 0.f;
-  }
-  row_totals<T>(total, 0, lds);
-  const float mean = total[0] / p.width;
-  const E* s0 = static_cast<const E*>(p.sum ? p.sum : p.x) + base;  // what this thread itself wrote
-  float sums[2] = {0.f, 0.f};
-  for (int i = threadIdx.x * V; i < p.width; i += T * V) {
-    float s[V];
-    load8<false>(s0 + i, p.width - i, s);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float d = i + e < p.width ? s[e] - mean : 0.f;
-      sums[0] += d;
-      sums[1] += d * d;
+      for (int e = 0; e < V; ++e) {
+        const float d = i + e < p.width ? s[e] - mean : 0.f;
+        sums[0] += d;
+        sums[1] += d * d;
+      }
     }
-  }
-  row_totals<T>(sums, 0, lds + 1);
-  const Stats t(sums[0], sums[1], p.width, p.eps);
-  for (int i = threadIdx.x * V; i < p.width; i += T * V) {
-    float s[V], w[V], b[V] = {};
-    load8<false>(s0 + i, p.width - i, s);
-    load8<false>(p.weight + i, p.width - i, w);
-    if (p.bias) load8<false>(p.bias + i, p.width - i, b);
+    row_totals<T>(sums, 0, lds + 1);
+    const Stats t(sums[0], sums[1], p.width, p.eps);
+    for (int i = threadIdx.x * V; i < p.width; i += T * V) {
+      float s[V], w[V], b[V] = {};
+      load8<false>(s0 + i, p.width - i, s);
+      load8<false>(p.weight + i, p.width - i, w);
+      if (p.bias) load8<false>(p.bias + i, p.width - i, b);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = (s[e] - mean - t.shift) * t.rstd * w[e] + b[e];
-    store8(static_cast<E*>(p.y) + base + i, p.width - i, s);
+      for (int e = 0; e < V; ++e) s[e] = (s[e] - mean - t.shift) * t.rstd * w[e] + b[e];
+      store8(static_cast<E*>(p.y) + base + i, p.width - i, s);
+    }
   }
 }
 
@@ -507,7 +509,7 @@ RowSplit split(int width) {
   if (width <= 4096) return {512, 1, 1536};
   if (width <= 8192) return {512, 2, 1024};
   if (width <= 16384) return {1024, 2, 512};
-  return {0, 0, 0};
+  return {0, 0, 4096};
 }
 // The backward pass keeps its parts of dweight and dbias for a workgroup's whole walk, so it has as many as the card
 // runs at once (16384 x 2048 bf16: 512 62 us, 384 71, 768 68).  One vector a lane as far as a workgroup reaches: two
@@ -537,7 +539,7 @@ template <typename E, bool DROP>
 hipError_t launch_rows(const LayernormParams& p, hipStream_t st) {
   const RowSplit s = split(p.width);
   if (s.lanes == 0) {
-    hipLaunchKernelGGL((layernorm_wide_kernel<E, DROP>), dim3((unsigned)p.rows), dim3(1024), 0, st, p);
+    hipLaunchKernelGGL((layernorm_wide_kernel<E, DROP>), dim3((unsigned)(p.rows < s.most ? p.rows : s.most)), dim3(1024), 0, st, p);
     return hipGetLastError();
   }
   const dim3 grid((unsigned)workgroups(p.rows, s, threads(s.lanes)));

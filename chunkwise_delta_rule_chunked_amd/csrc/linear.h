@@ -69,16 +69,16 @@ void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, i
 // bf16 inputs in one file, float32 in another
 hipError_t lin_chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
 hipError_t lin_chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);
-hipError_t lin_summary_bf16(const LinChain* forward, const LinChain* reverse, hipStream_t st);
-hipError_t lin_summary_f32(const LinChain* forward, const LinChain* reverse, hipStream_t st);
+hipError_t lin_summary_bf16(const LinChain& forward, const LinChain* reverse, hipStream_t st);
+hipError_t lin_summary_f32(const LinChain& forward, const LinChain* reverse, hipStream_t st);
 hipError_t lin_backward_bf16(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, hipStream_t st);
 hipError_t lin_backward_f32(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, hipStream_t st);
 
 inline hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, int form, hipStream_t st) {
   return bf16 ? lin_chain_bf16(c, reverse, form, st) : lin_chain_f32(c, reverse, form, st);
 }
-// Each segment's state from zero, `forward` and `reverse` in one launch (either may be nullptr, and have run = 0).
-inline hipError_t launch_lin_summary(const LinChain* forward, const LinChain* reverse, bool bf16, hipStream_t st) {
+// Each segment's state from zero, of `forward` and (unless nullptr) `reverse` in one launch; either may have run = 0.
+inline hipError_t launch_lin_summary(const LinChain& forward, const LinChain* reverse, bool bf16, hipStream_t st) {
   return bf16 ? lin_summary_bf16(forward, reverse, st) : lin_summary_f32(forward, reverse, st);
 }
 // The three chains of a backward pass in one launch, forms PAIRS, PLAIN and SUMS, or all PLAIN without `gates`; dv's STATE

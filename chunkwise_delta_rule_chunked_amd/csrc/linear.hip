@@ -199,14 +199,14 @@ __global__ __launch_bounds__(WAVE) void gate_heads_kernel(int B, int H, int P, c
 template <typename E>
 __global__ __launch_bounds__(256) void share_kernel(const float* dq_part, const float* dk_part, E* dq, E* dk, long quads, int share,
                                                     int width) {
-  const long t = (long)blockIdx.x * 256 + threadIdx.x;
-  if (t >= 2 * quads) return;
-  const bool second = t >= quads;
-  const long i = (second ? t - quads : t) * 4, row = i / width;
-  const float* from = (second ? dk_part : dq_part) + row * share * width + i % width;
-  floatx4 s = *reinterpret_cast<const floatx4*>(from);
-  for (int k = 1; k < share; ++k) s += *reinterpret_cast<const floatx4*>(from + (long)k * width);
-  store4<E>((second ? dk : dq) + i, s[0], s[1], s[2], s[3]);
+  for (long t = (long)blockIdx.x * 256 + threadIdx.x; t < 2 * quads; t += (long)gridDim.x * 256) {
+    const bool second = t >= quads;
+    const long i = (second ? t - quads : t) * 4, row = i / width;
+    const float* from = (second ? dk_part : dq_part) + row * share * width + i % width;
+    floatx4 s = *reinterpret_cast<const floatx4*>(from);
+    for (int k = 1; k < share; ++k) s += *reinterpret_cast<const floatx4*>(from + (long)k * width);
+    store4<E>((second ? dk : dq) + i, s[0], s[1], s[2], s[3]);
+  }
 }
 
 // One token: S <- a S + k v^T, o = scale S^T q.  Bound by the state, read and written once: a workgroup has
@@ -337,7 +337,8 @@ hipError_t launch_lin_gates(const LinGates& p, hipStream_t st) {
 hipError_t launch_lin_share(const float* dq_part, const float* dk_part, void* dq, void* dk, long rows, int heads, int share, int width,
                             bool bf16_out, hipStream_t st) {
   const long quads = rows * heads * width / 4;
-  const dim3 grid((unsigned)((2 * quads + 255) / 256));
+  const long all = (2 * quads + 255) / 256, most = 1 << 16;  // more walk: a launch has fewer than 2^32 threads
+  const dim3 grid((unsigned)(all < most ? all : most));
   if (bf16_out)
     hipLaunchKernelGGL((share_kernel<bf16>), grid, dim3(256), 0, st, dq_part, dk_part, static_cast<bf16*>(dq), static_cast<bf16*>(dk),
                        quads, share, width);

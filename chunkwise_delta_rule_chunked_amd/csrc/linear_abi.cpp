@@ -32,6 +32,9 @@ int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, bool backwar
   if (s->n_h != 1 || qk_heads < 1 || s->H % qk_heads != 0 || s->L > (1 << 30)) return DELTA_ERR_BAD_SHAPE;
   if (gate != DELTA_LIN_GATE_NONE && gate != DELTA_LIN_GATE_TOKEN && gate != DELTA_LIN_GATE_HEAD) return DELTA_ERR_UNSUPPORTED_DIM;
   if ((long long)s->H * (s->dk > s->dv ? s->dk : s->dv) > (1LL << 20)) return DELTA_ERR_BAD_SHAPE;
+  // a launch has fewer than 2^32 threads: up to 1024 for a sequence and head, one for four elements of a state
+  const long long heads = (long long)s->B * s->H;
+  if (heads > (1LL << 20) || heads * s->dk * s->dv > (1LL << 33)) return DELTA_ERR_BAD_SHAPE;
   n.B = s->B, n.L = s->L, n.H = s->H, n.Hk = qk_heads, n.dk = s->dk, n.dv = s->dv, n.gate = gate;
   n.bf16 = s->dtype == DELTA_BF16, n.scale = s->scale;
   delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, backward, n.NT, n.P, n.NS);
@@ -156,7 +159,7 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   c.out = O, c.out_f32 = !n.bf16;
   if (n.P != 1) {  // P = 0: no tokens, the state as it is
     c.run = S_final ? n.P : n.P - 1;
-    if (n.P > 0 && (rc = hip_status(delta::launch_lin_summary(&c, nullptr, n.bf16, st)))) return rc;
+    if (n.P > 0 && (rc = hip_status(delta::launch_lin_summary(c, nullptr, n.bf16, st)))) return rc;
     if ((rc = hip_status(delta::launch_lin_combine(&c, nullptr, nullptr, st))) || n.P == 0) return rc;
     c.run = n.P;
   }
@@ -225,7 +228,7 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   dvc.write = dvc.inner = n.scale;
   if (n.P > 1) {
     dqc.run = n.P - 1, dvc.run = dS0 ? n.P : n.P - 1;
-    if ((rc = hip_status(delta::launch_lin_summary(&dqc, &dvc, n.bf16, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_summary(dqc, &dvc, n.bf16, st)))) return rc;
     if ((rc = hip_status(delta::launch_lin_combine(&dqc, &dvc, dg_log ? w.bounds : nullptr, st)))) return rc;
     dqc.run = dvc.run = n.P;
   }

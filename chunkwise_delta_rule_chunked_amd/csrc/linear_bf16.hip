@@ -5,7 +5,7 @@ namespace delta {
 
 hipError_t lin_chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st) { return lin::chain<bf16>(c, reverse, form, st); }
 
-hipError_t lin_summary_bf16(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
+hipError_t lin_summary_bf16(const LinChain& forward, const LinChain* reverse, hipStream_t st) {
   return lin::summary<bf16>(forward, reverse, st);
 }
 

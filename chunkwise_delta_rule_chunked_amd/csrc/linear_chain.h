@@ -642,18 +642,17 @@ hipError_t chain(const LinChain& c, bool reverse, int form, hipStream_t st) {
 }
 
 template <typename E, int KW, int CT>
-hipError_t run_summary(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
-  const unsigned split = forward ? blocks(*forward, 4 * CT) : 0, all = split + (reverse ? blocks(*reverse, 4 * CT) : 0);
+hipError_t run_summary(const LinChain& forward, const LinChain* reverse, hipStream_t st) {
+  const unsigned split = blocks(forward, 4 * CT), all = split + (reverse ? blocks(*reverse, 4 * CT) : 0);
   if (all == 0) return hipSuccess;
   hipLaunchKernelGGL((summary_kernel<E, KW, CT>), dim3(all), dim3(4 * WAVE), (Config<E, KW, 4, CT, false, PLAIN, true>::LDS), st,
-                     forward ? *forward : *reverse, reverse ? *reverse : *forward, split);
+                     forward, reverse ? *reverse : forward, split);
   return hipGetLastError();
 }
 template <typename E>
-hipError_t summary(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
-  const LinChain& c = forward ? *forward : *reverse;
-  const int w = c.y.width;
-  const bool wide = c.z.width > 64;
+hipError_t summary(const LinChain& forward, const LinChain* reverse, hipStream_t st) {
+  const int w = forward.y.width;
+  const bool wide = forward.z.width > 64;
   if (w <= 32) return wide ? run_summary<E, 32, 2>(forward, reverse, st) : run_summary<E, 32, 1>(forward, reverse, st);
   if (w <= 64) return wide ? run_summary<E, 64, 2>(forward, reverse, st) : run_summary<E, 64, 1>(forward, reverse, st);
   return wide ? run_summary<E, 128, 2>(forward, reverse, st) : run_summary<E, 128, 1>(forward, reverse, st);

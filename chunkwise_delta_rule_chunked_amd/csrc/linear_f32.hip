@@ -5,7 +5,7 @@ namespace delta {
 
 hipError_t lin_chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st) { return lin::chain<float>(c, reverse, form, st); }
 
-hipError_t lin_summary_f32(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
+hipError_t lin_summary_f32(const LinChain& forward, const LinChain* reverse, hipStream_t st) {
   return lin::summary<float>(forward, reverse, st);
 }
 

@@ -12,8 +12,8 @@
  * same bits, whatever the device's load or the call's timing.
  *
  * Shapes: s->n_h must be 1, s->chunk is ignored, dk in {16, 32, 64, 128}, dv a multiple of 16 up to
- * 256, H * max(dk, dv) <= 2^20, L <= 2^30.  `qk_heads` heads of q and k, which divides H: value head h
- * reads query and key head h / (H / qk_heads).
+ * 256, H * max(dk, dv) <= 2^20, B * H <= 2^20, B * H * dk * dv <= 2^33, L <= 2^30.  `qk_heads` heads of q
+ * and k, which divides H: value head h reads query and key head h / (H / qk_heads).
  *
  * Gates: log decays in float32, one of DELTA_LIN_GATE_*.  g <= 0 is expected; a positive value is
  * computed as given, as long as the products of the gates within a chunk of 64 tokens stay in

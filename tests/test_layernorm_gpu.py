@@ -229,6 +229,55 @@ def test_more_rows_than_workgroups(N, W):
         assert ((G[n].double() - ref).abs() <= (N / 256 + 600 + W / 64 + 32) * U * mag).all(), n
 
 
+@pytest.mark.parametrize("N,W", [(200001, 40), (25001, 1000), (13001, 2048), (2001, 4096), (4200, 16392)])
+def test_more_rows_than_forward_workgroups(N, W):
+    """The forward pass has more workgroups before they walk; with dropout, whose mask goes by the row."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    x, res, w, b = r(N, W), r(N, W), 1 + 0.1 * r(W).float(), r(W).float()
+    s, y = D.layer_layernorm(x, w, b, res, p=0.25, seed=9)
+    assert torch.equal(s, D.layer_dropout(x, res, p=0.25, seed=9))
+    assert torch.equal(y, D.layer_layernorm(s, w, b)[1])
+    for a in (0, N // 2 + 1, N - 5):
+        assert torch.equal(D.layer_layernorm(s[a:a + 5].contiguous(), w, b)[1], y[a:a + 5])
+
+
+@pytest.mark.parametrize("p", [0.0, 0.3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,W", [(1, 1024), (4103, 1024), (1031, 2048), (517, 4096), (259, 8192)])
+def test_backward_rows_at_any_element(N, W, dtype, p):
+    """Rows of whole vectors that start on 16 bytes are loaded a step ahead, others are not: both against float64, with
+    rows behind the tensors left as they were."""
+    say("layernorm bwd, rows at an odd element", N, W, dtype, p)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    flat = [torch.randn((N + 2) * W + 1, generator=gen, device="cuda").to(t) for _ in range(3)]
+    w = 1 + 0.1 * torch.randn(W, generator=gen, device="cuda")
+    for off in (0, 1):
+        s, dy, ds = (f[off:off + N * W].view(N, W) for f in flat)
+        outs = [torch.full(((N + 2) * W + 1,), 7.0, dtype=t, device="cuda") for _ in range(2)]
+        names = ("dresidual", "dx") if p else ("dresidual",)
+        G = D.layer_layernorm_bwd(dy, s, w, ds, eps=1e-2, p=p, seed=5,
+                                  grads={n: o[off:off + N * W].view(N, W) for n, o in zip(names, outs)})
+        for o in outs[:len(names)]:
+            assert bool((o[:off] == 7).all()) and bool((o[off + N * W:] == 7).all())
+        S, Y = s.double(), dy.double()
+        rstd = 1 / torch.sqrt(S.var(1, keepdim=True, correction=0) + 1e-2)
+        z, wd = (S - S.mean(1, keepdim=True)) * rstd, w.double() * Y
+        ref = ds.double() + rstd * (wd - wd.mean(1, keepdim=True) - z * (wd * z).mean(1, keepdim=True))
+        # as in test_layernorm_bwd, the dropped channels' reference through the same mask
+        zz = z.abs() + 1
+        mag = ds.double().abs() + rstd * (wd.abs() + wd.abs().mean(1, keepdim=True) + zz * (wd.abs() * zz).mean(1, keepdim=True))
+        rel = (W / 64 + 32) * U
+        check("dresidual", G["dresidual"], ref.cpu().numpy(), (rel * mag * (1 + HALF[dtype]) + HALF[dtype] * ref.abs() + 1e-38).cpu().numpy())
+        if p:
+            f = D.layer_dropout(torch.ones(N, W, device="cuda"), p=p, seed=5).double()
+            check("dx", G["dx"], (f * ref).cpu().numpy(),
+                  (f * ((rel + 2 * U) * mag * (1 + HALF[dtype]) + (HALF[dtype] + U) * ref.abs()) + 1e-38).cpu().numpy())
+        check("dweight", G["dweight"], (Y * z).sum(0).cpu().numpy(), ((N + W / 64 + 32) * U * (Y.abs() * zz).sum(0) + 1e-38).cpu().numpy())
+        check("dbias", G["dbias"], Y.sum(0).cpu().numpy(), (N * U * Y.abs().sum(0) + 1e-38).cpu().numpy())
+
+
 def test_special_rows():
     W = 300
     x = np.ones((6, W), dtype=np.float32)

@@ -246,6 +246,19 @@ def test_shared_heads_are_repeated_heads(dtype):
         assert ((G[n].double() - want).abs() <= HALF[dtype] * (parts.abs().sum(3) + want.abs()) * 1.01 + 4 * U * parts.abs().sum(3)).all(), n
 
 
+def test_shared_heads_of_more_rows_than_the_sum_has_threads():
+    """In float32 dq and dk of a shared head are the sums of what each value head's own call gives, bit for bit."""
+    B, L, Hk, H, dk, dv = 1, 70001, 4, 8, 128, 16
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    q, k, v, dO, g = r(B, L, Hk, dk), r(B, L, Hk, dk) / 16, r(B, L, H, dv), r(B, L, H, dv), -torch.rand((B, L, H), generator=gen, device="cuda")
+    shared = D.bwd_lin(q, k, v, g, None, dO)
+    each = D.bwd_lin(q.repeat_interleave(2, 2), k.repeat_interleave(2, 2), v, g, None, dO)
+    for n in ("dq", "dk"):
+        assert torch.equal(shared[n], each[n][:, :, 0::2] + each[n][:, :, 1::2]), n
+    assert torch.equal(shared["dv"], each["dv"]) and torch.equal(shared["dg_log"], each["dg_log"])
+
+
 def test_in_place_and_split_over_calls():
     c = Case(2, 1000, 1, 3, 64, 48, "bf16", "token")
     q, k, v, g, S0 = c.dev
@@ -441,6 +454,28 @@ def test_on_another_stream_and_two_at_once():
         again = calls(cs[0])["bwd"]()
     streams[0].synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, ref[0][1]))
+
+
+def test_captured_calls_of_one_workspace():
+    """Two graphs whose calls share a workspace, replayed one after the other, in either order."""
+    cs = [Case(1, 1500, 2, 2, 64, 64, "bf16", "token", seed=s) for s in (0, 50)]
+    ref = [[t.clone() for t in calls(c)["bwd"]()] for c in cs]
+    ws = torch.empty(D.bwd_lin_workspace_bytes(1, 1500, 2, 2, 64, 64), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for c in cs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(calls(c)["bwd"](workspace=ws))
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        ws.fill_(255)                                      # NaN wherever it is read before it is written
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], ref[i]))
 
 
 def test_calls_from_several_threads():

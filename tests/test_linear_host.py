@@ -102,6 +102,16 @@ def test_bwd_refusals(lib, no_gpu):
     assert bwd(dSf=fake(20), dS0=fake(20)) == -6 and bwd(S0=fake(20), dS0=fake(20)) == -6
 
 
+def test_sizes_whose_launches_would_not_fit(lib, no_gpu):
+    F, B = "delta_fwd_lin_workspace_bytes", "delta_bwd_lin_workspace_bytes"
+    big = dict(L=1, dk=16, dv=16)
+    for kw, rc in ((dict(big, B=1 << 20, H=1), 0), (dict(big, B=(1 << 20) + 1, H=1), -2), (dict(big, B=1 << 12, H=1 << 9), -2),
+                   (dict(L=1, dk=128, dv=256, B=1 << 18, H=1), 0), (dict(L=1, dk=128, dv=256, B=(1 << 18) + 1, H=1), -2)):
+        assert size(F, ctypes.byref(shape(**kw)), 1)[0] == rc and size(B, ctypes.byref(shape(**kw)), 1, 1)[0] == rc, kw
+        if rc:
+            assert fwd(shape(**kw), hk=1) == rc and bwd(shape(**kw), hk=1) == rc and dec(shape(**kw), hk=1) == rc, kw
+
+
 def test_decode_refusals(lib, no_gpu):
     for n in ("q", "k", "v", "g", "S", "O"):
         assert dec(**{n: None}) == -1, n
