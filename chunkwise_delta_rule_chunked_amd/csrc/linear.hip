@@ -280,27 +280,34 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 // Segments of a sequence, of NS chunks each.  A segment's chunks follow one another, so a call takes some time for each
 // chunk of a segment; and it moves four states (backward: twelve, three chains being side by side) for each segment of
 // each sequence and head.  The sum of the two is least where NS goes with the square root of (heads x chunks); the
-// factors are measured (us, 128 x 128 states, NS under and over the rule's in brackets): forward 4 x 8 heads of 2K tokens
-// 59 (2: 66, 8: 78), 2 x 16 of 8K 125 (4: 174, 16: 156); backward 4 x 8 of 2K 129 (4: 129, 16: 203), 8 x 8 of 777 130
-// (4: 140, 13: 138), 8 x 16 of 512 94 (4: 132), 1 of 4K 65 (1: 80, 4: 74).  A forward chain's workgroups all run at once,
-// two to a compute unit (float32: one): more would take a second round (64K tokens of 16 heads, 512 workgroups 417, 1024
-// 528), and where heads alone fill the compute units a summary is not worth its reads (256 heads of 1K 111, split in two 132).
+// factors are measured.  Then the launch should fill the card: forward 512 workgroups, backward 256 of each chain, no
+// more (a second round) and not much less.  Measured, us, 128 x 128 states, here and (segments: us) otherwise:
+//   backward bf16  2 x 16 heads of 8K tokens in 8 segments 367 (6: 405, 9: 412, 10: 384, 16: 383); 4 x 16 of 2K in 4 193 (3:
+//     214, 5: 220); 2 of 30000 in 79 164 (59: 161, 118: 196); 4 of 2K in 16 61 (8: 72, 32: 68)
+//     (a number a little over a whole round of the three, 512, is worse than that round: 2 x 16 of 4K in 5 200, in 6 214)
+//   backward float32  16 heads of 16K in 16 1067 (18: 1336, 23: 1279); 2 of 30000 in 85 355 (86: 418)
+//   forward bf16  4 x 16 of 2K in 8 77 (6: 85, 11: 104); 2 x 16 of 8K in 16 123 (8: 155); 64K of 16 heads in 32 417 (64: 528)
+//   forward float32, whose workgroups are alone on a compute unit with such states and which therefore takes no number
+//     between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16 of 8K, 64 x 64, in 16 136 (8: 182)
+// Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 321 in one,
+// 372 in two; 8 x 8 of 777 111 in one, 116 in three; 12 x 16 of 1K forward 69 in one, 76 in two.
 void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS) {
   const int C = lin_chunk(bf16);
   NT = (L + C - 1) / C;
+  P = NT > 0, NS = NT;
   const long units = (long)B * H * (backward ? 1 : (dv + LIN_SLAB - 1) / LIN_SLAB);
-  if (NT == 0 || units == 0 || (!backward && units >= 256)) {
-    P = NT > 0, NS = NT;
-    return;
-  }
-  const double ns = sqrt((double)units * NT / (backward ? 16 : 64));
-  NS = ns >= NT ? NT : ns < 1.5 ? 1 : (int)(ns + 0.5);
-  if (!backward) {
-    const long most = (bf16 ? 512 : 256) / units;  // at least 1
-    if ((NT + NS - 1) / NS > most) NS = (int)((NT + most - 1) / most);
-  }
-  P = (NT + NS - 1) / NS;
-  NS = (NT + P - 1) / P;  // as even as that many segments can be
+  if (NT == 0 || units == 0) return;
+  const long card = backward ? 256 : 512, most = card / units;
+  const double ns = sqrt((double)units * NT / (backward ? 24 : 64));
+  const int n = ns < 1.5 ? 1 : (int)(ns + 0.5);
+  long p = (NT + n - 1L) / n;
+  // a round of workgroups and few more
+  const long round = backward ? 512 / 3 : 256, few = backward ? 208 : 384;
+  if ((backward ? dv <= 128 : !bf16) && units * p > round && units * p <= few) p = round / units;
+  else if (4 * p >= 3 * most + backward) p = most;
+  if (p > NT) p = NT;
+  if (p < (backward ? 4 : 3)) return;
+  NS = (int)((NT + p - 1) / p);  // as even as that many segments can be
   P = (NT + NS - 1) / NS;
 }
 

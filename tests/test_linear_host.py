@@ -87,7 +87,8 @@ def test_fwd_refusals(lib, no_gpu):
     assert fwd(q=fake(0, 8)) == -4 and fwd(Sf=fake(20, 4)) == -4 and fwd(w=fake(7, 2)) == -4 and fwd(g=fake(3, 2)) == -4
     assert fwd(O=fake(0)) == -6 and fwd(O=fake(2)) == -6 and fwd(Sf=fake(5)) == -6
     assert fwd(S0=fake(20), Sf=fake(20, 256)) == -6                                # part of S0
-    assert fwd(w=None) == -5 and fwd(w=fake(0)) == -6
+    long = shape(L=5000)                                                           # in segments: with a workspace
+    assert fwd(long, w=None) == -5 and fwd(long, w=fake(0)) == -6
     assert D.load_library().delta_fwd_lin(None, 1, 0, *[None] * 8, 0, None) == -1
 
 
