@@ -209,68 +209,80 @@ __global__ __launch_bounds__(256) void share_kernel(const float* dq_part, const 
   }
 }
 
-// One token: S <- a S + k v^T, o = scale S^T q.  Bound by the state, read and written once: a workgroup has
-// SW columns of one head's state, a thread 4 rows x 4 columns in 16-byte accesses with non-temporal hints,
-// and the sums over the rows of S^T q meet in LDS.
-template <typename E, int DK, int SW>
-__global__ __launch_bounds__(DK * SW / 16) void decode_kernel(LinDecode p) {
-  constexpr int CQ = SW / 4, TH = DK / 4 * CQ, NW = (TH + WAVE - 1) / WAVE;
-  __shared__ floatx4 red[NW][CQ];
-  const int tid = threadIdx.x, cq = tid % CQ, r0 = tid / CQ * 4;
-  const int slabs = p.DV / SW, slab = blockIdx.x % slabs;
-  const long bh = blockIdx.x / slabs;
-  const int h = (int)(bh % p.H);
-  const long bk = bh / p.H * p.Hk + h / (p.H / p.Hk);
-  float* Sg = p.S + bh * DK * p.DV + slab * SW + cq * 4;
-  floatx4 s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(Sg + (long)(r0 + i) * p.DV));
-  const E *q = static_cast<const E*>(p.q) + bk * DK + r0, *k = static_cast<const E*>(p.k) + bk * DK + r0;
-  const E* v = static_cast<const E*>(p.v) + bh * p.DV + slab * SW + cq * 4;
+// One token: S <- a S + k v^T, o = scale S^T q.  Bound by the state, read and written once.  A workgroup has `pack`
+// units, a unit being one head's state or a slab of its columns; of a unit, a thread has one of `quads` groups of four
+// columns and U consecutive rows, in 16-byte accesses with non-temporal hints.  The sums over the rows of S^T q meet in
+// LDS.  Measured at 64 x 16 states of 128 x 128 (a captured graph): 23.5 us, 5.8 TB/s; with 4 rows a thread 25.6, with 16
+// 25.2, with 512 threads 24.8, with a loop over the rows of a state 28.6.  Accesses run along a state's rows, in one step:
+// slabs of 16 columns where a width is no multiple of 32 took 72 us for 33M elements of 64 x 80 states, 47 like this.
+// Small states share a workgroup: 33M elements of 16 x 16 states 49 us, one to a workgroup 64.
+constexpr int DECODE_TH = 256, DECODE_WGS = 1024;
+template <typename E, int DK, int U>
+__global__ __launch_bounds__(DECODE_TH) void decode_kernel(LinDecode p, int quads, int slabs, int pack) {
+  constexpr int GROUPS = DK / U;
+  __shared__ floatx4 red[DECODE_TH];
+  const int per = quads * GROUPS, tid = threadIdx.x, in = tid % per, r0 = in / quads * U;
+  const long unit = (long)blockIdx.x * pack + tid / per, bh = unit / slabs;
+  const int quad = (int)(unit % slabs) * quads + in % quads;
+  const bool on = tid < per * pack && bh < (long)p.B * p.H && quad < p.DV / 4;
   typedef E E4 __attribute__((ext_vector_type(4)));
-  const E4 q4 = *reinterpret_cast<const E4*>(q), k4 = *reinterpret_cast<const E4*>(k), v4 = *reinterpret_cast<const E4*>(v);
-  const float a = p.gate == LIN_GATE_NONE ? 1.f : expf(p.g[p.gate == LIN_GATE_TOKEN ? bh : h]);
   floatx4 o = {};
+  if (on) {
+    const int h = (int)(bh % p.H);
+    const long bk = bh / p.H * p.Hk + h / (p.H / p.Hk);
+    float* Sg = p.S + (bh * DK + r0) * p.DV + quad * 4;
+    floatx4 s[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < U; ++i) s[i] = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(Sg + (long)i * p.DV));
+    const E *q = static_cast<const E*>(p.q) + bk * DK + r0, *k = static_cast<const E*>(p.k) + bk * DK + r0;
+    const E4 v4 = *reinterpret_cast<const E4*>(static_cast<const E*>(p.v) + bh * p.DV + quad * 4);
+    const float a = p.gate == LIN_GATE_NONE ? 1.f : expf(p.g[p.gate == LIN_GATE_TOKEN ? bh : h]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      s[i][c] = a * s[i][c] + to_float((E)k4[i]) * to_float((E)v4[c]);
-      o[c] += to_float((E)q4[i]) * s[i][c];
+    for (int i = 0; i < U; i += 4) {
+      const E4 q4 = *reinterpret_cast<const E4*>(q + i), k4 = *reinterpret_cast<const E4*>(k + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[i + j][e] = a * s[i + j][e] + to_float((E)k4[j]) * to_float((E)v4[e]);
+          o[e] += to_float((E)q4[j]) * s[i + j][e];
+        }
     }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) __builtin_nontemporal_store(s[i], reinterpret_cast<floatx4*>(Sg + (long)(r0 + i) * p.DV));
-#pragma unroll
-  for (int off = CQ; off < (TH < WAVE ? TH : WAVE); off <<= 1)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], off, WAVE);
-  if constexpr (NW > 1) {
-    if (tid % WAVE < CQ) red[tid / WAVE][tid % WAVE] = o;
-    barrier_lds();
-    if (tid < CQ) {
-      o = red[0][tid];
-#pragma unroll
-      for (int w = 1; w < NW; ++w) o += red[w][tid];
-    }
+    for (int i = 0; i < U; ++i) __builtin_nontemporal_store(s[i], reinterpret_cast<floatx4*>(Sg + (long)i * p.DV));
   }
-  if (tid < CQ) store4<E>(static_cast<E*>(p.O) + bh * p.DV + slab * SW + cq * 4, p.scale * o[0], p.scale * o[1], p.scale * o[2], p.scale * o[3]);
+  red[tid] = o;
+  barrier_lds();
+  if (on && r0 == 0) {
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) o += red[tid + k * quads];
+    store4<E>(static_cast<E*>(p.O) + bh * p.DV + quad * 4, p.scale * o[0], p.scale * o[1], p.scale * o[2], p.scale * o[3]);
+  }
 }
 
-template <typename E, int DK>
-hipError_t decode_by_slab(const LinDecode& p, hipStream_t st) {
-  const unsigned heads = (unsigned)(p.B * p.H);
-  if (p.DV % 32 == 0) hipLaunchKernelGGL((decode_kernel<E, DK, 32>), dim3(heads * (p.DV / 32)), dim3(DK * 2), 0, st, p);
-  else hipLaunchKernelGGL((decode_kernel<E, DK, 16>), dim3(heads * (p.DV / 16)), dim3(DK), 0, st, p);
+template <typename E, int DK, int U>
+hipError_t decode(const LinDecode& p, hipStream_t st) {
+  constexpr int GROUPS = DK / U, MOST = DECODE_TH / GROUPS / 4;  // tiles of 16 columns that a workgroup's threads reach
+  const long heads = (long)p.B * p.H;
+  const int tiles = p.DV / 16;
+  long s = (DECODE_WGS + heads - 1) / heads;  // slabs: enough for the card, of two tiles at least
+  if (s > (tiles + 1) / 2) s = (tiles + 1) / 2;
+  if (s < (tiles + MOST - 1) / MOST) s = (tiles + MOST - 1) / MOST;
+  const int per = (int)((tiles + s - 1) / s), slabs = (tiles + per - 1) / per, threads = 4 * per * GROUPS;
+  const long units = heads * slabs, many = units / DECODE_WGS;
+  const int fit = DECODE_TH / threads, pack = many < 1 ? 1 : many < fit ? (int)many : fit;
+  const dim3 grid((unsigned)((units + pack - 1) / pack)), block((threads * pack + WAVE - 1) / WAVE * WAVE);
+  hipLaunchKernelGGL((decode_kernel<E, DK, U>), grid, block, 0, st, p, 4 * per, slabs, pack);
   return hipGetLastError();
 }
 
 template <typename E>
 hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
   switch (p.DK) {
-    case 16: return decode_by_slab<E, 16>(p, st);
-    case 32: return decode_by_slab<E, 32>(p, st);
-    case 64: return decode_by_slab<E, 64>(p, st);
-    case 128: return decode_by_slab<E, 128>(p, st);
+    case 16: return decode<E, 16, 4>(p, st);
+    case 32: return decode<E, 32, 4>(p, st);
+    case 64: return decode<E, 64, 8>(p, st);
+    case 128: return decode<E, 128, 8>(p, st);
     default: return hipErrorInvalidValue;
   }
 }

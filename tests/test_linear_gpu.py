@@ -376,6 +376,36 @@ def test_decode_continues_a_prefill(B, Hk, H, dk, dv, dtype, kind):
     c.check_fwd(torch.cat(outs, 1), S)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hk,H,dk,dv", [
+    (1, 1, 1, 128, 16), (2101, 1, 3, 16, 16), (1031, 5, 5, 16, 48), (6, 2, 2, 16, 256), (131, 3, 9, 32, 112), (515, 4, 4, 32, 32),
+    (41, 1, 7, 128, 112), (31, 5, 5, 64, 80), (3, 3, 3, 128, 240), (257, 2, 8, 64, 64), (9, 1, 1, 64, 144)])
+def test_decode_widths(B, Hk, H, dk, dv, dtype):
+    """States that share a workgroup, slabs with a narrower last one, and what lies behind the tensors left as it was.
+    Bounds: a state's element has three roundings and expf's (4 u); o a sum of dk products, each of which carries its
+    state's error, and its own rounding."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    q, k, v = r(B, 1, Hk, dk).to(t), r(B, 1, Hk, dk).to(t), r(B, 1, H, dv).to(t)
+    g = -torch.rand((B, 1, H), generator=gen, device="cuda")
+    n, m, pad = B * H * dk * dv, B * H * dv, 64
+    flat, out = torch.full((n + pad,), 7.0, device="cuda"), torch.full((m + pad,), 7.0, device="cuda", dtype=t)
+    S0 = r(B, H, dk, dv)
+    S = flat[:n].view(B, H, dk, dv).copy_(S0)
+    O = D.decode_lin(q, k, v, g, S, scale=0.5, O=out[:m].view(B, 1, H, dv))
+    assert bool((flat[n:] == 7).all()) and bool((out[m:] == 7).all())
+    u, rep = 2.0 ** -24, H // Hk
+    Q, K = (x.double().repeat_interleave(rep, 2)[:, 0] for x in (q, k))
+    decayed, taken = g.double().exp()[:, 0, :, None, None] * S0.double(), K[..., None] * v.double()[:, 0, :, None, :]
+    ref, mag = decayed + taken, decayed.abs() + taken.abs()
+    assert bool(((S.double() - ref).abs() <= 6 * u * mag).all())
+    o = 0.5 * (Q[..., None] * ref).sum(2)
+    tol = 0.5 * (dk + 8) * u * (Q.abs()[..., None] * mag).sum(2)
+    half = torch.finfo(t).eps / 2
+    assert bool(((O.double()[:, 0] - o).abs() <= tol * (1 + half) + half * o.abs()).all())
+
+
 def test_offsets_past_32_bits():
     """2.3e9 elements of each tensor: the last sequence against a call on it alone (which is split into
     segments, where the whole batch is not), and the states of both."""
