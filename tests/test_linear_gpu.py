@@ -157,6 +157,15 @@ def test_lin(case):
         assert (t is None and G2[n] is None) or torch.equal(t, G2[n]), n
 
 
+@pytest.mark.parametrize("case", [
+    (5, 450, 8, 16, 128, 128, "bf16", "token", (70, 200, 449), True, True), (6, 200, 8, 16, 64, 80, "f32", "head", (), True, True),
+    (5, 170, 16, 16, 128, 128, "f32", "token", (33,), False, True), (6, 300, 16, 16, 32, 144, "bf16", "token", (64,), True, False),
+    (260, 130, 1, 1, 16, 32, "bf16", "none", (), True, True), (33, 200, 2, 8, 32, 64, "bf16", "head", (), True, True)], ids=name)
+def test_many_heads_in_one_segment(case):
+    """Chunk after chunk in one launch, where heads alone fill the card."""
+    test_lin(case)
+
+
 def test_the_full_shape():
     """The 2 x 8K-token, 16-head shape with heads that share q and k; the oracle on two value heads of one
     sequence, one from either end."""
