@@ -136,8 +136,10 @@ __global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
       const size_t i = (bh * p.NT + n) * p.C + lane;
       const float gl = gate(n);
       const double e = wave_total(lane < p.C ? p.e[i] : 0.0), f = wave_total(lane < p.C ? p.f[i] : 0.0);
-      const double a = wave_total((double)(gl < LOG_GATE_FLOOR ? LOG_GATE_FLOOR : gl));
-      if (lane == 0) se[c] = e, sf[c] = f, shut[c] = expf((float)a) == 0.f;
+      const bool reset = expf(gl) == 0.f;
+      const double a = wave_total(reset ? 0.0 : (double)gl);
+      const bool none = __ballot(reset) || expf((float)a) == 0.f;
+      if (lane == 0) se[c] = e, sf[c] = f, shut[c] = none;
     }
     __syncthreads();
     if (tid == 0)

@@ -1,0 +1,124 @@
+"""Linear attention where its inputs leave the ordinary: gates above 1 next to resets and over several segments, and
+sequences whose tokens differ by orders of magnitude.
+
+Tolerances are those of test_linear_gpu.py (u = 2^-24, M the same recurrence on magnitudes), elementwise.  A decay e^x
+carries (2 + |x|) u, so along a path over n chunks whose log gates add up to at most X in magnitude in each, the
+decays carry n (4 + X) u: c = dk + dv + 64 + n (4 + X) + 100.
+"""
+import numpy as np
+import pytest
+
+from oracle import linear as Lo
+from parity import say, to_dev
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+import chunkwise_delta_rule_chunked_amd as D  # noqa: E402
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+CHUNK = {"bf16": 64, "f32": 32}
+
+
+def draw(seed, shape, dtype="f32"):
+    x = np.random.default_rng(seed).standard_normal(shape).astype(np.float32)
+    return torch.from_numpy(x).to(torch.bfloat16).float().numpy() if dtype == "bf16" else x
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def check(name, got, ref, tol):
+    got = host(got)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        over = np.nan_to_num(np.abs(got - ref) / tol, nan=np.inf, posinf=np.inf)
+    over[got == ref] = 0.0
+    say("  %s: max error / bound %.3f" % (name, over.max()))
+    assert over.max() <= 1.0, (name, float(over.max()), np.unravel_index(over.argmax(), over.shape))
+
+
+class Problem:
+    """Inputs by hand, the oracle's results, and the bounds above."""
+
+    def __init__(self, dtype, q, k, v, g, S0=None, dO=None, dS=None, scale=1.0):
+        self.dtype, self.x, self.dO, self.dS, self.scale = dtype, dict(q=q, k=k, v=v, g=g, S0=S0), dO, dS, scale
+        self.dev = [to_dev(self.x[n], dtype if n in "qkv" else "f32") for n in ("q", "k", "v", "g", "S0")]
+        L, C = q.shape[1], CHUNK[dtype]
+        finite = np.where(np.isfinite(g), np.abs(g), 0.0)
+        X = max(finite[:, i:i + C].sum(1).max() for i in range(0, L, C))
+        self.c = q.shape[3] + v.shape[3] + 64 + -(-L // C) * (4 + X) + 100
+        self.once = HALF["bf16"] if dtype == "bf16" else 0.0
+        self.abs = {n: a if a is None or n == "g" else np.abs(a) for n, a in self.x.items()}
+
+    def rounded(self, M, ref):
+        return (self.once + self.c * U) * M + HALF[self.dtype] * (np.abs(ref) + (self.once + self.c * U) * M) + 1e-36
+
+    def check_fwd(self):
+        O, S = D.fwd_lin(*self.dev, scale=self.scale)
+        torch.cuda.synchronize()
+        Or, Sr = Lo.fwd(**self.x, scale=self.scale)
+        Om, Sm = Lo.fwd(**self.abs, scale=self.scale)
+        check("S_final", S, Sr, self.c * U * Sm + 1e-36)
+        check("O", O, Or, self.rounded(Om, Or))
+        return O, S
+
+    def check_bwd(self):
+        """dq, dk, dv and dS0, as test_linear_gpu.py bounds them."""
+        mag = lambda x: None if x is None else np.abs(x)
+        ref = Lo.bwd(*self.x.values(), self.dO, self.dS, self.scale)
+        M = Lo.bwd(*self.abs.values(), mag(self.dO), mag(self.dS), self.scale)
+        G = D.bwd_lin(*self.dev, to_dev(self.dO, self.dtype), to_dev(self.dS, "f32"), scale=self.scale)
+        torch.cuda.synchronize()
+        for n in ("dq", "dk", "dv"):
+            check(n, G[n], ref[n], self.rounded(M[n], ref[n]))
+        check("dS0", G["dS0"], ref["dS0"], self.c * U * M["dS0"] + 1e-36)
+        return G, ref, M
+
+
+def above_one(seed, B, L, H, span, top):
+    """Gates up to e^(top / span), most of them above 1, with a reset at least every `span` tokens: their product
+    over any stretch between two resets, and over any chunk, is below e^top."""
+    r = np.random.default_rng(seed)
+    g = (r.uniform(-0.2, 1.0, (B, L, H)) * top / span).astype(np.float32)
+    t = int(r.integers(0, span))
+    while t < L:
+        g[:, t] = -np.inf if r.random() < 0.5 else -104.5      # exp(-104.5) is 0 in float32 too
+        t += int(r.integers(span // 3, span))
+    return g
+
+
+# ---- resets among gates above 1 -------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H", [(1, 1), (3, 100)])
+def test_a_reset_stays_one_behind_gates_above_1(dtype, B, H):
+    """The first gate is a reset and nothing is written behind it: every output is 0, however large the gates behind
+    the reset are (a chunk's product is in float32's range), in segments and without."""
+    C = CHUNK[dtype]
+    L, d = 6 * C, 16
+    g = np.full((B, L, H), 80.0 / C, np.float32)
+    g[:, 0] = -np.inf
+    z, r = np.zeros((B, L, H, d), np.float32), draw(1, (B, L, H, d), dtype)
+    O, S = D.fwd_lin(*(to_dev(x, dtype) for x in (r, z, r)), to_dev(g, "f32"), torch.ones(B, H, d, d, device="cuda"))
+    assert not O.any() and not S.any()
+    # mirrored: the last gate a reset, and only the state behind it has a gradient
+    g = np.full((B, L, H), 80.0 / C, np.float32)
+    g[:, -1] = -np.inf
+    G = D.bwd_lin(*(to_dev(x, dtype) for x in (z, r, r)), to_dev(g, "f32"), None, to_dev(z, dtype), torch.ones(B, H, d, d, device="cuda"))
+    # (not dg_log: the states themselves grow by e^80 in each of six chunks, past float32, and their products with 0 are NaN)
+    assert not G["dS0"].any() and not G["dk"][:, :-1].any() and not G["dv"][:, :-1].any()
+
+
+@pytest.mark.parametrize("B,L,Hk,H,dk,dv,dtype", [
+    (1, 64, 1, 1, 16, 16, "bf16"), (2, 200, 1, 2, 32, 48, "f32"), (1, 700, 1, 2, 64, 64, "bf16"), (1, 450, 2, 2, 128, 144, "f32"),
+    (2, 333, 1, 1, 32, 160, "bf16"), (3, 130, 30, 90, 16, 32, "bf16"), (1, 500, 3, 3, 64, 32, "f32")])
+def test_gates_above_1_between_resets(B, L, Hk, H, dk, dv, dtype):
+    r = lambda seed, *shape, t=dtype: draw(seed, shape, t)
+    p = Problem(dtype, r(1, B, L, Hk, dk), r(2, B, L, Hk, dk), r(3, B, L, H, dv), above_one(4, B, L, H, 60, 50.0),
+                r(5, B, H, dk, dv, t="f32"), r(6, B, L, H, dv), r(7, B, H, dk, dv, t="f32"), dk ** -0.5)
+    say("above 1", B, L, Hk, H, dk, dv, dtype)
+    p.check_fwd()
+    G, _, _ = p.check_bwd()
+    hard = np.exp(p.x["g"].astype(np.float32)) == 0
+    assert hard.any() and not host(G["dg_log"])[hard].any()
