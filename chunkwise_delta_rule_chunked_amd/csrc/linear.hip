@@ -15,6 +15,14 @@ __device__ inline double wave_total(double x) {
   return x;
 }
 
+// s e^d for a segment's sum of log gates.  With gates above 1 e^d may be no float32 number although s e^d is (s is small, or
+// 0): then in three steps, each between s and the result.  Past e^240 every s is 0, infinite or 0 again.
+__device__ inline floatx4 decayed(floatx4 s, double d) {
+  if (!(fabs(d) > 80.0) || d == -INFINITY) return s * expf((float)d);
+  const float third = expf((float)(fmin(fmax(d, -240.0), 240.0) / 3));
+  return s * third * third * third;
+}
+
 // One chain's states of one place, four elements a lane, from segment to segment: a segment's result becomes its start,
 // start_{p+1} = e^decay_p start_p + result_p.  BOUNDS: and the parts of the inner products with the other chain's starts
 // (segment p of the reverse chain starts behind segment P - 1 - p of the other).
@@ -57,7 +65,7 @@ __device__ inline void walk(const Walk& w, int P, long quads, long bh, long q, c
         at[(p0 + k) * quads] = s;
         if constexpr (BOUNDS)
           if (p0 + k > 0) x[k] = dot(s, o[k]);
-        s = s * expf((float)w.decay[bh * P + p0 + k]) + r[k];
+        s = decayed(s, w.decay[bh * P + p0 + k]) + r[k];
       }
     if constexpr (BOUNDS) {
 #pragma unroll

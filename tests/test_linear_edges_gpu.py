@@ -122,3 +122,40 @@ def test_gates_above_1_between_resets(B, L, Hk, H, dk, dv, dtype):
     G, _, _ = p.check_bwd()
     hard = np.exp(p.x["g"].astype(np.float32)) == 0
     assert hard.any() and not host(G["dg_log"])[hard].any()
+
+
+# ---- gates above 1 over several segments -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gates_above_1_before_anything_is_written(dtype):
+    """A chunk's product is in float32's range (e^38), a segment's (e^153) is not, but there is nothing for it to
+    multiply: the state is 0 until the last tokens, and its gradient behind the first."""
+    B, L, H, d = 1, 4096, 16, 16
+    g = np.full((B, L, H), 0.6, np.float32)
+    late, early = np.arange(L)[:, None, None] >= L - 60, np.arange(L)[:, None, None] < 60
+    r = lambda seed: draw(seed, (B, L, H, d), dtype)
+    p = Problem(dtype, r(1), (r(2) * late).astype(np.float32), r(3), g, None, (r(4) * early).astype(np.float32))
+    say("before anything is written", dtype)
+    p.check_fwd()
+    G, _, _ = p.check_bwd()
+    assert not G["dg_log"].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_small_state_grows_past_a_segments_range(dtype):
+    """A start state of 1e-30 and gates of e^130 in all within a segment (e^42 at most in a chunk), and back again for
+    the gradient of the state behind the last token: the results are float32 numbers, the segment's product is none."""
+    B, L, H, d = 1, 4096, 16, 16
+    t = np.arange(L)[None, :, None]
+    r = lambda seed, *s: draw(seed, s, dtype)
+    grow = np.broadcast_to(((t >= 20) & (t < 220)) * np.float32(0.65), (B, L, H)).astype(np.float32)
+    x = [r(s, B, L, H, d) for s in (1, 2, 3)]
+    still = (x[1] * (t[..., None] >= 220)).astype(np.float32)
+    p = Problem(dtype, x[0], still, x[2], grow, np.float32(1e-30) * draw(5, (B, H, d, d)))
+    say("a small state", dtype)
+    p.check_fwd()
+    late = grow[:, ::-1].copy()                                   # the same in the last segment, met by the gradient first
+    end = (x[1] * (t[..., None] >= L - 20)).astype(np.float32)    # (the states would outgrow float32)
+    p = Problem(dtype, x[0], end, x[2], late, None, (r(6, B, L, H, d) * (t[..., None] < L - 220)).astype(np.float32),
+                np.float32(1e-30) * draw(7, (B, H, d, d)))
+    p.check_bwd()
