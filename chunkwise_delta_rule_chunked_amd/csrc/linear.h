@@ -19,6 +19,12 @@ constexpr int lin_chunk(bool bf16) { return bf16 ? 64 : 32; }
 // Inner products of states are left in parts of 256 elements.
 constexpr int lin_parts(int dk, int dv) { return dk * dv / 256; }
 
+// A log gate as a term of a chunk's sums.  One whose exp is 0 in float32 (below ln 2^-150) is a hard reset, and so far
+// from the others that no chunk of 64 gates whose products are float32 numbers makes up for it: the exp of a sum with
+// a reset in it is 0.  Differences of such sums are still good to 2^-29.
+constexpr double LIN_RESET = -131072.0;
+__device__ inline double lin_log_gate(float g) { return g < -103.972076f ? LIN_RESET : (double)g; }
+
 // One operand of a chain: [B, L, heads, width], head h of the chain reading head h / (H / heads).
 struct LinRole {
   const void* p;

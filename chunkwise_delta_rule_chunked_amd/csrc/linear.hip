@@ -144,10 +144,8 @@ __global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
       const size_t i = (bh * p.NT + n) * p.C + lane;
       const float gl = gate(n);
       const double e = wave_total(lane < p.C ? p.e[i] : 0.0), f = wave_total(lane < p.C ? p.f[i] : 0.0);
-      const bool reset = expf(gl) == 0.f;
-      const double a = wave_total(reset ? 0.0 : (double)gl);
-      const bool none = __ballot(reset) || expf((float)a) == 0.f;
-      if (lane == 0) se[c] = e, sf[c] = f, shut[c] = none;
+      const double a = wave_total(lin_log_gate(gl));
+      if (lane == 0) se[c] = e, sf[c] = f, shut[c] = expf((float)a) == 0.f;
     }
     __syncthreads();
     if (tid == 0)
@@ -163,7 +161,7 @@ __global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
       const double e = lane < p.C ? p.e[i] : 0.0, f = lane < p.C ? p.f[i] : 0.0;
       // Sums from this token on and up to it, as far as the next reset: beyond one there is nothing to add but what
       // rounding leaves of sums that cancel.
-      const bool reset = expf(gate(n)) == 0.f;
+      const bool reset = lin_log_gate(gate(n)) == LIN_RESET;
       const unsigned long long resets = __ballot(reset);
       double up = e, down = f;
 #pragma unroll

@@ -12,7 +12,8 @@
 // mirrored order, and forms that also leave what the gates' gradients need while its operands are at hand.
 // Every exponent goes from a later token back to an earlier one, so decays are at most 1 for log gates up to 0; for
 // gates above 1 the products within a chunk have to be float32 numbers.  The sums of log gates are held in 64
-// bits, because their differences are what is used.  A hard reset is no term of them: what spans one is an exact 0.
+// bits, because their differences are what is used.  What spans a hard reset is an exact
+// 0 (lin_log_gate).
 //
 // A workgroup has a segment of the sequence for one head and some columns of the state: each wavefront has
 // CT tiles of 16 columns and all rows, in MFMA accumulators for the whole segment.  The two row tiles 2u,
@@ -287,36 +288,30 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   };
   auto back_of = [](int hi) { return 8 * hi * (hi - 1); };  // where the decays to block hi begin
   double sum = 0.0;  // log gates of the chunks so far, -inf with a reset among them (keeper)
-  // A reset counts as 0 in the sums and zeroes every factor that spans it: added to them, gates above 1 behind it could
-  // outweigh it.
   auto tables = [&](int i, float gl) {
-    const bool reset = expf(gl) == 0.f;
-    const unsigned long long resets = __ballot(reset);  // by token
-    double a = reset ? 0.0 : (double)gl;
+    double a = lin_log_gate(gl);
 #pragma unroll
     for (int o = 1; o < C; o <<= 1) {
       const double up = __shfl_up(a, o, WAVE);
       if (lane >= o) a += up;
     }
     const double last = __shfl(a, C - 1, WAVE);
-    sum += resets ? -INFINITY : last;
+    sum += last < LIN_RESET / 2 ? -INFINITY : last;
     const Table t = table(i);
-    const unsigned long long upto = resets << (63 - lane), past = resets >> lane >> 1;  // among tokens 0 .. lane; behind it
-    const float begin = upto ? 0.f : expf((float)a), end = past ? 0.f : expf((float)(last - a));
+    const float begin = expf((float)a), end = expf((float)(last - a));
     const double ref = __shfl(a, max(16 * (lane >> 4) - 1, 0), WAVE);
     if (lane < C) {
-      // two tokens with a reset between are 2^17 apart, far past float32's exponents (and the sums still good to 2^-29)
-      t.gc[lane] = a * 1.4426950408889634074 - 131072.0 * __popcll(upto);
+      t.gc[lane] = a * 1.4426950408889634074;
       t.fx[lane] = (REV ? end : begin) * p.outer;
       t.fy[lane] = (REV ? begin : end) * p.write;
-      t.in[lane] = resets >> 16 * (lane >> 4) << (63 - (lane & 15)) ? 0.f : expf((float)(lane < 16 ? a : a - ref));
+      t.in[lane] = expf((float)(lane < 16 ? a : a - ref));
     }
 #pragma unroll
     for (int hi = 1; hi < NB; ++hi) {
-      const float to = past & ((1ull << (16 * hi - 1 - min(lane, 16 * hi - 1))) - 1) ? 0.f : expf((float)(__shfl(a, 16 * hi - 1, WAVE) - a));
+      const float to = expf((float)(__shfl(a, 16 * hi - 1, WAVE) - a));
       if (lane < 16 * hi) t.back[back_of(hi) + lane] = to;
     }
-    if (lane == 0) *t.whole = resets ? 0.f : expf((float)last);
+    if (lane == 0) *t.whole = expf((float)last);
   };
 
   // ---- the state: rows srow(t, 4 g + j) of column m of this wavefront's tiles
