@@ -16,8 +16,13 @@ enum { LIN_PLAIN = 0, LIN_PAIRS = 1, LIN_SUMS = 2, LIN_STATE = 3 };
 // Tokens of a chunk: float32 tiles are twice as large, and their products run at a sixteenth of the rate.
 constexpr int lin_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
-// Inner products of states are left in parts of 256 elements.
-constexpr int lin_parts(int dk, int dv) { return dk * dv / 256; }
+// Rows that a chain's registers hold for a state of `rows`, and the bytes of such a state as they hold it (linear_chain.h):
+// 16 x 16 tiles, an even number of them across.
+constexpr int lin_rows(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+constexpr size_t lin_state_bytes(int rows, int cols) { return (size_t)((cols / 16 + 1) / 2 * 2) * (lin_rows(rows) / 16) * 1024; }
+
+// Chunks of a workgroup of the gates' gradients.
+constexpr int LIN_GATE_CHUNKS = 16;
 
 // A log gate as a term of a chunk's sums.  One whose exp is 0 in float32 (below ln 2^-150) is a hard reset, and so far
 // from the others that no chunk of 64 gates whose products are float32 numbers makes up for it: the exp of a sum with
@@ -48,18 +53,21 @@ struct LinChain {
   void* out;               // [B, L, H, z.width] in the inputs' type, or float32
   bool out_f32;
   float* tok;              // PAIRS, SUMS: [B, H, NT chunks] a value per token
+  float* pair;             // PAIRS: the same of the pairs within its chunk
+  int part;                // of a backward pass: 0 the whole walk, 1 the first half of its chunks, 2 the rest
+  float* wait;             // part 1, 2: [B, H, P] states between the two, as the registers hold them
+  float *states, *edge;    // PAIRS, SUMS: [B, H, NT] states left by the one for the other; e^gc_C <S, G> of the chunk
 };
 
 // Gradients of the log gates from what the two backward chains left.
 struct LinGates {
-  int B, L, H, C, NT, P, NS, dk, dv;
-  const float *e, *f;      // [B, H, NT * C]
-  const double* bounds;    // P > 1: [B, H, P, lin_parts] parts of <S, G> before each segment
-  const float *S0, *dS0;   // P = 1: [B, H] states and their gradients before the first token (nullptr: no such term)
+  int B, L, H, C, NT;
+  const float *e, *f, *pair;  // [B, H, NT * C]
+  const float* edge;          // [B, H, NT]
   const float* g;
   int gate;
-  float* dg;               // [B, L, H], or [H] through `part`
-  double* part;            // gate HEAD: [B, H, P]
+  float* dg;                  // [B, L, H], or [H] through `part`
+  double* part;               // gate HEAD: [B, H, workgroups of a head]
 };
 
 struct LinDecode {
@@ -87,15 +95,14 @@ inline hipError_t launch_lin_chain(const LinChain& c, bool bf16, bool reverse, i
 inline hipError_t launch_lin_summary(const LinChain& forward, const LinChain* reverse, bool bf16, hipStream_t st) {
   return bf16 ? lin_summary_bf16(forward, reverse, st) : lin_summary_f32(forward, reverse, st);
 }
-// The three chains of a backward pass in one launch, forms PAIRS, PLAIN and SUMS, or all PLAIN without `gates`; dv's STATE
-// with `state`.  Only for values of up to 128 channels.
+// The three chains of a backward pass side by side in one launch, forms PAIRS, PLAIN and SUMS, or all PLAIN without `gates`;
+// dv's STATE with `state`.  Only for values of up to 128 channels.  A chain with run = 0 is left out.
 inline hipError_t launch_lin_backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, bool gates, bool state, bool bf16,
                                       hipStream_t st) {
   return bf16 ? lin_backward_bf16(dq, dv, dk, gates, state, st) : lin_backward_f32(dq, dv, dk, gates, state, st);
 }
-// The segments' results become their starts, of both chains (either nullptr); with both also, where `bounds`, the parts of
-// <S, G> before each segment (before the first only if both states are there: forward's start, reverse's end).
-hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, double* bounds, hipStream_t st);
+// The segments' results become their starts, of both chains (either nullptr).
+hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, hipStream_t st);
 hipError_t launch_lin_gates(const LinGates& p, hipStream_t st);
 // The parts of dq and of dk, each [rows, heads, share, width], added up over `share`.
 hipError_t launch_lin_share(const float* dq_part, const float* dk_part, void* dq, void* dk, long rows, int heads, int share, int width,

@@ -24,172 +24,88 @@ __device__ inline floatx4 decayed(floatx4 s, double d) {
 }
 
 // One chain's states of one place, four elements a lane, from segment to segment: a segment's result becomes its start,
-// start_{p+1} = e^decay_p start_p + result_p.  BOUNDS: and the parts of the inner products with the other chain's starts
-// (segment p of the reverse chain starts behind segment P - 1 - p of the other).
+// start_{p+1} = e^decay_p start_p + result_p.
 struct Walk {
   const floatx4* start;
   floatx4 *segs, *end;
   const double* decay;
 };
-template <bool BOUNDS>
-__device__ inline void walk(const Walk& w, int P, long quads, long bh, long q, const floatx4* other, const floatx4* other0,
-                            double* bounds) {
-  auto dot = [](const floatx4& a, const floatx4& b) {
-    double x = 0.0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x += (double)a[k] * b[k];
-    return x;
-  };
-  auto bound = [&](int place, double x) {
-    x = wave_total(x);
-    if (threadIdx.x % WAVE == 0) bounds[((bh * P + place) * quads + q) / WAVE] = x;
-  };
+__device__ inline void walk(const Walk& w, int P, long quads, long bh, long q) {
   floatx4 s = w.start ? w.start[bh * quads + q] : floatx4{};
   floatx4* at = w.segs + bh * P * quads + q;
-  const floatx4* ot = other + bh * P * quads + q;
   const int n = w.end ? P : P - 1;  // without an end the last segment has no result
   constexpr int AHEAD = 8;          // results loaded at a time
   for (int p0 = 0; p0 < n; p0 += AHEAD) {
-    floatx4 r[AHEAD], o[BOUNDS ? AHEAD : 1];
-    double x[AHEAD] = {};
+    floatx4 r[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
-      if (p0 + k < n) {
-        r[k] = at[(p0 + k) * quads];
-        if constexpr (BOUNDS)
-          if (p0 + k > 0) o[k] = ot[(P - p0 - k) * quads];
-      }
+      if (p0 + k < n) r[k] = at[(p0 + k) * quads];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
       if (p0 + k < n) {
         at[(p0 + k) * quads] = s;
-        if constexpr (BOUNDS)
-          if (p0 + k > 0) x[k] = dot(s, o[k]);
         s = decayed(s, w.decay[bh * P + p0 + k]) + r[k];
       }
-    if constexpr (BOUNDS) {
-#pragma unroll
-      for (int o2 = WAVE / 2; o2 > 0; o2 >>= 1)
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) x[k] += __shfl_xor(x[k], o2, WAVE);
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (p0 + k > 0 && p0 + k < n && threadIdx.x % WAVE == 0) bounds[((bh * P + P - p0 - k) * quads + q) / WAVE] = x[k];
-    }
   }
-  if (w.end) {
-    w.end[bh * quads + q] = s;
-    if constexpr (BOUNDS) bound(0, other0 ? dot(s, other0[bh * quads + q]) : 0.0);
-  } else if (P > 0) {
-    at[(P - 1) * quads] = s;
-    if constexpr (BOUNDS) {
-      bound(1, dot(s, ot[quads]));
-      bound(0, 0.0);
-    }
-  }
+  if (w.end) w.end[bh * quads + q] = s;
+  else if (P > 0) at[(P - 1) * quads] = s;
 }
 
-template <bool FORWARD, bool REVERSE, bool BOUNDS>
-__global__ __launch_bounds__(256) void combine_kernel(int P, long quads, long all, Walk forward, Walk reverse, double* bounds) {
+template <bool FORWARD, bool REVERSE>
+__global__ __launch_bounds__(256) void combine_kernel(int P, long quads, long all, Walk forward, Walk reverse) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x, bh = i / quads, q = i % quads;
-  if (i >= all) return;  // whole wavefronts: a state is a multiple of 256 elements
-  if constexpr (FORWARD) walk<false>(forward, P, quads, bh, q, nullptr, nullptr, nullptr);
-  // the forward chain's starts are this lane's own
-  if constexpr (REVERSE) walk<BOUNDS>(reverse, P, quads, bh, q, forward.segs, forward.start, bounds);
+  if (i >= all) return;
+  if constexpr (FORWARD) walk(forward, P, quads, bh, q);
+  if constexpr (REVERSE) walk(reverse, P, quads, bh, q);
 }
 
-// d log g of the tokens of one segment.  With b the inner product of the state before a chunk and its
-// gradient, and X = e^gc_C <G, S> what the chunk's two ends share,
-//     b = X + sum e,   b' = X + sum f,   d log g_t = X + sum_{r < t} f_r + sum_{r >= t} e_r
-// (e with the pairs' row and column sums, which cancel over a chunk).  b is formed from the states at the
-// segment's start and carried on from chunk to chunk; a chunk that lets nothing through has X = 0.
-constexpr int GATE_TH = 1024, GATE_WAVES = GATE_TH / WAVE, GATE_CHUNKS = 64;
-__global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p) {
-  __shared__ double sums[GATE_WAVES], se[GATE_CHUNKS], sf[GATE_CHUNKS];
-  __shared__ bool shut[GATE_CHUNKS];
-  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
-  const int seg = blockIdx.x % p.P;
-  const long bh = blockIdx.x / p.P;
+// d log g_t = a_t <G_t, S_{t-1}>: every pair of a write before t and a read from t on.  For the tokens of a chunk these
+// are
+//     X + sum_{r >= t} e_r + sum_{r < t} f_r + pair_t
+// with X = e^gc_C <G, S> what passes the chunk whole, e_r what the state at its start gives to token r's output (reads
+// in it of writes before it), f_r the same in the other order, and pair_t the pairs in it around t.  All are formed from
+// states with their decays, and sums run over terms that all cross t: a token's error goes by what crosses that token.
+// (X carried from chunk to chunk by e and f, which differ by it, keeps the errors of far larger tokens that the state has
+// long forgotten.)  A wavefront has a chunk.
+constexpr int GATE_TH = 256, GATE_WAVES = GATE_TH / WAVE;
+__global__ __launch_bounds__(GATE_TH) void gates_kernel(LinGates p, int groups) {
+  __shared__ double sums[GATE_WAVES];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const long bh = blockIdx.x / groups;
   const int h = (int)(bh % p.H);
   const long b = bh / p.H;
-  double before = 0.0, all = 0.0;
-  if (p.P > 1) {
-    const int parts = lin_parts(p.dk, p.dv);
-    for (int k = lane; k < parts; k += WAVE) before += p.bounds[(bh * p.P + seg) * parts + k];
-    before = wave_total(before);
-  } else if (p.S0) {
-    const int size = p.dk * p.dv;
-    for (int i = 4 * tid; i < size; i += 4 * GATE_TH) {
-      const floatx4 s = *reinterpret_cast<const floatx4*>(p.S0 + bh * size + i), d = *reinterpret_cast<const floatx4*>(p.dS0 + bh * size + i);
+  const int first = blockIdx.x % groups * LIN_GATE_CHUNKS, last = min(first + LIN_GATE_CHUNKS, p.NT);
+  double all = 0.0;
+  for (int n = first + wave; n < last; n += GATE_WAVES) {
+    const size_t i = (bh * p.NT + n) * p.C + lane;
+    const long token = (long)n * p.C + lane;
+    const bool in = lane < p.C, on = in && token < p.L;
+    double up = in ? p.e[i] : 0.0, down = in ? p.f[i] : 0.0, dg = in ? p.pair[i] : 0.0;
+    const float gate = !on ? 0.f : p.gate == LIN_GATE_TOKEN ? p.g[(b * p.L + token) * p.H + h] : p.g[h];
+    dg += p.edge[bh * p.NT + n];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) before += (double)s[k] * d[k];
+    for (int o = 1; o < WAVE; o <<= 1) {
+      const double u = __shfl_down(up, o, WAVE), d = __shfl_up(down, o, WAVE);
+      if (lane + o < WAVE) up += u;
+      if (lane >= o) down += d;
     }
-    before = wave_total(before);
-    if (lane == 0) sums[wave] = before;
-    __syncthreads();
-    before = 0.0;
-    for (int k = 0; k < GATE_WAVES; ++k) before += sums[k];
-    __syncthreads();
-  }
-  const int first = seg * p.NS, count = min(p.NS, p.NT - first);
-  auto token = [&](int n) { return n * p.C + lane; };
-  auto gate = [&](int n) {
-    if (lane >= p.C || token(n) >= p.L) return 0.f;
-    return p.gate == LIN_GATE_TOKEN ? p.g[(b * p.L + token(n)) * p.H + h] : p.g[h];
-  };
-  for (int c0 = 0; c0 < count; c0 += GATE_CHUNKS) {
-    const int nc = min(GATE_CHUNKS, count - c0);
-    for (int c = wave; c < nc; c += GATE_WAVES) {
-      const int n = first + c0 + c;
-      const size_t i = (bh * p.NT + n) * p.C + lane;
-      const float gl = gate(n);
-      const double e = wave_total(lane < p.C ? p.e[i] : 0.0), f = wave_total(lane < p.C ? p.f[i] : 0.0);
-      const double a = wave_total(lin_log_gate(gl));
-      if (lane == 0) se[c] = e, sf[c] = f, shut[c] = expf((float)a) == 0.f;
+    const double past = __shfl_up(down, 1, WAVE);
+    dg += up;
+    if (lane > 0) dg += past;
+    if (lin_log_gate(gate) == LIN_RESET) dg = 0.0;  // nothing flows past a reset
+    if (on) {
+      if (p.gate == LIN_GATE_TOKEN) p.dg[(b * p.L + token) * p.H + h] = (float)dg;
+      else all += dg;
     }
-    __syncthreads();
-    if (tid == 0)
-      for (int c = 0; c < nc; ++c) {
-        const double X = shut[c] ? 0.0 : before - se[c];
-        before = X + sf[c];
-        se[c] = X;
-      }
-    __syncthreads();
-    for (int c = wave; c < nc; c += GATE_WAVES) {
-      const int n = first + c0 + c;
-      const size_t i = (bh * p.NT + n) * p.C + lane;
-      const double e = lane < p.C ? p.e[i] : 0.0, f = lane < p.C ? p.f[i] : 0.0;
-      // Sums from this token on and up to it, as far as the next reset: beyond one there is nothing to add but what
-      // rounding leaves of sums that cancel.
-      const bool reset = lin_log_gate(gate(n)) == LIN_RESET;
-      const unsigned long long resets = __ballot(reset);
-      double up = e, down = f;
-#pragma unroll
-      for (int o = 1; o < WAVE; o <<= 1) {
-        const double u = __shfl_down(up, o, WAVE), d = __shfl_up(down, o, WAVE);
-        const unsigned long long span = (1ull << o) - 1;  // o tokens
-        if (lane + o < WAVE && !(resets >> (lane + 1) & span)) up += u;
-        if (lane >= o && !(resets >> (lane - o + 1) & span)) down += d;
-      }
-      double past = __shfl_up(down, 1, WAVE);
-      if (lane == 0) past = 0.0;
-      const double dg = reset ? 0.0 : se[c] + up + past;  // nothing flows past a reset
-      if (lane < p.C && token(n) < p.L) {
-        if (p.gate == LIN_GATE_TOKEN) p.dg[(b * p.L + token(n)) * p.H + h] = (float)dg;
-        else all += dg;
-      }
-    }
-    __syncthreads();
   }
   if (p.gate == LIN_GATE_HEAD) {
     all = wave_total(all);
-    __syncthreads();
     if (lane == 0) sums[wave] = all;
     __syncthreads();
-    if (tid == 0) {
+    if (threadIdx.x == 0) {
       double s = 0.0;
       for (int k = 0; k < GATE_WAVES; ++k) s += sums[k];
-      p.part[bh * p.P + seg] = s;
+      p.part[blockIdx.x] = s;
     }
   }
 }
@@ -331,7 +247,7 @@ void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, i
   P = (NT + NS - 1) / NS;
 }
 
-hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, double* bounds, hipStream_t st) {
+hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, hipStream_t st) {
   const LinChain& c = forward ? *forward : *reverse;
   const long quads = (long)c.y.width * c.z.width / 4, all = quads * c.B * c.H;
   const dim3 grid((unsigned)((all + 255) / 256));
@@ -344,20 +260,20 @@ hipError_t launch_lin_combine(const LinChain* forward, const LinChain* reverse, 
     return w;
   };
   const Walk f = of(forward), r = of(reverse);
-  if (!reverse) hipLaunchKernelGGL((combine_kernel<true, false, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
-  else if (!forward) hipLaunchKernelGGL((combine_kernel<false, true, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
-  else if (!bounds) hipLaunchKernelGGL((combine_kernel<true, true, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
-  else hipLaunchKernelGGL((combine_kernel<true, true, true>), grid, dim3(256), 0, st, c.P, quads, all, f, r, bounds);
+  if (!reverse) hipLaunchKernelGGL((combine_kernel<true, false>), grid, dim3(256), 0, st, c.P, quads, all, f, r);
+  else if (!forward) hipLaunchKernelGGL((combine_kernel<false, true>), grid, dim3(256), 0, st, c.P, quads, all, f, r);
+  else hipLaunchKernelGGL((combine_kernel<true, true>), grid, dim3(256), 0, st, c.P, quads, all, f, r);
   return hipGetLastError();
 }
 
 hipError_t launch_lin_gates(const LinGates& p, hipStream_t st) {
-  const long n = (long)p.B * p.H * p.P;
+  const int groups = (p.NT + LIN_GATE_CHUNKS - 1) / LIN_GATE_CHUNKS;
+  const long n = (long)p.B * p.H * groups;
   if (n > 0) {
-    hipLaunchKernelGGL(gates_kernel, dim3((unsigned)n), dim3(GATE_TH), 0, st, p);
+    hipLaunchKernelGGL(gates_kernel, dim3((unsigned)n), dim3(GATE_TH), 0, st, p, groups);
     if (const hipError_t e = hipGetLastError()) return e;
   }
-  if (p.gate == LIN_GATE_HEAD) hipLaunchKernelGGL(gate_heads_kernel, dim3(p.H), dim3(WAVE), 0, st, p.B, p.H, p.P, p.part, p.dg);
+  if (p.gate == LIN_GATE_HEAD) hipLaunchKernelGGL(gate_heads_kernel, dim3(p.H), dim3(WAVE), 0, st, p.B, p.H, groups, p.part, p.dg);
   return hipGetLastError();
 }
 

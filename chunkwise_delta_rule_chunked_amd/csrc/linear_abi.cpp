@@ -71,22 +71,27 @@ size_t carve(const Lin& n, void* base, FwdSpace& w) {
 
 struct BwdSpace {
   float *segs, *gsegs;
-  double *decay, *gdecay, *part, *bounds;
-  float *e, *f, *dS0, *dq, *dk;
+  double *decay, *gdecay, *part;
+  float *e, *f, *pair, *edge, *states, *wait_q, *wait_k, *wait_v, *dq, *dk;
 };
-size_t carve(const Lin& n, void* base, BwdSpace& w) {
+size_t carve(const Lin& n, bool gates, void* base, BwdSpace& w) {
   Carve c{static_cast<char*>(base)};
-  const bool split = n.P > 1, gates = n.gate != DELTA_LIN_GATE_NONE;
-  const size_t heads = (size_t)n.B * n.H, tokens = heads * n.NT * delta::lin_chunk(n.bf16) * 4;
+  const bool split = n.P > 1, halves = gates && n.dv <= 128;
+  const size_t heads = (size_t)n.B * n.H, chunks = heads * n.NT, tokens = chunks * delta::lin_chunk(n.bf16) * 4;
+  const size_t qk_state = delta::lin_state_bytes(n.dv, n.dk), v_state = delta::lin_state_bytes(n.dk, n.dv);
   w.segs = c.take<float>(split ? n.state * n.P : 0);
   w.gsegs = c.take<float>(split ? n.state * n.P : 0);
   w.decay = c.take<double>(split ? heads * n.P * 8 : 0);
   w.gdecay = c.take<double>(split ? heads * n.P * 8 : 0);
-  w.part = c.take<double>(n.gate == DELTA_LIN_GATE_HEAD ? heads * n.P * 8 : 0);
+  w.part = c.take<double>(gates && n.gate == DELTA_LIN_GATE_HEAD ? heads * ((n.NT + delta::LIN_GATE_CHUNKS - 1) / delta::LIN_GATE_CHUNKS) * 8 : 0);
   w.e = c.take<float>(gates ? tokens : 0);
   w.f = c.take<float>(gates ? tokens : 0);
-  w.bounds = c.take<double>(gates && split ? heads * n.P * delta::lin_parts(n.dk, n.dv) * 8 : 0);
-  w.dS0 = c.take<float>(gates && n.L > 0 ? n.state : 0);  // where the caller wants none
+  w.pair = c.take<float>(gates ? tokens : 0);
+  w.edge = c.take<float>(gates ? chunks * 4 : 0);
+  w.states = c.take<float>(gates ? chunks * qk_state : 0);
+  w.wait_q = c.take<float>(halves ? heads * n.P * qk_state : 0);
+  w.wait_k = c.take<float>(halves ? heads * n.P * qk_state : 0);
+  w.wait_v = c.take<float>(halves ? heads * n.P * v_state : 0);
   w.dq = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);  // parts of the heads that share
   w.dk = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);
   return c.used;
@@ -160,7 +165,7 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   if (n.P != 1) {  // P = 0: no tokens, the state as it is
     c.run = S_final ? n.P : n.P - 1;
     if (n.P > 0 && (rc = hip_status(delta::launch_lin_summary(c, nullptr, n.bf16, st)))) return rc;
-    if ((rc = hip_status(delta::launch_lin_combine(&c, nullptr, nullptr, st))) || n.P == 0) return rc;
+    if ((rc = hip_status(delta::launch_lin_combine(&c, nullptr, st))) || n.P == 0) return rc;
     c.run = n.P;
   }
   return hip_status(delta::launch_lin_chain(c, n.bf16, false, n.P == 1 && S_final ? delta::LIN_STATE : delta::LIN_PLAIN, st));
@@ -172,7 +177,7 @@ int delta_bwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, int32_
   if (rc) return rc;
   if (!bytes) return DELTA_ERR_NULL_ARG;
   BwdSpace w;
-  *bytes = carve(n, nullptr, w);
+  *bytes = carve(n, gate != DELTA_LIN_GATE_NONE, nullptr, w);
   return DELTA_OK;
 }
 
@@ -186,7 +191,7 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   if ((gate == DELTA_LIN_GATE_NONE) != (g_log == nullptr) && (g_log || n.nv > 0)) return DELTA_ERR_NULL_ARG;
   if (gate == DELTA_LIN_GATE_NONE && dg_log) return DELTA_ERR_UNSUPPORTED_DIM;
   BwdSpace w;
-  const size_t need = carve(n, nullptr, w);
+  const size_t need = carve(n, dg_log != nullptr, nullptr, w);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DELTA_ERR_WORKSPACE;
   if ((rc = check_aligned({q, k, v, S0, dO, dS_final, dq, dk, dv, dS0, workspace}, g_log, dg_log))) return rc;
   const Range in[] = {span(q, n.nqk),    span(k, n.nqk),   span(v, n.nv),           span(g_log, n.ng),
@@ -198,20 +203,18 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   if ((rc = launch_guard())) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (g_log && validate_on() && (rc = validate_gates(g_log, n.ng / 4, st))) return rc;
-  carve(n, workspace, w);
+  carve(n, dg_log != nullptr, workspace, w);
 
   LinGates gp;
   memset(&gp, 0, sizeof(gp));
-  gp.B = n.B, gp.L = n.L, gp.H = n.H, gp.C = delta::lin_chunk(n.bf16), gp.NT = n.NT, gp.P = n.P, gp.NS = n.NS;
-  gp.dk = n.dk, gp.dv = n.dv, gp.e = w.e, gp.f = w.f, gp.bounds = w.bounds;
-  if (dg_log && S0 && !dS0) dS0 = w.dS0;
-  gp.S0 = S0, gp.dS0 = dS0;
+  gp.B = n.B, gp.L = n.L, gp.H = n.H, gp.C = delta::lin_chunk(n.bf16), gp.NT = n.NT;
+  gp.e = w.e, gp.f = w.f, gp.pair = w.pair, gp.edge = w.edge;
   gp.g = g_log, gp.gate = gate, gp.dg = dg_log, gp.part = w.part;
   if (n.state == 0 || n.L == 0) {
     if (n.state > 0 && dS0) {
       LinChain c = chain_of(n, g_log);
       c.y.width = n.dk, c.z.width = n.dv, c.start = dS_final, c.end = dS0;
-      if ((rc = hip_status(delta::launch_lin_combine(nullptr, &c, nullptr, st)))) return rc;
+      if ((rc = hip_status(delta::launch_lin_combine(nullptr, &c, st)))) return rc;
     }
     gp.B = 0;
     return sum_only ? hip_status(delta::launch_lin_gates(gp, st)) : DELTA_OK;
@@ -229,7 +232,7 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   if (n.P > 1) {
     dqc.run = n.P - 1, dvc.run = dS0 ? n.P : n.P - 1;
     if ((rc = hip_status(delta::launch_lin_summary(dqc, &dvc, n.bf16, st)))) return rc;
-    if ((rc = hip_status(delta::launch_lin_combine(&dqc, &dvc, dg_log ? w.bounds : nullptr, st)))) return rc;
+    if ((rc = hip_status(delta::launch_lin_combine(&dqc, &dvc, st)))) return rc;
     dqc.run = dvc.run = n.P;
   }
   LinChain dkc = dvc;
@@ -239,9 +242,22 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
   dqc.out = shared ? w.dq : dq, dkc.out = shared ? w.dk : dk, dvc.out = dv;
   dqc.out_f32 = dkc.out_f32 = shared || !n.bf16, dvc.out_f32 = !n.bf16;
   const bool state = n.P == 1 && dS0;
-  if (n.dv <= 128) {
-    if ((rc = hip_status(delta::launch_lin_backward(dqc, dvc, dkc, dg_log != nullptr, state, n.bf16, st)))) return rc;
-  } else {
+  dqc.pair = w.pair, dqc.states = dkc.states = w.states, dqc.edge = dkc.edge = w.edge;
+  if (!dg_log && n.dv <= 128) {
+    if ((rc = hip_status(delta::launch_lin_backward(dqc, dvc, dkc, false, state, n.bf16, st)))) return rc;
+  } else if (n.dv <= 128) {
+    // S and G meet at every chunk: in a first launch dq walks a segment's first half from the front and dk the other from
+    // the back, each leaving its states, and in a second each meets the other's.  dv is in halves too where all three run
+    // at once; else whole, in the first launch, where it takes the time of two halves beside it (2 x 16 heads of 8K tokens:
+    // 24 chunks in a row, in halves 32).
+    dqc.wait = w.wait_q, dkc.wait = w.wait_k, dvc.wait = w.wait_v;
+    const bool halves = 3LL * n.B * n.H * n.P <= (n.bf16 ? 512 : 256);
+    for (int part = 1; part <= 2; ++part) {
+      dqc.part = dkc.part = part, dvc.part = halves ? part : 0;
+      if (part == 2 && !halves) dvc.run = 0;
+      if ((rc = hip_status(delta::launch_lin_backward(dqc, dvc, dkc, true, state, n.bf16, st)))) return rc;
+    }
+  } else {  // dq leaves all states, dk meets them
     if ((rc = hip_status(delta::launch_lin_chain(dqc, n.bf16, false, dg_log ? delta::LIN_PAIRS : delta::LIN_PLAIN, st)))) return rc;
     if ((rc = hip_status(delta::launch_lin_chain(dvc, n.bf16, true, state ? delta::LIN_STATE : delta::LIN_PLAIN, st)))) return rc;
     if ((rc = hip_status(delta::launch_lin_chain(dkc, n.bf16, true, dg_log ? delta::LIN_SUMS : delta::LIN_PLAIN, st)))) return rc;

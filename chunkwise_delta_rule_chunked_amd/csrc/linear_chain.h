@@ -137,10 +137,18 @@ constexpr int terms(int n) {
 __device__ inline float sum_groups(float x) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(1.f, x, floatx4{}, 0, 0, 0)[0];
 }
+// The sum of the lanes l % 16, l % 16 + 16, ... below l's own group of 16.
+__device__ inline float sum_groups_below(float x, int lane) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32((lane >> 4) < ((lane & 15) >> 2) ? 1.f : 0.f, x, floatx4{}, 0, 0, 0)[0];
+}
 // The sum over a group of 16 lanes, in each of them.
 template <int CTRL>
+__device__ inline float from_dpp(float x) {  // 0 from outside the group
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
 __device__ inline float add_dpp(float x) {
-  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+  return x + from_dpp<CTRL>(x);
 }
 __device__ inline float sum_row(float x) {
   x = add_dpp<0xb1>(x);    // lanes 1, 0, 3, 2 of each four
@@ -148,17 +156,32 @@ __device__ inline float sum_row(float x) {
   x = add_dpp<0x141>(x);   // mirrored in each eight
   return add_dpp<0x140>(x);  // and in all sixteen
 }
+// Sums within a group of 16 lanes: from each lane on (itself too), and of the lanes below it.
+__device__ inline float sum_from(float x) {
+  x = add_dpp<0x101>(x);
+  x = add_dpp<0x102>(x);
+  x = add_dpp<0x104>(x);
+  return add_dpp<0x108>(x);
+}
+__device__ inline float sum_below(float x) {
+  x = from_dpp<0x111>(x);
+  x = add_dpp<0x111>(x);
+  x = add_dpp<0x112>(x);
+  x = add_dpp<0x114>(x);
+  return add_dpp<0x118>(x);
+}
 
 template <int N>
 struct Int {
   static constexpr int value = N;
 };
 
-// What a chain forms beside out.  SUMS: per token the sum over columns of w_i times the state's share of out_i (e).
-// PAIRS: also, for pairs j < i, M_ij = e^(gc_i - gc_j) (x_i . y_j)(w_i . z_j), and per token e + M's row sums - its
-// column sums.  STATE: the state behind the last token.  A state that is an output, or that the gates' gradients are
-// formed from, takes in float32 weights whole (three bf16 terms); one that only out reads, whose products round it to
-// bf16, one term.
+// What a chain forms beside out.  SUMS: per token the sum over columns of w_i times the state's share of out_i.
+// PAIRS: also, for pairs j < i of a chunk, M_ij = e^(gc_i - gc_j) (x_i . y_j)(w_i . z_j), and per token t the sum of M over
+// j < t <= i.  And these two, which walk in opposite orders over states in the same registers, form the inner product of S
+// and G at every chunk: the one that comes to it first leaves its state as the registers hold it, the other multiplies.
+// STATE: the state behind the last token.  A state that is an output, or that the gates' gradients are formed from,
+// takes in float32 weights whole (three bf16 terms); one that only out reads, whose products round it to bf16, one term.
 constexpr int PLAIN = LIN_PLAIN, PAIRS = LIN_PAIRS, SUMS = LIN_SUMS, STATE = LIN_STATE;
 constexpr bool for_gates(int form) { return form == PAIRS || form == SUMS; }
 
@@ -177,7 +200,7 @@ struct Config {
   // is in, and from it to each later block; the chunk's
   static constexpr int BACK = 16 * (NB * (NB - 1) / 2), TABLE = 4 * (5 * C + BACK) + 16;
   static constexpr int PART = TAB + 2 * TABLE, PARTS = FORM == PAIRS ? NW + 2 * NB : FORM == SUMS ? NW : 0;
-  static constexpr int LDS = PART + PARTS * C * 4;
+  static constexpr int EDGE = PART + PARTS * C * 4, LDS = EDGE + (for_gates(FORM) ? 4 * NW : 0);
 };
 
 template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
@@ -196,6 +219,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   E* const wt = reinterpret_cast<E*>(smem + K::W);
   E* const at = reinterpret_cast<E*>(smem + K::A);
   float* const part = reinterpret_cast<float*>(smem + K::PART);
+  float* const dots = reinterpret_cast<float*>(smem + K::EDGE);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = p.z.width / 16, slabs = (tiles + NW * CT - 1) / (NW * CT), per = (tiles + slabs - 1) / slabs;
@@ -209,6 +233,10 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   // the segments are the same ones in either order
   const int first = (REV ? p.P - 1 - seg : seg) * p.NS, count = min(p.NS, p.NT - first);
   auto chunk_at = [&](int i) { return REV ? first + count - 1 - i : first + i; };
+  // the chunks of this launch; either order's first half is the other's second
+  const int cut = SUM || p.part == 0 ? count : REV ? count / 2 : (count + 1) / 2;
+  const int begin = !SUM && p.part == 2 ? cut : 0, stop = !SUM && p.part == 1 ? cut : count;
+  if (begin == stop) return;
 
   // ---- tiles: registers for the next chunk's pieces
   struct Source {
@@ -262,7 +290,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   float gate = 0.f;  // of this lane's token of the chunk after the one in the registers (keeper)
   auto load_all = [&](int i) {
     const int n = chunk_at(i);
-    if (keeper && i + 1 < count) gate = gate_of(i + 1);
+    if (keeper && i + 1 < stop) gate = gate_of(i + 1);
     if constexpr (!SUM) load(rx, sx, n, CX{});
     load(ry, sy, n, CX{});
     load(rz, sz, n, CZ{});
@@ -335,8 +363,11 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
         }
       }
   };
-  const float first_gate = keeper ? gate_of(0) : 0.f;
-  load_all(0);  // under way while the state is loaded
+  // A state as the registers hold it: 16 x 16 tiles of a lane's four elements each.
+  const int slot = (tiles + 1) / 2 * 2 * NT * (4 * WAVE);
+  auto raw = [&](float* base, long i, int ln) { return reinterpret_cast<floatx4*>(base + i * slot) + wave * (CT * NT * WAVE) + ln; };
+  const float first_gate = keeper ? gate_of(begin) : 0.f;
+  load_all(begin);  // under way while the state is loaded
   const float* from = SUM ? nullptr : p.P > 1 ? p.segs + (bh * p.P + seg) * size : p.start ? p.start + bh * size : nullptr;
   const __amdgpu_buffer_rsrc_t start = buffer_rsrc(const_cast<float*>(from), from ? size * 4 : 0);  // else all 0
   if constexpr (SUM) {
@@ -344,6 +375,14 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[c][t] = floatx4{};
+  } else if (begin > 0) {
+    if (live) {
+      const floatx4* q = raw(p.wait, bh * p.P + seg, lane);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) S[c][t] = q[(c * NT + t) * WAVE];
+    }
   } else {
     each([&](int c, int t, int i) { S[c][t] = __builtin_bit_cast(floatx4, buffer_load16(start, i)); },
          [&](int c, int t, int j, int i) { S[c][t][j] = buffer_load4(start, i); });
@@ -352,22 +391,50 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   // what is never written again: blocks of A past the diagonal, slots of wavefronts without columns
   if constexpr (!SUM)
     for (int i = tid; i < C * C; i += TH) at[i] = (E)0.f;
-  for (int i = tid; i < K::PARTS * C; i += TH) part[i] = 0.f;
+  for (int i = tid; i < K::PARTS * C + (GATES ? NW : 0); i += TH) part[i] = 0.f;
 
-  if (keeper) tables(0, first_gate);
+  if (keeper) tables(begin, first_gate);
   put_all();
   float next = gate;  // gates of the chunk whose tables come next
-  if (count > 1) load_all(1);
+  if (begin + 1 < stop) load_all(begin + 1);
   barrier_lds();
 
-  for (int i = 0; i < count; ++i) {
+  for (int i = begin; i < stop; ++i) {
     const int n = chunk_at(i);
     const Table tab = table(i);
     // LDS addresses are formed again in every chunk, from a lane that the optimiser cannot see through: hoisted
     // out of the loop they take a hundred registers
     const int ln = hidden(lane);
     const int g4 = ln >> 4, m = ln & 15;
-    if (keeper && i + 1 < count) tables(i + 1, next);
+    if (keeper && i + 1 < stop) tables(i + 1, next);
+
+    // S before the chunk, or G behind it, left for the other order's walk or met by it; a chunk that lets nothing through
+    // needs neither
+    [[maybe_unused]] const bool meets = GATES && (FORM == PAIRS ? p.part == 2 : p.part != 1);
+    if constexpr (GATES) {
+      const bool open = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, *tab.whole)) != 0;
+      if (live && open) {
+        floatx4* q = raw(p.states, bh * p.NT + n, ln);
+        if (meets) {
+          floatx4 other[CT][NT], dot = {};
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) other[c][t] = q[(c * NT + t) * WAVE];
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) dot += S[c][t] * other[c][t];
+          const float all = sum_groups(sum_row((dot[0] + dot[1]) + (dot[2] + dot[3])));
+          if (ln == 0) dots[wave] = all;
+        } else {
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) q[(c * NT + t) * WAVE] = S[c][t];
+        }
+      }
+    }
 
     // A = inner Gamma (x y^T), block by block: rows j of the product are y's tokens, so a lane has four
     // consecutive j of one token i
@@ -398,7 +465,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
               const bool on = REV ? tj + r >= ti : tj + r <= ti;
               const float factor = p.inner * __builtin_amdgcn_exp2f(on ? (float)e : -INFINITY);
               v[r] = on ? d[r] * factor : 0.f;
-              if constexpr (FORM == PAIRS) d2[r] = tj + r == ti ? 0.f : v[r] * d2[r];
+              if constexpr (FORM == PAIRS) d2[r] = tj + r < ti ? v[r] * d2[r] : 0.f;
             }
           } else {  // through the end of the block before hi: two decays
             const float* back = tab.back + back_of(hi);
@@ -411,9 +478,22 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
             }
           }
           store4<E>(at + RA::at(ti, tj), v[0], v[1], v[2], v[3]);
+          // Pairs around a token t: of another block's two halves their row sums from t on, or column sums before t; of
+          // its own block the sum over j < t in each row, then over the rows from t on.
           if constexpr (FORM == PAIRS) {
-            const float row = sum_groups((d2[0] + d2[1]) + (d2[2] + d2[3]));
-            if (g4 == 0) part[(NW + jb) * C + ti] = row;
+            const float four = (d2[0] + d2[1]) + (d2[2] + d2[3]);
+            if (hi == lo) {
+              float before = sum_groups_below(four, ln);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float own = d2[r];
+                d2[r] = ti >= tj + r ? before : 0.f;
+                before += own;
+              }
+            } else {
+              const float row = sum_groups(four);
+              if (g4 == 0) part[(NW + jb) * C + ti] = row;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) d2[r] = sum_row(d2[r]);
             if (m == 0) *reinterpret_cast<floatx4*>(part + (NW + NB + ib) * C + tj) = d2;
@@ -503,10 +583,10 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
     }
     barrier_lds();  // A is whole; the tiles have been read
 
-    if (i + 1 < count) {
+    if (i + 1 < stop) {
       put_all();
       next = gate;
-      if (i + 2 < count) load_all(i + 2);
+      if (i + 2 < stop) load_all(i + 2);
     }
     if constexpr (!SUM) {
       if (live) {
@@ -547,13 +627,31 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
           float e = 0.f;
 #pragma unroll
           for (int k = 0; k < NW; ++k) e += part[k * C + lane];
-          if constexpr (FORM == PAIRS) {
-            float row = 0.f, down = 0.f;
-#pragma unroll
-            for (int k = 0; k < NB; ++k) row += part[(NW + k) * C + lane], down += part[(NW + NB + k) * C + lane];
-            e += row - down;
-          }
           p.tok[(bh * p.NT + n) * C + lane] = e;
+          if constexpr (FORM == PAIRS) {
+            const int own = lane >> 4;
+            float row = 0.f, col = 0.f, around = part[(NW + NB + own) * C + lane];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              row += part[(NW + k) * C + lane];  // none from blocks behind
+              const float down = part[(NW + NB + k) * C + lane];
+              col += k > own ? down : 0.f;
+              if (NB == 4 && k >= 2) {  // blocks 0 and 2, 0 and 3, 1 and 3 lie on either side of others
+                const int whole = __builtin_bit_cast(int, sum_row(down));
+                const float from0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(whole, 0));
+                const float from1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(whole, 16));
+                around += own == 1 ? from0 : own == 2 && k == 3 ? from0 + from1 : 0.f;
+              }
+            }
+            p.pair[(bh * p.NT + n) * C + lane] = around + sum_from(row) + sum_below(col);
+          }
+        }
+        if (meets && tid == 0) {
+          float dot = 0.f;
+#pragma unroll
+          for (int k = 0; k < NW; ++k) dot += dots[k];
+          const float whole = *tab.whole;
+          p.edge[bh * p.NT + n] = whole == 0.f ? 0.f : whole * dot;
         }
       }
     }
@@ -561,7 +659,15 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   }
 
   float* to = SUM ? p.segs + (bh * p.P + seg) * size : FORM == STATE ? p.end + bh * size : nullptr;
-  if (to) {
+  if (!SUM && p.part == 1) {
+    if (live) {
+      floatx4* q = raw(p.wait, bh * p.P + seg, lane);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) q[(c * NT + t) * WAVE] = S[c][t];
+    }
+  } else if (to) {
     const __amdgpu_buffer_rsrc_t end = buffer_rsrc(to, size * 4);
     each([&](int c, int t, int i) { buffer_store16(end, i, S[c][t]); },
          [&](int c, int t, int j, int i) { buffer_store4(end, i, S[c][t][j]); });
@@ -589,14 +695,14 @@ __global__ __launch_bounds__(4 * WAVE, (waves<E, KW, 4, CT>())) void summary_ker
 }
 
 // The three chains of a backward pass side by side: workgroups bound by products run next to ones bound by memory, and
-// there is one tail.  KQ, KV: the rows for q's and k's width, and for v's; LAST: dv's form, which may leave its state.
+// there is one tail.  dv's come first, which may walk twice as far (linear_abi.cpp).  KQ, KV: the rows for q's and k's width, and for v's; LAST: dv's form, which may leave its state.
 template <typename E, int KQ, int KV, bool GATES, int LAST>
 __global__ __launch_bounds__(4 * WAVE, sizeof(E) == 2 ? 2 : 1) void backward_kernel(LinChain dq, LinChain dv, LinChain dk, unsigned first,
                                                                                unsigned second) {
   constexpr int CQ = KQ == 128 ? 2 : 1, CV = KV == 128 ? 2 : 1;
-  if (blockIdx.x < first) walk<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>(dq, blockIdx.x);
-  else if (blockIdx.x < second) walk<E, KV, 4, CQ, true, GATES ? SUMS : PLAIN, false>(dk, blockIdx.x - first);
-  else walk<E, KQ, 4, CV, true, LAST, false>(dv, blockIdx.x - second);
+  if (blockIdx.x < first) walk<E, KQ, 4, CV, true, LAST, false>(dv, blockIdx.x);
+  else if (blockIdx.x < second) walk<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>(dq, blockIdx.x - first);
+  else walk<E, KV, 4, CQ, true, GATES ? SUMS : PLAIN, false>(dk, blockIdx.x - second);
 }
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
@@ -670,8 +776,8 @@ template <typename E, int KQ, int KV, bool GATES, int LAST>
 hipError_t run_backward(const LinChain& dq, const LinChain& dv, const LinChain& dk, hipStream_t st) {
   constexpr int CQ = KQ == 128 ? 2 : 1, CV = KV == 128 ? 2 : 1;
   constexpr int LDS = max_of(Config<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>::LDS, Config<E, KQ, 4, CV, true, LAST, false>::LDS);
-  const unsigned first = blocks(dq, 4 * CQ), second = first + blocks(dk, 4 * CQ);
-  hipLaunchKernelGGL((backward_kernel<E, KQ, KV, GATES, LAST>), dim3(second + blocks(dv, 4 * CV)), dim3(4 * WAVE), LDS, st, dq, dv,
+  const unsigned first = blocks(dv, 4 * CV), second = first + blocks(dq, 4 * CQ);
+  hipLaunchKernelGGL((backward_kernel<E, KQ, KV, GATES, LAST>), dim3(second + blocks(dk, 4 * CQ)), dim3(4 * WAVE), LDS, st, dq, dv,
                      dk, first, second);
   return hipGetLastError();
 }

@@ -47,7 +47,7 @@ def lin_workspace_bytes(B, L, Hk, H, dk, dv, dtype=BF16) -> int:
 
 @functools.lru_cache(maxsize=1024)
 def bwd_lin_workspace_bytes(B, L, Hk, H, dk, dv, dtype=BF16, gate=GATE_TOKEN) -> int:
-    """Workspace of bwd_lin for this shape (gate: 0 none, 1 [B, L, H], 2 [H])."""
+    """Workspace of bwd_lin for this shape (gate: 0 none, or no dg_log wanted, 1 [B, L, H], 2 [H])."""
     return _bytes_of(_load(), "delta_bwd_lin_workspace_bytes", _plan(B, L, Hk, H, dk, dv, dtype, 1.0)[0], Hk, gate)
 
 
@@ -122,7 +122,7 @@ def bwd_lin(q, k, v, g_log, S0, dO, dS_final=None, *, scale: float = 1.0, want_d
             g["dg_log"], pg = _out(g["dg_log"], "dg_log", g_log.shape, _f32, dev, g_log)
         if g["dS0"] is not None or want_dS0:
             g["dS0"], p00 = _out(g["dS0"], "dS0", sshp, _f32, dev, v)
-        ws, nws, keep = _workspace(workspace, bwd_lin_workspace_bytes(*dims, code, gate), dev)
+        ws, nws, keep = _workspace(workspace, bwd_lin_workspace_bytes(*dims, code, gate if pg else GATE_NONE), dev)
         rc = _load().delta_bwd_lin(ref, Hk, gate, *ptrs, p0, pd, ps, *outs, pg, p00, ws, nws, _raw(dev))
     _check(rc, "delta_bwd_lin")
     return g

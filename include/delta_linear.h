@@ -69,9 +69,12 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
  *   dv       [B, L, H, dv] dtype          written
  *   dg_log   as g_log, float32            written, or NULL; must be NULL for DELTA_LIN_GATE_NONE
  *   dS0      [B, H, dk, dv] float32       written, or NULL
- *   workspace   as above, delta_bwd_lin_workspace_bytes
- * At a hard reset dg = 0 and nothing flows back.  A fixed decay's gradient is the sum over all tokens
- * and sequences, held in 64 bits.  Outputs may not overlap the inputs, each other or the workspace.
+ *   workspace   as above, delta_bwd_lin_workspace_bytes.  With gates it holds a state for each chunk (64 tokens,
+ *               float32 32); a call without dg_log takes the size for DELTA_LIN_GATE_NONE
+ * At a hard reset dg = 0 and nothing flows back.  dg_t is formed from the states before and the gradients
+ * behind its chunk and the pairs of tokens around t, so its error goes by the magnitudes that cross
+ * t, whatever the sequence holds elsewhere.  A fixed decay's gradient is the sum of such terms over all
+ * tokens and sequences, added up in 64 bits.  Outputs may not overlap the inputs, each other or the workspace.
  */
 int delta_bwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, int32_t gate, size_t* bytes);
 int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const void* q, const void* k, const void* v,

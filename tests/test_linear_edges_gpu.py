@@ -159,3 +159,75 @@ def test_a_small_state_grows_past_a_segments_range(dtype):
     p = Problem(dtype, x[0], end, x[2], late, None, (r(6, B, L, H, d) * (t[..., None] < L - 220)).astype(np.float32),
                 np.float32(1e-30) * draw(7, (B, H, d, d)))
     p.check_bwd()
+
+
+# ---- gradients of the gates where tokens differ by orders of magnitude ------------------------------
+
+def crossing(x, dO, dS, scale):
+    """Per token, what the gate's gradient is a sum of, in magnitudes: a_t <|S_{t-1}|, |G_t|> of the recurrences on
+    magnitudes (every pair of a write before t and a read from t on, with its decays)."""
+    a = Lo._gates(x["g"], *dO.shape[:3])
+    S, (G, _) = Lo.states(x["k"], x["v"], x["g"], x["S0"]), Lo.flows(x["q"], dO, x["g"], dS, scale)
+    return np.stack([a[:, t] * (S[t] * G[t]).sum((2, 3)) for t in range(dO.shape[1])], 1)
+
+
+def check_gates(name, got, x, dO, dS, scale, c):
+    """dg_log elementwise: the two states of every product are each within c u of their magnitudes, as S_final and dS0
+    are, and the product's sums add 64 terms in a lane and 64 more over lanes, tokens and blocks at most: an error of
+    (2 c + 128) u times what crosses this very token.  1e-30 for what falls out of float32."""
+    ref = Lo.bwd(x["q"], x["k"], x["v"], x["g"], x["S0"], dO, dS, scale)["dg_log"]
+    mag = {n: a if a is None or n == "g" else np.abs(a) for n, a in x.items()}
+    tol = (2 * c + 128) * U * crossing(mag, np.abs(dO), None if dS is None else np.abs(dS), scale) + 1e-30
+    if ref.ndim == 1:  # the sum over tokens in 64 bits, rounded once
+        tol = tol.sum((0, 1)) + U * np.abs(ref)
+    check(name, got, ref, tol)
+
+
+def steps(kind, L):
+    """How much larger the tokens of v and dO are."""
+    s, t = np.ones(L, np.float32), np.arange(L)
+    if kind == "early":
+        s[t < 40] = 1e3
+    elif kind == "twice":
+        s[(t % 211 > 20) & (t % 211 < 33)] = 1e4
+    elif kind == "late":
+        s[t >= L - 40] = 1e3
+    return s[None, :, None, None]
+
+
+@pytest.mark.parametrize("B,L,Hk,H,dk,dv,dtype,kind,rate", [
+    (33, 300, 2, 2, 16, 32, "bf16", "early", 0.3), (33, 300, 2, 2, 32, 16, "f32", "early", 0.3), (33, 700, 1, 2, 16, 16, "f32", "twice", 0.1),
+    (33, 900, 2, 2, 128, 128, "bf16", "twice", 0.1), (33, 300, 2, 2, 128, 128, "f32", "late", 0.3), (70, 400, 1, 1, 64, 80, "bf16", "late", 0.02),
+    (1, 3000, 2, 2, 64, 64, "bf16", "early", 0.3), (1, 2000, 1, 2, 32, 96, "f32", "twice", 0.1), (40, 500, 1, 2, 32, 240, "bf16", "twice", 0.1),
+    (40, 300, 2, 2, 128, 144, "f32", "early", 0.3), (2, 130, 1, 1, 64, 48, "bf16", "twice", 1.0), (1, 64, 1, 1, 16, 16, "bf16", "late", 0.5),
+    (1, 33, 1, 1, 16, 16, "f32", "early", 0.5), (2, 1, 1, 1, 32, 16, "bf16", "even", 0.5), (3, 65, 1, 3, 128, 32, "bf16", "even", 0.05)])
+@pytest.mark.parametrize("gate", ["token", "head"])
+def test_gradients_of_gates_next_to_much_larger_tokens(B, L, Hk, H, dk, dv, dtype, kind, rate, gate):
+    """Each token's gradient is as good as what crosses that token, whatever the sequence holds elsewhere (the state
+    forgets it), with a launch of one segment and of several; the oracle on the first and last sequence."""
+    r = lambda seed, *shape, t=dtype: draw(seed, shape, t)
+    big = steps(kind, L)
+    to = lambda x: draw_as(x * big, dtype)
+    g = -np.random.default_rng(5).uniform(0.5, 1.5, (B, L, H) if gate == "token" else H).astype(np.float32) * np.float32(rate)
+    x = dict(q=r(1, B, L, Hk, dk), k=r(2, B, L, Hk, dk), v=to(r(3, B, L, H, dv)), g=g, S0=r(6, B, H, dk, dv, t="f32"))
+    dO, dS, scale = to(r(4, B, L, H, dv)), r(7, B, H, dk, dv, t="f32"), dk ** -0.5
+    dev = [to_dev(x[n], dtype if n in "qkv" else "f32") for n in ("q", "k", "v", "g", "S0")]
+    say("gates", B, L, Hk, H, dk, dv, dtype, kind, gate)
+    C = CHUNK[dtype]
+    c = dk + dv + 64 + -(-L // C) * (4 + 1.5 * rate * C) + 100
+    one = lambda b: {n: a if n == "g" and gate == "head" else a[b:b + 1] for n, a in x.items()}
+    if gate == "token":
+        G = D.bwd_lin(*dev, to_dev(dO, dtype), to_dev(dS, "f32"), scale=scale)
+        for b in {0, B - 1}:
+            check_gates("dg_log", G["dg_log"][b:b + 1], one(b), dO[b:b + 1], dS[b:b + 1], scale, c)
+        return
+    # a fixed decay's gradient takes all sequences: with nothing else than the first and the last one's dO and dS
+    dO[1:-1], dS[1:-1] = 0, 0
+    G = D.bwd_lin(*dev, to_dev(dO, dtype), to_dev(dS, "f32"), scale=scale)
+    pick = [0, B - 1] if B > 1 else [0]
+    two = {n: a if n == "g" else a[pick] for n, a in x.items()}
+    check_gates("dg_log", G["dg_log"], two, dO[pick], dS[pick], scale, c)
+
+
+def draw_as(x, dtype):
+    return torch.from_numpy(x).to(torch.bfloat16).float().numpy() if dtype == "bf16" else x.astype(np.float32)
