@@ -247,11 +247,14 @@ int delta_bwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
     if ((rc = hip_status(delta::launch_lin_backward(dqc, dvc, dkc, false, state, n.bf16, st)))) return rc;
   } else if (n.dv <= 128) {
     // S and G meet at every chunk: in a first launch dq walks a segment's first half from the front and dk the other from
-    // the back, each leaving its states, and in a second each meets the other's.  dv is in halves too where all three run
-    // at once; else whole, in the first launch, where it takes the time of two halves beside it (2 x 16 heads of 8K tokens:
-    // 24 chunks in a row, in halves 32).
+    // the back, each leaving its states, and in a second each meets the other's.  dv goes in halves beside them, or whole in
+    // the first launch, by which of the two takes fewer rounds of half walks on what the card holds at once: 256 workgroups
+    // of each chain in bf16 (2 x 16 heads of 8K tokens, 8 segments) three rounds, dv in halves four; 160 in float32 four, dv
+    // whole five.
     dqc.wait = w.wait_q, dkc.wait = w.wait_k, dvc.wait = w.wait_v;
-    const bool halves = 3LL * n.B * n.H * n.P <= (n.bf16 ? 512 : 256);
+    const long units = (long)n.B * n.H * n.P, card = n.bf16 ? 512 : 256;
+    auto rounds = [card](long halves) { return (halves + card - 1) / card; };
+    const bool halves = 2 * rounds(3 * units) < std::max(2L, rounds(4 * units)) + rounds(2 * units);
     for (int part = 1; part <= 2; ++part) {
       dqc.part = dkc.part = part, dvc.part = halves ? part : 0;
       if (part == 2 && !halves) dvc.run = 0;

@@ -235,8 +235,8 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   auto chunk_at = [&](int i) { return REV ? first + count - 1 - i : first + i; };
   // the chunks of this launch; either order's first half is the other's second
   const int cut = SUM || p.part == 0 ? count : REV ? count / 2 : (count + 1) / 2;
-  const int begin = !SUM && p.part == 2 ? cut : 0, stop = !SUM && p.part == 1 ? cut : count;
-  if (begin == stop) return;
+  const int first_step = !SUM && p.part == 2 ? cut : 0, stop = !SUM && p.part == 1 ? cut : count;
+  if (first_step == stop) return;
 
   // ---- tiles: registers for the next chunk's pieces
   struct Source {
@@ -317,29 +317,30 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   auto back_of = [](int hi) { return 8 * hi * (hi - 1); };  // where the decays to block hi begin
   double sum = 0.0;  // log gates of the chunks so far, -inf with a reset among them (keeper)
   auto tables = [&](int i, float gl) {
+    const int ln = hidden(lane);
     double a = lin_log_gate(gl);
 #pragma unroll
     for (int o = 1; o < C; o <<= 1) {
       const double up = __shfl_up(a, o, WAVE);
-      if (lane >= o) a += up;
+      if (ln >= o) a += up;
     }
     const double last = __shfl(a, C - 1, WAVE);
     sum += last < LIN_RESET / 2 ? -INFINITY : last;
     const Table t = table(i);
     const float begin = expf((float)a), end = expf((float)(last - a));
-    const double ref = __shfl(a, max(16 * (lane >> 4) - 1, 0), WAVE);
-    if (lane < C) {
-      t.gc[lane] = a * 1.4426950408889634074;
-      t.fx[lane] = (REV ? end : begin) * p.outer;
-      t.fy[lane] = (REV ? begin : end) * p.write;
-      t.in[lane] = expf((float)(lane < 16 ? a : a - ref));
+    const double ref = __shfl(a, max(16 * (ln >> 4) - 1, 0), WAVE);
+    if (ln < C) {
+      t.gc[ln] = a * 1.4426950408889634074;
+      t.fx[ln] = (REV ? end : begin) * p.outer;
+      t.fy[ln] = (REV ? begin : end) * p.write;
+      t.in[ln] = expf((float)(ln < 16 ? a : a - ref));
     }
 #pragma unroll
     for (int hi = 1; hi < NB; ++hi) {
       const float to = expf((float)(__shfl(a, 16 * hi - 1, WAVE) - a));
-      if (lane < 16 * hi) t.back[back_of(hi) + lane] = to;
+      if (ln < 16 * hi) t.back[back_of(hi) + ln] = to;
     }
-    if (lane == 0) *t.whole = expf((float)last);
+    if (ln == 0) *t.whole = expf((float)last);
   };
 
   // ---- the state: rows srow(t, 4 g + j) of column m of this wavefront's tiles
@@ -366,8 +367,8 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   // A state as the registers hold it: 16 x 16 tiles of a lane's four elements each.
   const int slot = (tiles + 1) / 2 * 2 * NT * (4 * WAVE);
   auto raw = [&](float* base, long i, int ln) { return reinterpret_cast<floatx4*>(base + i * slot) + wave * (CT * NT * WAVE) + ln; };
-  const float first_gate = keeper ? gate_of(begin) : 0.f;
-  load_all(begin);  // under way while the state is loaded
+  const float first_gate = keeper ? gate_of(first_step) : 0.f;
+  load_all(first_step);  // under way while the state is loaded
   const float* from = SUM ? nullptr : p.P > 1 ? p.segs + (bh * p.P + seg) * size : p.start ? p.start + bh * size : nullptr;
   const __amdgpu_buffer_rsrc_t start = buffer_rsrc(const_cast<float*>(from), from ? size * 4 : 0);  // else all 0
   if constexpr (SUM) {
@@ -375,7 +376,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[c][t] = floatx4{};
-  } else if (begin > 0) {
+  } else if (first_step > 0) {
     if (live) {
       const floatx4* q = raw(p.wait, bh * p.P + seg, lane);
 #pragma unroll
@@ -393,13 +394,13 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
     for (int i = tid; i < C * C; i += TH) at[i] = (E)0.f;
   for (int i = tid; i < K::PARTS * C + (GATES ? NW : 0); i += TH) part[i] = 0.f;
 
-  if (keeper) tables(begin, first_gate);
+  if (keeper) tables(first_step, first_gate);
   put_all();
   float next = gate;  // gates of the chunk whose tables come next
-  if (begin + 1 < stop) load_all(begin + 1);
+  if (first_step + 1 < stop) load_all(first_step + 1);
   barrier_lds();
 
-  for (int i = begin; i < stop; ++i) {
+  for (int i = first_step; i < stop; ++i) {
     const int n = chunk_at(i);
     const Table tab = table(i);
     // LDS addresses are formed again in every chunk, from a lane that the optimiser cannot see through: hoisted
@@ -416,22 +417,31 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
       if (live && open) {
         floatx4* q = raw(p.states, bh * p.NT + n, ln);
         if (meets) {
-          floatx4 other[CT][NT], dot = {};
+          // two groups on their way (16 heads of 2 x 8K tokens 452 us; all 64 registers of them spill, 472; half of them a
+          // phase ahead spill too, 554)
+          constexpr int GROUP = CT * NT < 4 ? CT * NT : 4, AHEAD = 2, GROUPS = CT * NT / GROUP;
+          floatx4 other[AHEAD][GROUP], dot = {};
+          auto fetch = [&](int k) {
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+            for (int e = 0; e < GROUP; ++e) other[k % AHEAD][e] = __builtin_nontemporal_load(q + (k * GROUP + e) * WAVE);
+          };
 #pragma unroll
-            for (int t = 0; t < NT; ++t) other[c][t] = q[(c * NT + t) * WAVE];
+          for (int k = 0; k < AHEAD && k < GROUPS; ++k) fetch(k);
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+          for (int k = 0; k < GROUPS; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) dot += S[c][t] * other[c][t];
+            for (int e = 0; e < GROUP; ++e) dot += S[(k * GROUP + e) / NT][(k * GROUP + e) % NT] * other[k % AHEAD][e];
+            if (k + AHEAD < GROUPS) fetch(k + AHEAD);
+          }
+          __builtin_amdgcn_sched_barrier(0);
           const float all = sum_groups(sum_row((dot[0] + dot[1]) + (dot[2] + dot[3])));
           if (ln == 0) dots[wave] = all;
         } else {
 #pragma unroll
           for (int c = 0; c < CT; ++c)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) q[(c * NT + t) * WAVE] = S[c][t];
+            for (int t = 0; t < NT; ++t) __builtin_nontemporal_store(S[c][t], q + (c * NT + t) * WAVE);
         }
       }
     }
@@ -623,18 +633,19 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
         }
       }
       if constexpr (GATES) {
-        if (wave == 0 && lane < C) {
+        const int tok = hidden(lane);
+        if (wave == 0 && tok < C) {
           float e = 0.f;
 #pragma unroll
-          for (int k = 0; k < NW; ++k) e += part[k * C + lane];
-          p.tok[(bh * p.NT + n) * C + lane] = e;
+          for (int k = 0; k < NW; ++k) e += part[k * C + tok];
+          p.tok[(bh * p.NT + n) * C + tok] = e;
           if constexpr (FORM == PAIRS) {
-            const int own = lane >> 4;
-            float row = 0.f, col = 0.f, around = part[(NW + NB + own) * C + lane];
+            const int own = tok >> 4;
+            float row = 0.f, col = 0.f, around = part[(NW + NB + own) * C + tok];
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-              row += part[(NW + k) * C + lane];  // none from blocks behind
-              const float down = part[(NW + NB + k) * C + lane];
+              row += part[(NW + k) * C + tok];  // none from blocks behind
+              const float down = part[(NW + NB + k) * C + tok];
               col += k > own ? down : 0.f;
               if (NB == 4 && k >= 2) {  // blocks 0 and 2, 0 and 3, 1 and 3 lie on either side of others
                 const int whole = __builtin_bit_cast(int, sum_row(down));
@@ -643,7 +654,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
                 around += own == 1 ? from0 : own == 2 && k == 3 ? from0 + from1 : 0.f;
               }
             }
-            p.pair[(bh * p.NT + n) * C + lane] = around + sum_from(row) + sum_below(col);
+            p.pair[(bh * p.NT + n) * C + tok] = around + sum_from(row) + sum_below(col);
           }
         }
         if (meets && tid == 0) {
