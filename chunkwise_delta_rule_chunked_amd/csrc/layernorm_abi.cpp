@@ -54,6 +54,8 @@ int delta_layer_dropout(int64_t rows, int32_t width, int32_t dtype, const delta_
   int rc = rows_shape(rows, width, dtype, 0.f);
   if (rc) return rc;
   if (!drop) return DELTA_ERR_NULL_ARG;
+  // one launch has fewer than 2^32 threads, four vectors of eight channels each
+  if (rows * ((width + 7LL) / 8) > (1LL << 34) - 1024) return DELTA_ERR_BAD_SHAPE;
   DropoutParams p;
   if ((rc = drop_rule(drop, p.rule))) return rc;
   if (rows == 0) return DELTA_OK;

@@ -40,7 +40,7 @@ typedef struct {
  *   x, residual [rows, width] dtype; residual may be NULL for none
  *   y           [rows, width] dtype, written; may equal x or residual exactly
  * The gradient of x is the same call on the gradient of y, without a residual.  No other
- * overlap.
+ * overlap.  rows * ceil(width / 8) <= 2^34 - 2^10 (a launch's threads).
  */
 int delta_layer_dropout(int64_t rows, int32_t width, int32_t dtype, const delta_dropout* drop, const void* x,
                         const void* residual, void* y, void* stream);
