@@ -79,7 +79,8 @@ struct LinDecode {
   void* O;
 };
 
-void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS);
+// Chunks, segments, chunks of a segment; and the most segments of any sequence of up to this length.
+void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS, int& most_segments);
 // bf16 inputs in one file, float32 in another
 hipError_t lin_chain_bf16(const LinChain& c, bool reverse, int form, hipStream_t st);
 hipError_t lin_chain_f32(const LinChain& c, bool reverse, int form, hipStream_t st);

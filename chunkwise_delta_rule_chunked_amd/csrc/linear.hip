@@ -227,22 +227,24 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 //     between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16 of 8K, 64 x 64, in 16 136 (8: 182)
 // Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 321 in one,
 // 372 in two; 8 x 8 of 777 111 in one, 116 in three; 12 x 16 of 1K forward 69 in one, 76 in two.
-void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS) {
+void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS, int& most_segments) {
   const int C = lin_chunk(bf16);
   NT = (L + C - 1) / C;
-  P = NT > 0, NS = NT;
+  P = most_segments = NT > 0, NS = NT;
   const long units = (long)B * H * (backward ? 1 : (dv + LIN_SLAB - 1) / LIN_SLAB);
   if (NT == 0 || units == 0) return;
-  const long card = backward ? 256 : 512, most = card / units;
+  const long card = backward ? 256 : 512, most = card / units;  // no rule below takes more segments than `most`
   const double ns = sqrt((double)units * NT / (backward ? 24 : 64));
   const int n = ns < 1.5 ? 1 : (int)(ns + 0.5);
   long p = (NT + n - 1L) / n;
   // a round of workgroups and few more
   const long round = backward ? 512 / 3 : 256, few = backward ? 208 : 384;
   if ((backward ? dv <= 128 : !bf16) && units * p > round && units * p <= few) p = round / units;
-  else if (4 * p >= 3 * most + backward) p = most;
+  else if (backward ? 4 * p > 3 * most : 4 * p >= 3 * most) p = most;
   if (p > NT) p = NT;
-  if (p < (backward ? 4 : 3)) return;
+  const long least = backward ? 4 : 3, up_to = most < NT ? most : NT;
+  if (up_to >= least) most_segments = (int)up_to;
+  if (p < least) return;
   NS = (int)((NT + p - 1) / p);  // as even as that many segments can be
   P = (NT + NS - 1) / NS;
 }

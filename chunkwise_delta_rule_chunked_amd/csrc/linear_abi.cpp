@@ -21,6 +21,7 @@ namespace {
 
 struct Lin {
   int B, L, H, Hk, dk, dv, gate, NT, P, NS;
+  int most;  // segments that a sequence of up to this length is cut into
   bool bf16;
   float scale;
   size_t nqk, nv, ng, state;  // bytes of q, of v, of the gates, of the states
@@ -37,7 +38,7 @@ int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, bool backwar
   if (heads > (1LL << 20) || heads * s->dk * s->dv > (1LL << 33)) return DELTA_ERR_BAD_SHAPE;
   n.B = s->B, n.L = s->L, n.H = s->H, n.Hk = qk_heads, n.dk = s->dk, n.dv = s->dv, n.gate = gate;
   n.bf16 = s->dtype == DELTA_BF16, n.scale = s->scale;
-  delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, backward, n.NT, n.P, n.NS);
+  delta::lin_split(n.B, n.L, n.H, n.dv, n.bf16, backward, n.NT, n.P, n.NS, n.most);
   const size_t tokens = (size_t)n.B * n.L, e = esize(s->dtype);
   n.nqk = n.H ? tokens * n.Hk * n.dk * e : 0, n.nv = tokens * n.H * n.dv * e;
   n.ng = 4 * (gate == DELTA_LIN_GATE_TOKEN ? tokens * n.H : gate == DELTA_LIN_GATE_HEAD ? (size_t)n.H : 0);
@@ -45,7 +46,9 @@ int lin_shape(const delta_shape* s, int32_t qk_heads, int32_t gate, bool backwar
   return DELTA_OK;
 }
 
-// Regions of a workspace, each on its own 256 bytes; with a null base only their total is formed.
+// Regions of a workspace, each on its own 256 bytes; with a null base only their total is formed.  A longer sequence may
+// have fewer segments than a shorter one; there is room for the most of any up to this length, so that a workspace
+// for the longest serves all.
 struct Carve {
   char* base;
   size_t used = 0;
@@ -63,9 +66,9 @@ struct FwdSpace {
 };
 size_t carve(const Lin& n, void* base, FwdSpace& w) {
   Carve c{static_cast<char*>(base)};
-  const bool split = n.P > 1;
-  w.segs = c.take<float>(split ? n.state * n.P : 0);
-  w.decay = c.take<double>(split ? (size_t)n.B * n.H * n.P * 8 : 0);
+  const size_t segments = n.most > 1 ? (size_t)n.B * n.H * n.most : 0;
+  w.segs = c.take<float>(segments * n.dk * n.dv * 4);
+  w.decay = c.take<double>(segments * 8);
   return c.used;
 }
 
@@ -76,22 +79,23 @@ struct BwdSpace {
 };
 size_t carve(const Lin& n, bool gates, void* base, BwdSpace& w) {
   Carve c{static_cast<char*>(base)};
-  const bool split = n.P > 1, halves = gates && n.dv <= 128;
+  const bool halves = gates && n.dv <= 128;
   const size_t heads = (size_t)n.B * n.H, chunks = heads * n.NT, tokens = chunks * delta::lin_chunk(n.bf16) * 4;
   const size_t qk_state = delta::lin_state_bytes(n.dv, n.dk), v_state = delta::lin_state_bytes(n.dk, n.dv);
-  w.segs = c.take<float>(split ? n.state * n.P : 0);
-  w.gsegs = c.take<float>(split ? n.state * n.P : 0);
-  w.decay = c.take<double>(split ? heads * n.P * 8 : 0);
-  w.gdecay = c.take<double>(split ? heads * n.P * 8 : 0);
+  const size_t segments = n.most > 1 ? heads * n.most : 0, parts = heads * n.most;
+  w.segs = c.take<float>(segments * n.dk * n.dv * 4);
+  w.gsegs = c.take<float>(segments * n.dk * n.dv * 4);
+  w.decay = c.take<double>(segments * 8);
+  w.gdecay = c.take<double>(segments * 8);
   w.part = c.take<double>(gates && n.gate == DELTA_LIN_GATE_HEAD ? heads * ((n.NT + delta::LIN_GATE_CHUNKS - 1) / delta::LIN_GATE_CHUNKS) * 8 : 0);
   w.e = c.take<float>(gates ? tokens : 0);
   w.f = c.take<float>(gates ? tokens : 0);
   w.pair = c.take<float>(gates ? tokens : 0);
   w.edge = c.take<float>(gates ? chunks * 4 : 0);
   w.states = c.take<float>(gates ? chunks * qk_state : 0);
-  w.wait_q = c.take<float>(halves ? heads * n.P * qk_state : 0);
-  w.wait_k = c.take<float>(halves ? heads * n.P * qk_state : 0);
-  w.wait_v = c.take<float>(halves ? heads * n.P * v_state : 0);
+  w.wait_q = c.take<float>(halves ? parts * qk_state : 0);
+  w.wait_k = c.take<float>(halves ? parts * qk_state : 0);
+  w.wait_v = c.take<float>(halves ? parts * v_state : 0);
   w.dq = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);  // parts of the heads that share
   w.dk = c.take<float>(n.H != n.Hk ? heads * n.L * n.dk * 4 : 0);
   return c.used;

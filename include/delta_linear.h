@@ -45,7 +45,8 @@ enum {
  *   O       [B, L, H, dv] dtype      written
  *   S_final [B, H, dk, dv] float32   written, or NULL; may equal S0 exactly (in place)
  *   workspace   at least delta_fwd_lin_workspace_bytes bytes, 16-byte aligned; contents on entry are
- *               ignored; may be NULL when that size is 0
+ *               ignored; may be NULL when that size is 0.  The size never falls with L: a workspace for the
+ *               longest sequence serves shorter ones of the same B, heads, widths and type
  * States are float32, as if from float32 products, in either type; O is rounded once, from products
  * of operands in the inputs' type summed in float32 (for bf16 the state and the pairs' weights are
  * rounded to bf16 as operands).  No other overlap of outputs with inputs or with each other; 16-byte aligned

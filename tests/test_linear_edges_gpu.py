@@ -231,3 +231,20 @@ def test_gradients_of_gates_next_to_much_larger_tokens(B, L, Hk, H, dk, dv, dtyp
 
 def draw_as(x, dtype):
     return torch.from_numpy(x).to(torch.bfloat16).float().numpy() if dtype == "bf16" else x.astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_workspace_for_sequences_up_to_the_longest(dtype):
+    B, Hk, H, dk, dv = 3, 2, 6, 64, 80
+    code = D.BF16 if dtype == "bf16" else D.F32
+    ws = torch.empty(max(D.lin_workspace_bytes(B, 1500, Hk, H, dk, dv, code), D.bwd_lin_workspace_bytes(B, 1500, Hk, H, dk, dv, code, 1)),
+                     dtype=torch.uint8, device="cuda")
+    for L in (1500, 223, 260, 40, 700, 1):
+        r = lambda seed, *s: to_dev(draw(seed, s, dtype), dtype)
+        q, k, v, dO = r(1, B, L, Hk, dk), r(2, B, L, Hk, dk), r(3, B, L, H, dv), r(4, B, L, H, dv)
+        g = to_dev(-np.abs(draw(5, (B, L, H))), "f32")
+        ws.fill_(255)
+        for a, b in zip(D.fwd_lin(q, k, v, g), D.fwd_lin(q, k, v, g, workspace=ws)):
+            assert torch.equal(a, b)
+        for a, b in zip(D.bwd_lin(q, k, v, g, None, dO).values(), D.bwd_lin(q, k, v, g, None, dO, workspace=ws).values()):
+            assert torch.equal(a, b)
