@@ -15,13 +15,22 @@ __device__ inline double wave_total(double x) {
   return x;
 }
 
-// s e^d for a segment's sum of log gates.  With gates above 1 e^d may be no float32 number although s e^d is (s is small, or
-// 0): then in three steps, each between s and the result.  Past e^240 every s is 0, infinite or 0 again.
-__device__ inline floatx4 decayed(floatx4 s, double d) {
-  if (!(fabs(d) > 80.0) || d == -INFINITY) return s * expf((float)d);
-  const float third = expf((float)(fmin(fmax(d, -240.0), 240.0) / 3));
-  return s * third * third * third;
-}
+// e^d for a segment's sum d of log gates, as a factor to multiply by once or three times.  With gates above 1 e^d may be no
+// float32 number although s e^d is (s is small, or 0): then in three steps, each between s and the result.  Past e^240
+// every s is 0, infinite or 0 again.
+struct Decay {
+  float factor;
+  bool thrice;
+  __device__ inline Decay() {}
+  __device__ inline Decay(double d) : thrice(fabs(d) > 80.0 && d != -INFINITY) {
+    factor = expf((float)(thrice ? fmin(fmax(d, -240.0), 240.0) / 3 : d));
+  }
+  __device__ inline floatx4 operator()(floatx4 s) const {
+    s *= factor;
+    if (thrice) s = s * factor * factor;
+    return s;
+  }
+};
 
 // One chain's states of one place, four elements a lane, from segment to segment: a segment's result becomes its start,
 // start_{p+1} = e^decay_p start_p + result_p.
@@ -37,14 +46,15 @@ __device__ inline void walk(const Walk& w, int P, long quads, long bh, long q) {
   constexpr int AHEAD = 8;          // results loaded at a time
   for (int p0 = 0; p0 < n; p0 += AHEAD) {
     floatx4 r[AHEAD];
+    Decay decay[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
-      if (p0 + k < n) r[k] = at[(p0 + k) * quads];
+      if (p0 + k < n) r[k] = at[(p0 + k) * quads], decay[k] = Decay(w.decay[bh * P + p0 + k]);
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
       if (p0 + k < n) {
         at[(p0 + k) * quads] = s;
-        s = decayed(s, w.decay[bh * P + p0 + k]) + r[k];
+        s = decay[k](s) + r[k];
       }
   }
   if (w.end) w.end[bh * quads + q] = s;

@@ -203,7 +203,8 @@ struct Config {
   static constexpr int EDGE = PART + PARTS * C * 4, LDS = EDGE + (for_gates(FORM) ? 4 * NW : 0);
 };
 
-template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM>
+// PARTED: a launch may have a part of the walk (p.part).
+template <typename E, int KW, int NW, int CT, bool REV, int FORM, bool SUM, bool PARTED>
 __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
   constexpr int C = K::C, NB = K::NB, VW = K::VW, NT = K::NT, NU = K::NU, VEC = K::VEC, TH = K::TH;
@@ -234,8 +235,9 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   const int first = (REV ? p.P - 1 - seg : seg) * p.NS, count = min(p.NS, p.NT - first);
   auto chunk_at = [&](int i) { return REV ? first + count - 1 - i : first + i; };
   // the chunks of this launch; either order's first half is the other's second
-  const int cut = SUM || p.part == 0 ? count : REV ? count / 2 : (count + 1) / 2;
-  const int first_step = !SUM && p.part == 2 ? cut : 0, stop = !SUM && p.part == 1 ? cut : count;
+  const int half = PARTED ? p.part : 0;
+  const int cut = half == 0 ? count : REV ? count / 2 : (count + 1) / 2;
+  const int first_step = half == 2 ? cut : 0, stop = half == 1 ? cut : count;
   if (first_step == stop) return;
 
   // ---- tiles: registers for the next chunk's pieces
@@ -317,7 +319,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   auto back_of = [](int hi) { return 8 * hi * (hi - 1); };  // where the decays to block hi begin
   double sum = 0.0;  // log gates of the chunks so far, -inf with a reset among them (keeper)
   auto tables = [&](int i, float gl) {
-    const int ln = hidden(lane);
+    const int ln = GATES ? hidden(lane) : lane;
     double a = lin_log_gate(gl);
 #pragma unroll
     for (int o = 1; o < C; o <<= 1) {
@@ -411,7 +413,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
 
     // S before the chunk, or G behind it, left for the other order's walk or met by it; a chunk that lets nothing through
     // needs neither
-    [[maybe_unused]] const bool meets = GATES && (FORM == PAIRS ? p.part == 2 : p.part != 1);
+    [[maybe_unused]] const bool meets = GATES && (FORM == PAIRS ? half == 2 : half != 1);
     if constexpr (GATES) {
       const bool open = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, *tab.whole)) != 0;
       if (live && open) {
@@ -670,7 +672,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   }
 
   float* to = SUM ? p.segs + (bh * p.P + seg) * size : FORM == STATE ? p.end + bh * size : nullptr;
-  if (!SUM && p.part == 1) {
+  if (half == 1) {
     if (live) {
       floatx4* q = raw(p.wait, bh * p.P + seg, lane);
 #pragma unroll
@@ -695,14 +697,14 @@ constexpr int waves() {
 
 template <typename E, int KW, int NW, int CT, bool REV, int FORM>
 __global__ __launch_bounds__(NW * WAVE, (waves<E, KW, NW, CT>())) void chain_kernel(LinChain p) {
-  walk<E, KW, NW, CT, REV, FORM, false>(p, blockIdx.x);
+  walk<E, KW, NW, CT, REV, FORM, false, false>(p, blockIdx.x);
 }
 
 // The summaries of one chain, or of a chain and one in the other order behind it.
 template <typename E, int KW, int CT>
 __global__ __launch_bounds__(4 * WAVE, (waves<E, KW, 4, CT>())) void summary_kernel(LinChain forward, LinChain reverse, unsigned split) {
-  if (blockIdx.x < split) walk<E, KW, 4, CT, false, PLAIN, true>(forward, blockIdx.x);
-  else walk<E, KW, 4, CT, true, PLAIN, true>(reverse, blockIdx.x - split);
+  if (blockIdx.x < split) walk<E, KW, 4, CT, false, PLAIN, true, false>(forward, blockIdx.x);
+  else walk<E, KW, 4, CT, true, PLAIN, true, false>(reverse, blockIdx.x - split);
 }
 
 // The three chains of a backward pass side by side: workgroups bound by products run next to ones bound by memory, and
@@ -711,9 +713,9 @@ template <typename E, int KQ, int KV, bool GATES, int LAST>
 __global__ __launch_bounds__(4 * WAVE, sizeof(E) == 2 ? 2 : 1) void backward_kernel(LinChain dq, LinChain dv, LinChain dk, unsigned first,
                                                                                unsigned second) {
   constexpr int CQ = KQ == 128 ? 2 : 1, CV = KV == 128 ? 2 : 1;
-  if (blockIdx.x < first) walk<E, KQ, 4, CV, true, LAST, false>(dv, blockIdx.x);
-  else if (blockIdx.x < second) walk<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false>(dq, blockIdx.x - first);
-  else walk<E, KV, 4, CQ, true, GATES ? SUMS : PLAIN, false>(dk, blockIdx.x - second);
+  if (blockIdx.x < first) walk<E, KQ, 4, CV, true, LAST, false, GATES>(dv, blockIdx.x);
+  else if (blockIdx.x < second) walk<E, KV, 4, CQ, false, GATES ? PAIRS : PLAIN, false, GATES>(dq, blockIdx.x - first);
+  else walk<E, KV, 4, CQ, true, GATES ? SUMS : PLAIN, false, GATES>(dk, blockIdx.x - second);
 }
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
