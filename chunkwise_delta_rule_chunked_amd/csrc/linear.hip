@@ -227,16 +227,19 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 // chunk of a segment; and it moves four states (backward: twelve, three chains being side by side) for each segment of
 // each sequence and head.  The sum of the two is least where NS goes with the square root of (heads x chunks); the
 // factors are measured.  Then the launch should fill the card: forward 512 workgroups, backward 256 of each chain, no
-// more (a second round) and not much less.  Measured, us, 128 x 128 states, here and (segments: us) otherwise:
-//   backward bf16  2 x 16 heads of 8K tokens in 8 segments 367 (6: 405, 9: 412, 10: 384, 16: 383); 4 x 16 of 2K in 4 193 (3:
-//     214, 5: 220); 2 of 30000 in 79 164 (59: 161, 118: 196); 4 of 2K in 16 61 (8: 72, 32: 68)
-//     (a number a little over a whole round of the three, 512, is worse than that round: 2 x 16 of 4K in 5 200, in 6 214)
-//   backward float32  16 heads of 16K in 16 1067 (18: 1336, 23: 1279); 2 of 30000 in 79 355, in 86 418
+// more (a second round) and not much less.  Measured, us, 128 x 128 states, here and (segments: us) otherwise; backward
+// with the gates' gradients:
+//   backward bf16  2 x 16 heads of 8K tokens in 8 segments 454 (6: 503, 9: 513, 10: 488, 16: 482); 4 x 16 of 2K in 4 251 (3:
+//     262, 5: 293); 2 of 30000 in 79 184 (59: 179, 118: 215); 4 of 2K in 16 69 (8: 81, 32: 81)
+//   backward float32  16 heads of 16K in 16 1191 (18: 1484, 23: 1347); 2 of 30000 in 79 405, in 86 439
 //   forward bf16  4 x 16 of 2K in 8 77 (6: 85, 11: 104); 2 x 16 of 8K in 16 123 (8: 155); 64K of 16 heads in 32 417 (64: 528)
-//   forward float32, whose workgroups are alone on a compute unit with such states and which therefore takes no number
-//     between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16 of 8K, 64 x 64, in 16 136 (8: 182)
-// Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 321 in one,
-// 372 in two; 8 x 8 of 777 111 in one, 116 in three; 12 x 16 of 1K forward 69 in one, 76 in two.
+// A number of backward workgroups a little over a third of 512, which is one round of the three chains on the card, is
+// lowered to it: 16 heads of 4608 tokens would take 11 segments, 178 us (without gates' gradients 122), and take 10, 173
+// (102).  Only for the chains that run side by side.  Float32 forward, whose workgroups are alone on a compute unit with
+// such states, likewise takes no number between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16
+// of 8K, 64 x 64, in 16 136 (8: 182).
+// Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 366 in one,
+// 457 in two; 8 x 8 of 777 134 in one, 141 in three; 12 x 16 of 1K forward 69 in one, 76 in two.
 void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS, int& most_segments) {
   const int C = lin_chunk(bf16);
   NT = (L + C - 1) / C;
@@ -247,7 +250,6 @@ void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, i
   const double ns = sqrt((double)units * NT / (backward ? 24 : 64));
   const int n = ns < 1.5 ? 1 : (int)(ns + 0.5);
   long p = (NT + n - 1L) / n;
-  // a round of workgroups and few more
   const long round = backward ? 512 / 3 : 256, few = backward ? 208 : 384;
   if ((backward ? dv <= 128 : !bf16) && units * p > round && units * p <= few) p = round / units;
   else if (backward ? 4 * p > 3 * most : 4 * p >= 3 * most) p = most;

@@ -23,8 +23,10 @@
 //
 // Measured, 16 heads of 128 x 128 states in bf16.  Forward over 64K tokens: summaries 152 us (3.7 TB/s, matrix unit 29 %,
 // vector instructions 47 %), chain 247 us (4.6 TB/s, 15 %, 34 %); the loop alone goes at 5.4 TB/s, the rest is the states'
-// loads and the tail.  The three chains of a backward pass over 2 x 8K: 260 to 280 us (3.9 TB/s, 22 %, 40 %).  The state's
-// registers allow two wavefronts a SIMD, and nothing is saturated: what is left is waiting between a chunk's two barriers.
+// loads and the tail.  The three chains of a backward pass over 2 x 8K with the gates' gradients: 219 and 131 us in two
+// launches (4.3 and 4.6 TB/s, matrix unit 15 and 18 %, vector instructions 29 and 33 %), of which the states that meet are
+// a third of the bytes.  The state's registers allow two wavefronts a SIMD, and nothing is saturated: what is left is
+// waiting between a chunk's two barriers.
 // Four wavefronts of two column tiles against eight of one: chain 246 and 269 us.  Tiles of the next chunk go through
 // registers; straight to a second LDS stage the summaries gain 3 us and the other forms have no LDS for it.
 #pragma once

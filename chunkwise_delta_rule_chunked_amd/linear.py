@@ -100,7 +100,9 @@ def bwd_lin(q, k, v, g_log, S0, dO, dS_final=None, *, scale: float = 1.0, want_d
     """Backward pass of fwd_lin for the same arguments (delta_bwd_lin); dO has v's shape and type, dS_final
     [B,H,dk,dv] fp32 may be None for zero.  Returns a dict: dq, dk, dv in the inputs' type (dq and dk summed over
     the heads that share them), dg_log fp32 like g_log (None without gates or unless want_dg_log), dS0 fp32 (None
-    unless want_dS0).  `grads` may hold preallocated outputs under the same names."""
+    unless want_dS0).  With dg_log the workspace holds a state for each chunk, and bf16 dq and dk are formed from
+    states that are as good as float32 (else rounded to bf16): their last bits differ.  `grads` may hold preallocated
+    outputs under the same names."""
     dims, code, (ref, _), gate, ptrs = _inputs(q, k, v, g_log, scale)
     B, L, Hk, H, dk, dv = dims
     dev, sshp = q.device, (B, H, dk, dv)

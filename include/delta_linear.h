@@ -16,9 +16,9 @@
  * and k, which divides H: value head h reads query and key head h / (H / qk_heads).
  *
  * Gates: log decays in float32, one of DELTA_LIN_GATE_*.  g <= 0 is expected; a positive value is
- * computed as given, as long as the products of the gates within a chunk of 64 tokens stay in
- * float32's range.  g = -inf, or any g whose exp is 0 in float32, is the hard reset: the state before
- * it is multiplied by an exact 0.  Non-finite q, k or v propagate as in delta_fwd: such a value in one
+ * computed as given, as long as the products of the gates within a chunk of 64 tokens (up to the next
+ * reset) and the states themselves stay in float32's range.  g = -inf, or any g whose exp is 0 in float32
+ * (below -103.972), is the hard reset: the state before it is multiplied by an exact 0, whatever gates follow.  Non-finite q, k or v propagate as in delta_fwd: such a value in one
  * chunk reaches that chunk's outputs and every later state and output of its sequence and head, and
  * nothing before the chunk nor any other sequence or head that does not read it.
  */
@@ -49,7 +49,8 @@ enum {
  *               longest sequence serves shorter ones of the same B, heads, widths and type
  * States are float32, as if from float32 products, in either type; O is rounded once, from products
  * of operands in the inputs' type summed in float32 (for bf16 the state and the pairs' weights are
- * rounded to bf16 as operands).  No other overlap of outputs with inputs or with each other; 16-byte aligned
+ * rounded to bf16 as operands, and so are a token's weighted values where they enter a state that only
+ * outputs read).  No other overlap of outputs with inputs or with each other; 16-byte aligned
  * pointers (g_log: 4).  L = 0 writes S_final = S0 (or zeros).
  */
 int delta_fwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, size_t* bytes);
@@ -64,6 +65,8 @@ int delta_fwd_lin(const delta_shape* s, int32_t qk_heads, int32_t gate, const vo
  *     G_t = scale q_t dO_t^T + a_{t+1} G_{t+1},   dq_t = scale S_t dO_t,   dk_t = G_t v_t,
  *     dv_t = G_t^T k_t,   dg_t = a_t <G_t, S_{t-1}>,   dS0 = a_1 G_1
  *
+ * Precision as the forward pass's.  For bf16 with dg_log, dq and dk take the state's operands as three bf16 terms
+ * (as good as float32), without it as one: dq's and dk's last bits depend on whether dg_log is asked for.
  *   dO       [B, L, H, dv] dtype
  *   dS_final [B, H, dk, dv] float32   or NULL for zero
  *   dq, dk   [B, L, qk_heads, dk] dtype   written: the sums over the heads that share them, rounded once
