@@ -183,10 +183,12 @@ struct Int {
 // j < t <= i.  And these two, which walk in opposite orders over states in the same registers, form the inner product of S
 // and G at every chunk: the one that comes to it first leaves its state as the registers hold it, the other multiplies.
 // STATE: the state behind the last token.  A state that is an output, or that the gates' gradients are formed from,
-// takes in float32 weights whole (three bf16 terms); one that only out reads, whose products round it to bf16, one term.
-// out in bf16 is then off by 2.4e-3 in the 2-norm, where its own rounding is 1.7e-3.  Two terms for both (64K forward 417 to
-// 440 us, 16 x 16 heads of 1K backward without gates 211 to 250) give 2.25e-3; the rest is A, for a second term of which
-// the chains with gates have no LDS at two workgroups to a compute unit.
+// takes in float32 weights whole (three bf16 terms).  One that only out reads takes in two, good to 2^-16, and is rounded to
+// bf16 as the operand of out's product, as A is for the chunk's own share: out carries one operand's rounding and its own,
+// 2.4e-3 in the 2-norm where its own is 1.7e-3.  (One term into the state makes it 2.7e-3 where decays are slow, and takes 417
+// us for 424 of the 64K forward, 295 for 307 of 2 x 16 heads of 8K backward without gates.  Two terms as the operand too: 440
+// and 326, for 2.25e-3; the rest is A, for a second term of which the chains with gates have no LDS at two workgroups to a
+// compute unit.)
 constexpr int PLAIN = LIN_PLAIN, PAIRS = LIN_PAIRS, SUMS = LIN_SUMS, STATE = LIN_STATE;
 constexpr bool for_gates(int form) { return form == PAIRS || form == SUMS; }
 
@@ -214,7 +216,7 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
   typedef Config<E, KW, NW, CT, REV, FORM, SUM> K;
   constexpr int C = K::C, NB = K::NB, VW = K::VW, NT = K::NT, NU = K::NU, VEC = K::VEC, TH = K::TH;
   constexpr bool GATES = for_gates(FORM);
-  constexpr int INT = terms<E>(GATES ? 3 : 1), UPD = terms<E>(SUM || FORM != PLAIN ? 3 : 1);
+  constexpr int INT = terms<E>(GATES ? 3 : 1), UPD = terms<E>(SUM || FORM != PLAIN ? 3 : 2);
   typedef Rows<E, KW> RX;
   typedef Rows<E, VW> RZ;
   typedef Rows<E, C> RA;

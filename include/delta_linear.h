@@ -49,8 +49,7 @@ enum {
  *               longest sequence serves shorter ones of the same B, heads, widths and type
  * States are float32, as if from float32 products, in either type; O is rounded once, from products
  * of operands in the inputs' type summed in float32 (for bf16 the state and the pairs' weights are
- * rounded to bf16 as operands, and so are a token's weighted values where they enter a state that only
- * outputs read).  No other overlap of outputs with inputs or with each other; 16-byte aligned
+ * rounded to bf16 as operands).  No other overlap of outputs with inputs or with each other; 16-byte aligned
  * pointers (g_log: 4).  L = 0 writes S_final = S0 (or zeros).
  */
 int delta_fwd_lin_workspace_bytes(const delta_shape* s, int32_t qk_heads, size_t* bytes);

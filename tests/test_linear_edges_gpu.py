@@ -248,3 +248,35 @@ def test_one_workspace_for_sequences_up_to_the_longest(dtype):
             assert torch.equal(a, b)
         for a, b in zip(D.bwd_lin(q, k, v, g, None, dO).values(), D.bwd_lin(q, k, v, g, None, dO, workspace=ws).values()):
             assert torch.equal(a, b)
+
+
+# ---- bf16 outputs: their own rounding and one operand's --------------------------------------------
+
+@pytest.mark.parametrize("gate", ["none", "head", "token"])
+@pytest.mark.parametrize("B,L,Hk,H,dk,dv", [(4, 171, 8, 16, 32, 48), (2, 1500, 2, 2, 32, 64), (1, 1200, 1, 1, 128, 160), (40, 300, 2, 2, 64, 64),
+                                            (1, 1000, 2, 2, 128, 128)])
+def test_bf16_outputs_carry_one_operands_rounding(gate, B, L, Hk, H, dk, dv):
+    """Each output is a sum of products one operand of which is rounded to bf16 (the state, or a pair's weight), and is
+    rounded itself.  With rho the 2-norm of the outputs' own rounding and operands whose roundings are as large and
+    independent, that is sqrt(2) rho; a second operand's would make it sqrt(3).  Bound 1.5.  The oracle on the first and
+    last sequence."""
+    r = lambda seed, *shape, t="bf16": draw(seed, shape, t)
+    g = None if gate == "none" else -np.random.default_rng(5).uniform(0.0, 0.01, (B, L, H) if gate == "token" else H).astype(np.float32)
+    x = dict(q=r(1, B, L, Hk, dk), k=r(2, B, L, Hk, dk), v=r(3, B, L, H, dv), g=g, S0=r(6, B, H, dk, dv, t="f32"))
+    dO, dS, scale = r(4, B, L, H, dv), r(7, B, H, dk, dv, t="f32"), dk ** -0.5
+    dev = [to_dev(x[n], "bf16" if n in "qkv" else "f32") for n in ("q", "k", "v", "g", "S0")]
+    say("roundings", gate, B, L, Hk, H, dk, dv)
+    got = {"O": D.fwd_lin(*dev, scale=scale)[0]}
+    for want in (True, False):
+        G = D.bwd_lin(*dev, to_dev(dO, "bf16"), to_dev(dS, "f32"), scale=scale, want_dg_log=want)
+        got.update({"%s%d" % (n, want): G[n] for n in ("dq", "dk", "dv")})
+    pick = sorted({0, B - 1})
+    one = {n: a if a is None or a.ndim == 1 else a[pick] for n, a in x.items()}
+    ref = Lo.bwd(*one.values(), dO[pick], dS[pick], scale)
+    ref["O"] = Lo.fwd(**one, scale=scale)[0]
+    for n, t in got.items():
+        want = ref[n.rstrip("01")]
+        own = torch.from_numpy(want).to(torch.bfloat16).double().numpy() - want
+        ratio = np.linalg.norm(host(t[pick]) - want) / np.linalg.norm(own)
+        say("  %s: %.3f of its own rounding" % (n, ratio))
+        assert ratio <= 1.5, (n, ratio)
