@@ -229,17 +229,17 @@ hipError_t decode_by_dk(const LinDecode& p, hipStream_t st) {
 // factors are measured.  Then the launch should fill the card: forward 512 workgroups, backward 256 of each chain, no
 // more (a second round) and not much less.  Measured, us, 128 x 128 states, here and (segments: us) otherwise; backward
 // with the gates' gradients:
-//   backward bf16  2 x 16 heads of 8K tokens in 8 segments 454 (6: 503, 9: 513, 10: 488, 16: 482); 4 x 16 of 2K in 4 251 (3:
-//     262, 5: 293); 2 of 30000 in 79 184 (59: 179, 118: 215); 4 of 2K in 16 69 (8: 81, 32: 81)
-//   backward float32  16 heads of 16K in 16 1191 (18: 1484, 23: 1347); 2 of 30000 in 79 405, in 86 439
-//   forward bf16  4 x 16 of 2K in 8 77 (6: 85, 11: 104); 2 x 16 of 8K in 16 123 (8: 155); 64K of 16 heads in 32 417 (64: 528)
+//   backward bf16  2 x 16 heads of 8K tokens in 8 segments 461 (6: 500, 9: 516, 10: 491, 16: 489); 4 x 16 of 2K in 4 253 (3:
+//     263, 5: 292); 2 of 30000 in 79 184 (59: 178, 118: 215); 4 of 2K in 16 69 (8: 82, 32: 82)
+//   backward float32  16 heads of 16K in 16 1194 (18: 1480, 23: 1348); 2 of 30000 in 85 401, in 86 436
+//   forward bf16  4 x 16 of 2K in 8 82 (6: 91, 11: 109); 2 x 16 of 8K in 16 128 (8: 161); 64K of 16 heads in 32 424 (64: 534)
 // A number of backward workgroups a little over a third of 512, which is one round of the three chains on the card, is
 // lowered to it: 16 heads of 4608 tokens would take 11 segments, 178 us (without gates' gradients 122), and take 10, 173
 // (102).  Only for the chains that run side by side.  Float32 forward, whose workgroups are alone on a compute unit with
-// such states, likewise takes no number between one and one and a half times 256: 2 of 30000 in 128 144 (188: 178); 2 x 16
-// of 8K, 64 x 64, in 16 136 (8: 182).
-// Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 366 in one,
-// 457 in two; 8 x 8 of 777 134 in one, 141 in three; 12 x 16 of 1K forward 69 in one, 76 in two.
+// such states, likewise takes no number between one and one and a half times 256: 2 of 30000 in 128 151 (188: 190); 2 x 16
+// of 8K, 64 x 64, in 16 145 (8: 182).
+// Two segments (backward: three) are hardly ever worth the summaries' reads and launch: 8 x 16 of 2K backward 365 in one,
+// 465 in two; 8 x 8 of 777 134 in one, 142 in three; 12 x 16 of 1K forward 102 in one, 118 in two.
 void lin_split(int B, int L, int H, int dv, bool bf16, bool backward, int& NT, int& P, int& NS, int& most_segments) {
   const int C = lin_chunk(bf16);
   NT = (L + C - 1) / C;

@@ -21,10 +21,10 @@
 // product, in the order in which a 16-byte piece of an x row lies in LDS.  out is formed transposed, and a
 // wavefront's tiles interleave their columns, so a lane ends with 4 CT consecutive columns of a token.
 //
-// Measured, 16 heads of 128 x 128 states in bf16.  Forward over 64K tokens: summaries 152 us (3.7 TB/s, matrix unit 29 %,
-// vector instructions 47 %), chain 247 us (4.6 TB/s, 15 %, 34 %); the loop alone goes at 5.4 TB/s, the rest is the states'
-// loads and the tail.  The three chains of a backward pass over 2 x 8K with the gates' gradients: 219 and 131 us in two
-// launches (4.3 and 4.6 TB/s, matrix unit 15 and 18 %, vector instructions 29 and 33 %), of which the states that meet are
+// Measured, 16 heads of 128 x 128 states in bf16.  Forward over 64K tokens: summaries 152 us (3.8 TB/s, matrix unit 28 %,
+// vector instructions 47 %), chain 256 us (4.5 TB/s, 21 %, 40 %); the rest to the rate of a copy is the states' loads and
+// the tail.  The three chains of a backward pass over 2 x 8K with the gates' gradients: 221 and 135 us in two
+// launches (4.3 and 4.5 TB/s, matrix unit 16 and 18 %, vector instructions 30 and 33 %), of which the states that meet are
 // a third of the bytes.  The state's registers allow two wavefronts a SIMD, and nothing is saturated: what is left is
 // waiting between a chunk's two barriers.
 // Four wavefronts of two column tiles against eight of one: chain 246 and 269 us.  Tiles of the next chunk go through
@@ -426,8 +426,8 @@ __device__ __forceinline__ void walk(const LinChain& p, unsigned block) {
       if (live && open) {
         floatx4* q = raw(p.states, bh * p.NT + n, ln);
         if (meets) {
-          // two groups on their way (16 heads of 2 x 8K tokens 452 us; all 64 registers of them spill, 472; half of them a
-          // phase ahead spill too, 554)
+          // two groups on their way (when measured, 16 heads of 2 x 8K tokens 452 us; all 64 registers of them spill, 472; half
+          // of them a phase ahead spill too, 554)
           constexpr int GROUP = CT * NT < 4 ? CT * NT : 4, AHEAD = 2, GROUPS = CT * NT / GROUP;
           floatx4 other[AHEAD][GROUP], dot = {};
           auto fetch = [&](int k) {
