@@ -12,8 +12,7 @@
 // mirrored order, and forms that also leave what the gates' gradients need while its operands are at hand.
 // Every exponent goes from a later token back to an earlier one, so decays are at most 1 for log gates up to 0; for
 // gates above 1 the products within a chunk have to be float32 numbers.  The sums of log gates are held in 64
-// bits, because their differences are what is used.  What spans a hard reset is an exact
-// 0 (lin_log_gate).
+// bits, because their differences are what is used.  What spans a hard reset is an exact 0 (lin_log_gate).
 //
 // A workgroup has a segment of the sequence for one head and some columns of the state: each wavefront has
 // CT tiles of 16 columns and all rows, in MFMA accumulators for the whole segment.  The two row tiles 2u,
@@ -715,7 +714,8 @@ __global__ __launch_bounds__(4 * WAVE, (waves<E, KW, 4, CT>())) void summary_ker
 }
 
 // The three chains of a backward pass side by side: workgroups bound by products run next to ones bound by memory, and
-// there is one tail.  dv's come first, which may walk twice as far (linear_abi.cpp).  KQ, KV: the rows for q's and k's width, and for v's; LAST: dv's form, which may leave its state.
+// there is one tail.  dv's come first, which may walk twice as far (linear_abi.cpp).  KQ, KV: the rows for q's and k's width,
+// and for v's; LAST: dv's form, which may leave its state.
 template <typename E, int KQ, int KV, bool GATES, int LAST>
 __global__ __launch_bounds__(4 * WAVE, sizeof(E) == 2 ? 2 : 1) void backward_kernel(LinChain dq, LinChain dv, LinChain dk, unsigned first,
                                                                                unsigned second) {
